@@ -240,6 +240,44 @@ dap_status kv_append_paged_fp8(const void *k_new, const void *v_new, uint8_t *k_
                                const int32_t *positions, int B, int Hkv, int D, void *stream);
 
 /*
+ * Append runs of tokens (prompts, prompt chunks, drafted tokens) to the fp8 GQA cache, each row
+ * quantised as kv_append_paged_fp8 does.  The rows of all sequences are packed back to back: row r
+ * belongs to the sequence b with indptr[b] <= r < indptr[b + 1] and is written at logical position
+ * positions[b] + r - indptr[b].
+ *   k_new, v_new  device bf16 [total_tokens, Hkv, D], element strides (stride_t, stride_h, 1) each:
+ *                 slices of one projection's output need no copy.
+ *   indptr        device int32 [B + 1], non-decreasing (the qo_indptr of a multi-token decode's work map
+ *                 serves).  Rows outside every run (before indptr[0], at or past indptr[B]) are skipped:
+ *                 a captured call may be sized for more tokens than it gets.
+ *   positions     device int32 [B]: the position of each run's first row.
+ *   Supported: D in {64, 128, 256}, any page_size >= 1; rows and codes 16-byte aligned, strides multiples
+ *   of 8 elements, nonzero where the extent they step over is above 1.  A position outside
+ *   [0, max_pages * page_size) or a page outside the pool skips that row and sets DAP_DEVERR_SEQLEN /
+ *   DAP_DEVERR_PAGE.  No two rows may go to the same slot of a page.
+ */
+dap_status kv_append_paged_fp8_multi(const void *k_new, const void *v_new, long long k_stride_t,
+                                     long long k_stride_h, long long v_stride_t, long long v_stride_h,
+                                     uint8_t *k_codes, uint8_t *v_codes, void *k_scale, void *v_scale,
+                                     int num_pages, int page_size, const int32_t *block_table,
+                                     int max_pages, const int32_t *indptr, const int32_t *positions,
+                                     int total_tokens, int B, int Hkv, int D, void *stream);
+
+/*
+ * Read runs of the fp8 GQA cache back as bf16 rows: row r of k_out / v_out [total_tokens, Hkv, D]
+ * (element strides (stride_t, stride_h, 1)) is bf16(e4m3(code) * factor) of the position that
+ * kv_append_paged_fp8_multi would write row r at (same indptr, positions, block table; rows outside every
+ * run are left as they were).  A position outside [0, max_pages * page_size) or a page outside the pool
+ * gives a zero row and sets DAP_DEVERR_SEQLEN / DAP_DEVERR_PAGE.  Supported sizes, alignment and strides
+ * as kv_append_paged_fp8_multi.
+ */
+dap_status kv_read_paged_fp8(const uint8_t *k_codes, const uint8_t *v_codes, const void *k_scale,
+                             const void *v_scale, int num_pages, int page_size,
+                             const int32_t *block_table, int max_pages, const int32_t *indptr,
+                             const int32_t *positions, int total_tokens, int B, int Hkv, int D,
+                             void *k_out, void *v_out, long long k_stride_t, long long k_stride_h,
+                             long long v_stride_t, long long v_stride_h, void *stream);
+
+/*
  * Multi-token decode: several new tokens per sequence (speculative-decoding verification,
  * chunked short prefill) attending the paged cache causally [A: "Q Scheduling and KV
  * Addressing", the packed-q work map].

@@ -32,7 +32,7 @@ EXPORTS = ("dap_status_string", "dap_version", "dap_device_sm_count", "dap_plan_
            "dap_set_trace_events", "dap_get_device_errors", "dap_multi_tokens_per_tile",
            "dap_q_tile_map", "dap_workspace_bytes_multi", "decode_attn_paged_multi",
            "decode_attn_paged_fp8kv", "kv_append_paged_fp8", "decode_attn_paged_masked",
-           "dap_selftest_wait_timeout")
+           "dap_selftest_wait_timeout", "kv_append_paged_fp8_multi", "kv_read_paged_fp8")
 
 
 SPLITS_BALANCED = -1   # include/dap.h: DAP_SPLITS_BALANCED
@@ -118,6 +118,10 @@ def load(build_if_missing: bool = True):
         lib.decode_attn_paged_fp8kv.restype = I
         lib.kv_append_paged_fp8.argtypes = [P, P, P, P, P, P, I, I, P, I, P, I, I, I, P]
         lib.kv_append_paged_fp8.restype = I
+        lib.kv_append_paged_fp8_multi.argtypes = [P, P, LL, LL, LL, LL, P, P, P, P, I, I, P, I, P, P, I, I, I, I, P]
+        lib.kv_append_paged_fp8_multi.restype = I
+        lib.kv_read_paged_fp8.argtypes = [P, P, P, P, I, I, P, I, P, P, I, I, I, I, P, P, LL, LL, LL, LL, P]
+        lib.kv_read_paged_fp8.restype = I
         lib.dap_set_trace_events.argtypes = [P, P, P]
         lib.dap_set_trace_events.restype = None
         lib.dap_get_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), I]
@@ -643,3 +647,70 @@ def kv_append_paged_fp8(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_
                                         _ptr(positions), B, Hkv, D, _stream(stream, dev))
     _check(st, "kv_append_paged_fp8")
     return k_codes, v_codes, k_scale, v_scale
+
+
+# ---- runs of tokens in the fp8 (e4m3) cache -----------------------------------------------
+
+def _runs(block_table, indptr, positions):
+    B = positions.numel()
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous()
+          and block_table.shape[0] == B, "block_table must be contiguous int32 [B, max_pages]")
+    _need(indptr.dtype == torch.int32 and indptr.numel() == B + 1 and indptr.is_contiguous(),
+          "indptr must be contiguous int32 [B + 1]")
+    _need(positions.dtype == torch.int32 and positions.is_contiguous(), "positions must be contiguous int32 [B]")
+    return B
+
+
+def kv_append_paged_fp8_multi(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, *,
+                              stream=None):
+    """Quantise runs of tokens into the e4m3 GQA cache (include/dap.h:
+    kv_append_paged_fp8_multi).  k_new/v_new [total_tokens, Hkv, D] hold the rows of all
+    sequences back to back (views of a fused projection will do), ``indptr`` [B + 1] the runs'
+    boundaries and ``positions`` [B] the position of each run's first row.  Returns the four
+    cache arrays, updated in place."""
+    dev = _device_of("kv_append_paged_fp8_multi", k_new, v_new=v_new, k_codes=k_codes, v_codes=v_codes,
+                     k_scale=k_scale, v_scale=v_scale, block_table=block_table, indptr=indptr, positions=positions)
+    _bf16_3d(k_new, "k_new")
+    _bf16_3d(v_new, "v_new")
+    T, Hkv, D = k_new.shape
+    P, ps, Hkv2, D2 = _fp8kv_cache(k_codes, v_codes, k_scale, v_scale)
+    _need(v_new.shape == k_new.shape and (Hkv2, D2) == (Hkv, D), "cache heads / dims differ from the new rows")
+    B = _runs(block_table, indptr, positions)
+    with _on(dev):
+        st = load().kv_append_paged_fp8_multi(_ptr(k_new), _ptr(v_new), k_new.stride(0), k_new.stride(1),
+                                              v_new.stride(0), v_new.stride(1), _ptr(k_codes), _ptr(v_codes),
+                                              _ptr(k_scale), _ptr(v_scale), P, ps, _ptr(block_table),
+                                              block_table.shape[1], _ptr(indptr), _ptr(positions), T, B, Hkv, D,
+                                              _stream(stream, dev))
+    _check(st, "kv_append_paged_fp8_multi")
+    return k_codes, v_codes, k_scale, v_scale
+
+
+def kv_read_paged_fp8(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, *, total_tokens: int | None = None,
+                      k_out=None, v_out=None, stream=None):
+    """Read runs of the e4m3 GQA cache back as bf16 rows (include/dap.h: kv_read_paged_fp8).
+    Runs as kv_append_paged_fp8_multi; ``total_tokens`` (the host's copy of indptr[B]) sizes the
+    outputs when they are not given.  Returns (k_out, v_out) [total_tokens, Hkv, D]; rows outside
+    every run are not written."""
+    dev = _device_of("kv_read_paged_fp8", k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale,
+                     block_table=block_table, indptr=indptr, positions=positions, k_out=k_out, v_out=v_out)
+    P, ps, Hkv, D = _fp8kv_cache(k_codes, v_codes, k_scale, v_scale)
+    B = _runs(block_table, indptr, positions)
+    if total_tokens is None:
+        _need(k_out is not None or v_out is not None, "total_tokens is needed when no output is given")
+        total_tokens = (k_out if k_out is not None else v_out).shape[0]
+    T = int(total_tokens)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _bf16_3d(t, name)
+        _need(tuple(t.shape) == (T, Hkv, D), f"{name} must be [total_tokens, Hkv, D]")
+    with _on(dev):
+        st = load().kv_read_paged_fp8(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), P, ps,
+                                      _ptr(block_table), block_table.shape[1], _ptr(indptr), _ptr(positions), T, B,
+                                      Hkv, D, _ptr(k_out), _ptr(v_out), k_out.stride(0), k_out.stride(1),
+                                      v_out.stride(0), v_out.stride(1), _stream(stream, dev))
+    _check(st, "kv_read_paged_fp8")
+    return k_out, v_out

@@ -501,6 +501,72 @@ dap_status kv_append_paged_fp8(const void *k_new, const void *v_new, uint8_t *k_
                                    block_table, max_pages, positions, B, Hkv, D, static_cast<cudaStream_t>(stream));
 }
 
+static dap_status fp8_runs(bool write, const void *k_rows, const void *v_rows, long long k_stride_t,
+                           long long k_stride_h, long long v_stride_t, long long v_stride_h, const uint8_t *k_codes,
+                           const uint8_t *v_codes, const void *k_scale, const void *v_scale, int num_pages,
+                           int page_size, const int32_t *block_table, int max_pages, const int32_t *indptr,
+                           const int32_t *positions, int total_tokens, int B, int Hkv, int D, void *stream) {
+    if (total_tokens < 0 || B < 0 || Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1 || max_pages < 1 ||
+        k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
+        return DAP_ERR_SHAPE;
+    if (total_tokens == 0) return DAP_OK;
+    // rows without a sequence; rows that share memory (a write reads such rows, a read would race)
+    if (B == 0 || (total_tokens > 1 && (k_stride_t == 0 || v_stride_t == 0)) ||
+        (Hkv > 1 && (k_stride_h == 0 || v_stride_h == 0)))
+        return DAP_ERR_SHAPE;
+    if (!(D == 64 || D == 128 || D == 256)) return DAP_ERR_UNSUPPORTED;
+    if (!k_rows || !v_rows || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !indptr || !positions)
+        return DAP_ERR_NULL;
+    if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_codes) || !aligned16(v_codes) ||
+        (reinterpret_cast<uintptr_t>(k_scale) & 1u) || (reinterpret_cast<uintptr_t>(v_scale) & 1u) ||
+        !aligned4(block_table) || !aligned4(indptr) || !aligned4(positions) ||
+        ((k_stride_t | k_stride_h | v_stride_t | v_stride_h) & 7))
+        return DAP_ERR_ALIGN;
+    RunArgs a = {};
+    a.rows[0] = static_cast<__nv_bfloat16 *>(const_cast<void *>(k_rows));
+    a.rows[1] = static_cast<__nv_bfloat16 *>(const_cast<void *>(v_rows));
+    a.st[0] = k_stride_t;
+    a.st[1] = v_stride_t;
+    a.sh[0] = k_stride_h;
+    a.sh[1] = v_stride_h;
+    a.codes[0] = const_cast<uint8_t *>(k_codes);
+    a.codes[1] = const_cast<uint8_t *>(v_codes);
+    a.scale[0] = static_cast<__nv_bfloat16 *>(const_cast<void *>(k_scale));
+    a.scale[1] = static_cast<__nv_bfloat16 *>(const_cast<void *>(v_scale));
+    a.block_table = block_table;
+    a.indptr = indptr;
+    a.positions = positions;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.T = total_tokens;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.D = D;
+    return launch_fp8_runs(a, write, static_cast<cudaStream_t>(stream));
+}
+
+dap_status kv_append_paged_fp8_multi(const void *k_new, const void *v_new, long long k_stride_t, long long k_stride_h,
+                                     long long v_stride_t, long long v_stride_h, uint8_t *k_codes, uint8_t *v_codes,
+                                     void *k_scale, void *v_scale, int num_pages, int page_size,
+                                     const int32_t *block_table, int max_pages, const int32_t *indptr,
+                                     const int32_t *positions, int total_tokens, int B, int Hkv, int D,
+                                     void *stream) {
+    return fp8_runs(true, k_new, v_new, k_stride_t, k_stride_h, v_stride_t, v_stride_h, k_codes, v_codes, k_scale,
+                    v_scale, num_pages, page_size, block_table, max_pages, indptr, positions, total_tokens, B, Hkv, D,
+                    stream);
+}
+
+dap_status kv_read_paged_fp8(const uint8_t *k_codes, const uint8_t *v_codes, const void *k_scale, const void *v_scale,
+                             int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                             const int32_t *indptr, const int32_t *positions, int total_tokens, int B, int Hkv, int D,
+                             void *k_out, void *v_out, long long k_stride_t, long long k_stride_h,
+                             long long v_stride_t, long long v_stride_h, void *stream) {
+    return fp8_runs(false, k_out, v_out, k_stride_t, k_stride_h, v_stride_t, v_stride_h, k_codes, v_codes, k_scale,
+                    v_scale, num_pages, page_size, block_table, max_pages, indptr, positions, total_tokens, B, Hkv, D,
+                    stream);
+}
+
 dap_status decode_attn_paged_fp8(const void *q, const uint8_t *kv_cache, const void *inv_scale,
                                  const int64_t *slot_idx, const int64_t *lens, int T, int NH, int HD,
                                  int W, int num_blocks, int block_size, float scale, void *out,
@@ -582,6 +648,7 @@ dap_status dap_get_device_errors(unsigned int *flags, int clear) {
     if (!read_errors_multi_gather(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_multi_tc(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_fp8kv(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_fp8_runs(flags, clear != 0)) return DAP_ERR_CUDA;
     return DAP_OK;
 }
 

@@ -2,6 +2,7 @@
 // launchers (dap_decode.cu, dap_fp8.cu).  Not installed; not part of the ABI.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -109,6 +110,20 @@ dap_status launch_append_paged_fp8(const void *k_new, const void *v_new, uint8_t
                                    void *k_scale, void *v_scale, int num_pages, int page_size,
                                    const int32_t *block_table, int max_pages, const int32_t *pos, int B, int Hkv,
                                    int D, cudaStream_t stream);
+
+// Runs of tokens in the e4m3 GQA cache (K then V in every pair); the packed bf16 rows are the
+// input of a write and the output of a read.
+struct RunArgs {
+    __nv_bfloat16 *rows[2];
+    long long st[2], sh[2];  // element strides of the rows: token, kv head
+    uint8_t *codes[2];
+    __nv_bfloat16 *scale[2];
+    const int32_t *block_table, *indptr, *positions;
+    int num_pages, page_size, max_pages, T, B, Hkv, D;
+};
+dap_status launch_fp8_runs(const RunArgs &a, bool write, cudaStream_t stream);
+bool read_errors_fp8_runs(unsigned int *flags, bool clear);
+
 bool read_errors_multi(unsigned int *flags, bool clear);
 bool read_errors_multi_gather(unsigned int *flags, bool clear);
 bool read_errors_multi_tc(unsigned int *flags, bool clear);
