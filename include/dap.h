@@ -377,6 +377,64 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
                                     long long out_stride_h, void *stream);
 
 /*
+ * Decode of a batch whose sequences share long prefixes (a system prompt, a document asked by
+ * many): decode_attn_paged where the sequences come in groups, and the first prefix_lens[g] positions
+ * of every sequence of group g hold the same K and V.  The prefix is read through the block table of
+ * the group's first sequence, once for up to 256 query rows (sequences x the G heads of a kv head; 128
+ * at D = 256), as a matrix product on the tensor cores; the rest of each sequence is read through its
+ * own block table.  The result is decode_attn_paged's up to rounding.
+ *
+ * Groups are runs of consecutive sequences.  dap_shared_map builds the work map on the host:
+ *   group_sizes   host int32 [num_groups], each >= 0 (a sequence that shares nothing: a group of 1).
+ *   group_indptr  host int32 [num_groups + 1], seq_group  host int32 [sum of the sizes],
+ *   tile_group, tile_index  host int32 [max_tiles] (written): tile w covers the seqs_per_tile sequences
+ *                 from tile_index[w] * seqs_per_tile on of group tile_group[w].
+ * Returns the number of tiles, or -1 when max_tiles is too small or an input is invalid.
+ * dap_shared_seqs_per_tile: 256 / G (128 / G at D = 256), 0 for unsupported heads.
+ * dap_shared_prefix_splits: the planner's splits of the prefix for sm_count SMs (each split is one CTA
+ * per tile and kv head).  Pure host functions; no CUDA call.
+ */
+int dap_shared_seqs_per_tile(int Hq, int Hkv, int D);
+int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *group_indptr,
+                   int32_t *seq_group, int32_t *tile_group, int32_t *tile_index, int max_tiles);
+int dap_shared_prefix_splits(int sm_count, int num_tiles, int Hkv, int max_prefix_len);
+
+/* Workspace bytes of decode_attn_paged_shared for the split counts that a call runs: room for
+ * B * (prefix_splits + suffix_splits) * Hq partial rows of (D + 2) floats.  Pure host function. */
+size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int suffix_splits);
+
+/*
+ *   q, k_cache, v_cache, block_table, out, scale, strides, alignment: as decode_attn_paged.
+ *   seq_lens      device int32 [B]: the whole length of each sequence, its prefix included; 0 (an empty
+ *                 row, whose output is zero) or prefix_lens[g] <= seq_lens[b] <= prefix_lens[g] +
+ *                 max_suffix_len, within max_pages * page_size.  A length between 0 and the prefix gives a
+ *                 zero row, one past the bound is lowered to it; both set DAP_DEVERR_SEQLEN.
+ *   prefix_lens   device int32 [num_groups], each in [0, max_prefix_len] (else clamped and flagged).  A
+ *                 prefix need not end with a page: the page that it ends in may be each sequence's own.
+ *   group_indptr, seq_group, tile_group, tile_index: device copies of dap_shared_map's output.  An entry out
+ *                 of range leaves its tile or sequence out (DAP_DEVERR_QMAP; a zero row).
+ *   max_prefix_len, max_suffix_len  host: upper bounds of prefix_lens[g] and seq_lens[b] - prefix_lens[g].
+ *   prefix_splits, suffix_splits    0: the planner's (dap_shared_prefix_splits(SMs, num_tiles, Hkv,
+ *                 max_prefix_len); dap_resolve_splits(0, SMs, B, Hq, Hkv, D, page_size, max_suffix_len, 0));
+ *                 >= 1: explicit; both lowered as dap_resolve_splits does.  A part whose bound is 0 runs none.
+ *   workspace     device, >= dap_workspace_bytes_shared(B, Hq, D, the two counts run), 16-byte aligned.
+ *   Supported: D in {64, 128, 256}; G in {1, 2, 4, 8}; any page_size >= 1.  seqs_per_tile as
+ *   dap_shared_seqs_per_tile.  The summation order depends only on logical positions, the group sizes and the
+ *   split counts, so a result is the same for any placement of the pages.
+ */
+dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long long q_stride_h,
+                                    const void *k_cache, const void *v_cache, int num_pages,
+                                    int page_size, const int32_t *block_table, int max_pages,
+                                    const int32_t *seq_lens, const int32_t *prefix_lens,
+                                    const int32_t *group_indptr, const int32_t *seq_group,
+                                    const int32_t *tile_group, const int32_t *tile_index,
+                                    int num_groups, int num_tiles, int seqs_per_tile,
+                                    int max_prefix_len, int max_suffix_len, int B, int Hq, int Hkv,
+                                    int D, float scale, int prefix_splits, int suffix_splits,
+                                    void *workspace, size_t workspace_bytes, void *out,
+                                    long long out_stride_b, long long out_stride_h, void *stream);
+
+/*
  * fp8 sliding-window latent decode, K = V [C].
  *   For token t and window position j < W, slot = slot_idx[t, j]; the row takes part iff
  *   j < lens[t] and slot >= 0.  Its value is bf16(e4m3(kv_cache[slot / block_size,

@@ -32,7 +32,9 @@ EXPORTS = ("dap_status_string", "dap_version", "dap_device_sm_count", "dap_plan_
            "dap_set_trace_events", "dap_get_device_errors", "dap_multi_tokens_per_tile",
            "dap_q_tile_map", "dap_workspace_bytes_multi", "decode_attn_paged_multi",
            "decode_attn_paged_fp8kv", "kv_append_paged_fp8", "decode_attn_paged_masked",
-           "dap_selftest_wait_timeout", "kv_append_paged_fp8_multi", "kv_read_paged_fp8")
+           "dap_selftest_wait_timeout", "kv_append_paged_fp8_multi", "kv_read_paged_fp8",
+           "decode_attn_paged_shared", "dap_shared_seqs_per_tile", "dap_shared_map", "dap_shared_prefix_splits",
+           "dap_workspace_bytes_shared")
 
 
 SPLITS_BALANCED = -1   # include/dap.h: DAP_SPLITS_BALANCED
@@ -122,6 +124,17 @@ def load(build_if_missing: bool = True):
         lib.kv_append_paged_fp8_multi.restype = I
         lib.kv_read_paged_fp8.argtypes = [P, P, P, P, I, I, P, I, P, P, I, I, I, I, P, P, LL, LL, LL, LL, P]
         lib.kv_read_paged_fp8.restype = I
+        lib.dap_shared_seqs_per_tile.argtypes = [I, I, I]
+        lib.dap_shared_seqs_per_tile.restype = I
+        lib.dap_shared_map.argtypes = [P, I, I, P, P, P, P, I]
+        lib.dap_shared_map.restype = I
+        lib.dap_shared_prefix_splits.argtypes = [I, I, I, I]
+        lib.dap_shared_prefix_splits.restype = I
+        lib.dap_workspace_bytes_shared.argtypes = [I, I, I, I, I]
+        lib.dap_workspace_bytes_shared.restype = SZ
+        lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I,
+                                                 F, I, I, P, SZ, P, LL, LL, P]
+        lib.decode_attn_paged_shared.restype = I
         lib.dap_set_trace_events.argtypes = [P, P, P]
         lib.dap_set_trace_events.restype = None
         lib.dap_get_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), I]
@@ -577,6 +590,94 @@ def decode_attn_paged_multi(q, k_cache, v_cache, block_table, seq_lens, plan: Mu
                                          int(max_kv_len), B, Hq, Hkv, D, float(scale), int(S), _ptr(workspace),
                                          wbytes, _ptr(out), out.stride(0), out.stride(1), _stream(stream, dev))
     _check(st, "decode_attn_paged_multi")
+    return out
+
+
+# ---- decode of a batch that shares prefixes ------------------------------------------------
+
+class SharedPlan:
+    """The groups of one batch (consecutive sequences that share a prefix) and their work map on the
+    device (include/dap.h: dap_shared_map), made once for as long as the grouping lasts.  The lengths are
+    not part of it."""
+
+    def __init__(self, group_sizes, Hq: int, Hkv: int, D: int, device):
+        sizes = torch.as_tensor(group_sizes, dtype=torch.int32).cpu().contiguous().reshape(-1)
+        lib = load()
+        self.Hq, self.Hkv, self.D = int(Hq), int(Hkv), int(D)
+        self.seqs_per_tile = lib.dap_shared_seqs_per_tile(self.Hq, self.Hkv, self.D)
+        _need(self.seqs_per_tile > 0, "Hq / Hkv must be 1, 2, 4 or 8 and D 64, 128 or 256")
+        _need(sizes.numel() > 0 and int(sizes.min()) >= 0, "group_sizes must be one or more counts >= 0")
+        self.B, self.num_groups = int(sizes.sum(dtype=torch.int64)), sizes.numel()
+        cap = sum(-(-n // self.seqs_per_tile) for n in sizes.tolist())
+        host = torch.zeros(self.num_groups + 1 + self.B + 2 * cap, dtype=torch.int32)
+        parts = host.split([self.num_groups + 1, self.B, cap, cap])
+        self.num_tiles = lib.dap_shared_map(_ptr(sizes), self.num_groups, self.seqs_per_tile, *(_ptr(x) for x in parts),
+                                            cap)
+        _need(self.num_tiles == cap, "invalid group_sizes")
+        self.group_indptr, self.seq_group, self.tile_group, self.tile_index = \
+            host.to(device).split([self.num_groups + 1, self.B, cap, cap])
+
+    def splits(self, max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0, prefix_splits: int = 0,
+               suffix_splits: int = 0):
+        """The (prefix, suffix) split counts that a call with these bounds runs on the current device."""
+        lib = load()
+        sms = lib.dap_device_sm_count()
+        ps, ss = 0, 0
+        if max_prefix_len > 0:
+            ps = prefix_splits or lib.dap_shared_prefix_splits(sms, self.num_tiles, self.Hkv, max_prefix_len)
+            ps = lib.dap_resolve_splits(ps, sms, self.num_tiles, self.Hq, self.Hkv, self.D, 1, max_prefix_len, 0)
+        if max_suffix_len > 0:
+            ss = lib.dap_resolve_splits(suffix_splits, sms, self.B, self.Hq, self.Hkv, self.D, 1, max_suffix_len,
+                                        total_suffix)
+        return ps, ss
+
+
+def workspace_bytes_shared(plan: SharedPlan, *, max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0,
+                           prefix_splits: int = 0, suffix_splits: int = 0) -> int:
+    """Workspace bytes of a decode_attn_paged_shared call with these arguments on the current device."""
+    ps, ss = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits),
+                         int(suffix_splits))
+    return load().dap_workspace_bytes_shared(plan.B, plan.Hq, plan.D, ps, ss)
+
+
+def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan: SharedPlan, *,
+                             max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0,
+                             scale: float | None = None, prefix_splits: int = 0, suffix_splits: int = 0,
+                             workspace=None, out=None, stream=None):
+    """Paged GQA decode of a batch whose sequences share prefixes in groups (include/dap.h:
+    decode_attn_paged_shared): decode_attn_paged with the first prefix_lens[g] positions of a group read
+    once, through the block table of its first sequence.  ``seq_lens`` [B] count the prefix;
+    ``max_suffix_len`` bounds what a sequence has behind it; ``total_suffix`` is the host-known sum of
+    that, which the planner uses when given.  Returns ``out`` [B, Hq, D]."""
+    _bf16_3d(q, "q")
+    B, Hq, D = q.shape
+    _need((B, Hq, D) == (plan.B, plan.Hq, plan.D), "q differs from the plan's batch, heads or head dim")
+    dev = _device_of("decode_attn_paged_shared", q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                     seq_lens=seq_lens, prefix_lens=prefix_lens, plan=plan.group_indptr, workspace=workspace, out=out)
+    P, ps, Hkv = _paged_cache(q, k_cache, v_cache, block_table, seq_lens, B)
+    _need(Hkv == plan.Hkv, "the cache's kv heads differ from the plan's")
+    _need(prefix_lens.dtype == torch.int32 and prefix_lens.numel() == plan.num_groups and prefix_lens.is_contiguous(),
+          "prefix_lens must be contiguous int32 [num_groups]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
+    _bf16_3d(out, "out")
+    _need(out.shape == q.shape, "out must be [B, Hq, D]")
+    lib = load()
+    with _on(dev):
+        S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits),
+                        int(suffix_splits))
+        if workspace is None:
+            workspace = torch.empty(lib.dap_workspace_bytes_shared(B, Hq, D, *S), dtype=torch.uint8, device=dev)
+        st = lib.decode_attn_paged_shared(_ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), P, ps,
+                                          _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(prefix_lens),
+                                          _ptr(plan.group_indptr), _ptr(plan.seq_group), _ptr(plan.tile_group),
+                                          _ptr(plan.tile_index), plan.num_groups, plan.num_tiles, plan.seqs_per_tile,
+                                          int(max_prefix_len), int(max_suffix_len), B, Hq, Hkv, D, float(scale), *S,
+                                          _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
+                                          out.stride(0), out.stride(1), _stream(stream, dev))
+    _check(st, "decode_attn_paged_shared")
     return out
 
 

@@ -501,6 +501,135 @@ dap_status kv_append_paged_fp8(const void *k_new, const void *v_new, uint8_t *k_
                                    block_table, max_pages, positions, B, Hkv, D, static_cast<cudaStream_t>(stream));
 }
 
+int dap_shared_seqs_per_tile(int Hq, int Hkv, int D) {
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !supported_group(Hq / Hkv) || (D != 64 && D != 128 && D != 256)) return 0;
+    return (D == 256 ? 128 : 256) / (Hq / Hkv);
+}
+
+int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *group_indptr,
+                   int32_t *seq_group, int32_t *tile_group, int32_t *tile_index, int max_tiles) {
+    const int n = dap_q_tile_map(group_sizes, num_groups, seqs_per_tile, group_indptr, tile_group, tile_index, max_tiles);
+    if (n > 0 && !seq_group) return -1;
+    if (n > 0)
+        for (int g = 0; g < num_groups; ++g)
+            for (int b = group_indptr[g]; b < group_indptr[g + 1]; ++b) seq_group[b] = g;
+    return n;
+}
+
+int dap_shared_prefix_splits(int sm_count, int num_tiles, int Hkv, int max_prefix_len) {
+    if (sm_count <= 0 || num_tiles <= 0 || Hkv <= 0 || max_prefix_len <= 0) return 1;
+    // One CTA per SM.  The cost of S splits, in K/V tiles of one CTA: the waves of the grid times
+    // (a chunk's tiles and what a CTA takes to start and end, about 6), and half a tile for every
+    // partial that the combine reads.
+    const long long units = (long long)num_tiles * Hkv, tiles = ceil_div_ll(max_prefix_len, kTileTokens);
+    int best = 1;
+    double cost = 1e300;
+    for (long long S = 1; S <= std::min<long long>(tiles, std::max<long long>(1, 2 * sm_count / units)); ++S) {
+        const long long per = ceil_div_ll(tiles, S), n = ceil_div_ll(tiles, per);
+        const double c = (double)ceil_div_ll(units * n, sm_count) * (per + 6) + 0.5 * n;
+        if (c < cost) {
+            cost = c;
+            best = (int)n;
+        }
+    }
+    return best;
+}
+
+size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int suffix_splits) {
+    if (B <= 0 || Hq <= 0 || D <= 0 || prefix_splits < 0 || suffix_splits < 0) return 0;
+    const int S = prefix_splits + suffix_splits;
+    return partial_acc_bytes(B, Hq, D, S) + partial_ml_bytes(B, Hq, S);
+}
+
+dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long long q_stride_h, const void *k_cache,
+                                    const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                                    int max_pages, const int32_t *seq_lens, const int32_t *prefix_lens,
+                                    const int32_t *group_indptr, const int32_t *seq_group,
+                                    const int32_t *tile_group, const int32_t *tile_index, int num_groups,
+                                    int num_tiles, int seqs_per_tile, int max_prefix_len, int max_suffix_len, int B,
+                                    int Hq, int Hkv, int D, float scale, int prefix_splits, int suffix_splits,
+                                    void *workspace, size_t workspace_bytes, void *out, long long out_stride_b,
+                                    long long out_stride_h, void *stream) {
+    if (prefix_splits < 0 || prefix_splits > 65536 || suffix_splits < 0 || num_groups < 0 || num_tiles < 0 ||
+        max_suffix_len < 0)
+        return DAP_ERR_SHAPE;
+    dap_status st = check_common(q, q_stride_b, q_stride_h, seq_lens, max_prefix_len, B, Hq, Hkv, D, scale,
+                                 suffix_splits, out, out_stride_b, out_stride_h);
+    if (st != DAP_OK || B == 0) return st;
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 ||
+        (long long)max_prefix_len > (long long)max_pages * page_size ||
+        (long long)max_suffix_len > (long long)max_pages * page_size || num_groups < 1 || num_tiles < 1 ||
+        num_tiles > B)
+        return DAP_ERR_SHAPE;
+    if (!k_cache || !v_cache || !block_table || !prefix_lens || !group_indptr || !seq_group || !tile_group ||
+        !tile_index)
+        return DAP_ERR_NULL;
+    const int per_tile = dap_shared_seqs_per_tile(Hq, Hkv, D);
+    if (per_tile == 0) return DAP_ERR_UNSUPPORTED;
+    if (seqs_per_tile != per_tile) return DAP_ERR_SHAPE;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(prefix_lens) ||
+        !aligned4(group_indptr) || !aligned4(seq_group) || !aligned4(tile_group) || !aligned4(tile_index))
+        return DAP_ERR_ALIGN;
+    // every row ends in the combine; a part whose bound is 0 has no splits
+    if (max_prefix_len == 0) {
+        prefix_splits = 0;
+    } else {
+        if (prefix_splits == 0) {
+            const int sms = dap_device_sm_count();
+            if (sms <= 0) return DAP_ERR_CUDA;
+            prefix_splits = dap_shared_prefix_splits(sms, num_tiles, Hkv, max_prefix_len);
+        }
+        prefix_splits = dap_resolve_splits(prefix_splits, 0, num_tiles, Hq, Hkv, D, page_size, max_prefix_len, 0);
+    }
+    if (max_suffix_len == 0) {
+        suffix_splits = 0;
+    } else {
+        const int sms = suffix_splits == 0 ? dap_device_sm_count() : 0;
+        if (suffix_splits == 0 && sms <= 0) return DAP_ERR_CUDA;
+        suffix_splits = dap_resolve_splits(suffix_splits, sms, B, Hq, Hkv, D, page_size, max_suffix_len, 0);
+    }
+    const size_t need = dap_workspace_bytes_shared(B, Hq, D, prefix_splits, suffix_splits);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DAP_ERR_WORKSPACE;
+    SharedArgs a = {};
+    a.q = q;
+    a.q_sb = q_stride_b;
+    a.q_sh = q_stride_h;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.seq_lens = seq_lens;
+    a.prefix_lens = prefix_lens;
+    a.group_indptr = group_indptr;
+    a.seq_group = seq_group;
+    a.tile_group = tile_group;
+    a.tile_index = tile_index;
+    a.num_groups = num_groups;
+    a.num_tiles = num_tiles;
+    a.seqs_per_tile = seqs_per_tile;
+    a.max_prefix_len = max_prefix_len;
+    a.max_suffix_len = max_suffix_len;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.scale = scale;
+    a.prefix_splits = prefix_splits;
+    a.prefix_chunk = prefix_splits > 0 ? dap_chunk_tokens(max_prefix_len, prefix_splits) : kTileTokens;
+    a.suffix_splits = suffix_splits;
+    a.suffix_chunk = suffix_splits > 0 ? dap_chunk_tokens(max_suffix_len, suffix_splits) : kTileTokens;
+    a.workspace = workspace;
+    a.out = out;
+    a.o_sb = out_stride_b;
+    a.o_sh = out_stride_h;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (prefix_splits > 0 && (st = launch_shared_prefix(a, cs)) != DAP_OK) return st;
+    if (suffix_splits > 0 && (st = launch_shared_suffix(a, cs)) != DAP_OK) return st;
+    return launch_shared_combine(a, cs);
+}
+
 static dap_status fp8_runs(bool write, const void *k_rows, const void *v_rows, long long k_stride_t,
                            long long k_stride_h, long long v_stride_t, long long v_stride_h, const uint8_t *k_codes,
                            const uint8_t *v_codes, const void *k_scale, const void *v_scale, int num_pages,
@@ -649,6 +778,9 @@ dap_status dap_get_device_errors(unsigned int *flags, int clear) {
     if (!read_errors_multi_tc(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_fp8kv(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_fp8_runs(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_shared_prefix(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_shared_suffix(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_shared_suffix_gather(flags, clear != 0)) return DAP_ERR_CUDA;
     return DAP_OK;
 }
 

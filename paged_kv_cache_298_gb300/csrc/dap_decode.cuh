@@ -147,10 +147,22 @@ struct MmaConsumer {
     // byte offset of (key, dim) in the swizzled tile (tile_off)
     __device__ __forceinline__ uint32_t off(int key, int dim) const { return tile_off<C>(key, dim >> 3, rb); }
 
-    __device__ __forceinline__ void tile(uint8_t *stage, int nvalid) {
+    // Keys [nskip, nvalid) of the tile take part (nskip only with SKIP).
+    template <bool SKIP = false>
+    __device__ __forceinline__ void tile(uint8_t *stage, int nvalid, int nskip = 0) {
         const int nv = nvalid - key0;
-        if (nv <= 0) return;  // no key of this slice is valid
+        const int ns = SKIP ? nskip - key0 : 0;
+        if (nv <= 0 || (SKIP && ns >= 16)) return;  // no key of this slice is valid
         uint8_t *sV = stage + C::TILE_BYTES;
+        if (SKIP && ns > 0) {  // weight zero, whatever the rows before the first key hold
+            for (int i = lane; i < ns * C::NBLK * C::CPB; i += 32) {
+                const int row = key0 + i / (C::NBLK * C::CPB);
+                *reinterpret_cast<uint4 *>(sV + tile_off<C>(row, i % (C::NBLK * C::CPB), rb)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
         if (nv < 16) {  // rows past the end may hold anything: zero their V so 0 * V stays 0
             for (int i = lane; i < (16 - nv) * C::NBLK * C::CPB; i += 32) {
                 const int row = key0 + nv + i / (C::NBLK * C::CPB);
@@ -174,7 +186,7 @@ struct MmaConsumer {
             }
         }
         // online softmax, base 2; keys g (c0, c1) and g + 8 (c2, c3)
-        const bool v0 = g < nv, v1 = g + 8 < nv;
+        const bool v0 = g < nv && (!SKIP || g >= ns), v1 = g + 8 < nv && (!SKIP || g + 8 >= ns);
         float s[4];
         s[0] = v0 ? __fmul_rn(c[0], qscale) : -INFINITY;  // (rounded once: the same value feeds max and exp)
         s[1] = v0 ? __fmul_rn(c[1], qscale) : -INFINITY;

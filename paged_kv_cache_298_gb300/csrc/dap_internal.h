@@ -111,6 +111,33 @@ dap_status launch_append_paged_fp8(const void *k_new, const void *v_new, uint8_t
                                    const int32_t *block_table, int max_pages, const int32_t *pos, int B, int Hkv,
                                    int D, cudaStream_t stream);
 
+// Decode of a batch whose sequences share prefixes, already validated.
+struct SharedArgs {
+    const void *q;
+    long long q_sb, q_sh;
+    const void *k, *v;
+    int num_pages, page_size;
+    const int32_t *block_table;
+    int max_pages;
+    const int32_t *seq_lens, *prefix_lens;
+    const int32_t *group_indptr, *seq_group, *tile_group, *tile_index;
+    int num_groups, num_tiles, seqs_per_tile;
+    int max_prefix_len, max_suffix_len;
+    int B, Hq, Hkv, D;
+    float scale;
+    int prefix_splits, prefix_chunk, suffix_splits, suffix_chunk;  // 0 splits: the part is absent
+    void *workspace;
+    void *out;
+    long long o_sb, o_sh;
+};
+dap_status launch_shared_prefix(const SharedArgs &a, cudaStream_t stream);
+dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream);
+dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream);
+dap_status launch_shared_combine(const SharedArgs &a, cudaStream_t stream);
+bool read_errors_shared_prefix(unsigned int *flags, bool clear);
+bool read_errors_shared_suffix(unsigned int *flags, bool clear);
+bool read_errors_shared_suffix_gather(unsigned int *flags, bool clear);
+
 // Runs of tokens in the e4m3 GQA cache (K then V in every pair); the packed bf16 rows are the
 // input of a write and the output of a read.
 struct RunArgs {

@@ -1,0 +1,322 @@
+// dap_shared.cuh -- decode of a batch whose sequences share prefixes: what its kernels have in
+// common, and the suffix kernel (instantiated by dap_shared_suffix.cu and, for page sizes that are
+// not multiples of 8, dap_shared_suffix_gather.cu).  The prefix kernel is in dap_shared_prefix.cu.
+//
+// out[b,h] = sum_{t < L_b} softmax_t(scale q[b,h] . K[b,t]) V[b,t], where positions t < P_g hold the
+// same keys for every sequence b of group g.  The sum is cut into a prefix part and a suffix part,
+// each with its own running maximum and sum:
+//   * prefix: the G heads x the sequences of a group are the rows of a matrix product against the
+//     group's P_g keys, so every key is read once for up to 256 rows;
+//   * suffix: positions P_g .. L_b of each sequence, the split schedule of the single-token decode.
+// Each part is cut into splits that leave (acc, m, l) partials in the workspace, [B][prefix splits +
+// suffix splits][Hq][D] then [..][2], and a combine kernel merges a row's partials in that order.
+// The suffix kernel does not wait for the prefix kernel: it starts beside it as soon as every
+// prefix CTA runs (programmatic dependent launch), and one of its CTAs waits for the prefix
+// kernel's end before it exits, so that the combine, which waits for the suffix kernel, finds both.
+#pragma once
+
+#include "dap_decode.cuh"
+
+namespace dap {
+
+struct SharedParams {
+    SplitParams sp;  // q, caches, table, lengths, sizes, out; num_splits / chunk are the suffix's
+    const int32_t *prefix_lens, *group_indptr, *seq_group, *tile_group, *tile_index;
+    int num_groups, num_tiles, seqs_per_tile, max_prefix_len, max_suffix_len;
+    int prefix_splits, prefix_chunk, total_splits;
+    float *o_part, *ml_part;
+};
+
+// The prefix length of group g, inside its bound.
+__device__ __forceinline__ int group_prefix(const SharedParams &p, int g) {
+    return min(max(__ldg(p.prefix_lens + g), 0), p.max_prefix_len);
+}
+
+// Prefix length and length of sequence b: a length of 0, below the prefix or of no group means
+// that nothing is attended (a zero row).  `flags` gets the error bits.
+struct Span {
+    int P, L;
+};
+__device__ __forceinline__ Span seq_span(const SharedParams &p, int b, unsigned int *flags) {
+    const int g = __ldg(p.seq_group + b), Lraw = __ldg(p.sp.seq_lens + b);
+    if (g < 0 || g >= p.num_groups) {
+        *flags |= DAP_DEVERR_QMAP;
+        return {0, 0};
+    }
+    const int Praw = __ldg(p.prefix_lens + g);
+    Span s = {min(max(Praw, 0), p.max_prefix_len), Lraw};
+    if (Praw != s.P) *flags |= DAP_DEVERR_SEQLEN;
+    const long long top =
+        min((long long)s.P + p.max_suffix_len, (long long)p.sp.max_pages * p.sp.page_size);
+    if (Lraw < 0 || (Lraw > 0 && Lraw < s.P) || Lraw > top) {
+        *flags |= DAP_DEVERR_SEQLEN;
+        s.L = Lraw < s.P ? 0 : (int)top;
+    }
+    return s;
+}
+
+// Position that the suffix's first tile starts at: the boxes of a page start at multiples of R.
+__device__ __forceinline__ int suffix_start(const SharedParams &p, int P) { return P - P % p.sp.box_rows; }
+__device__ __forceinline__ int suffix_count(const SharedParams &p, const Span &s) {
+    if (s.L <= s.P) return 0;
+    return min(p.sp.num_splits, (s.L - suffix_start(p, s.P) + p.sp.chunk - 1) / p.sp.chunk);
+}
+
+// ---- suffix kernel: one CTA per (sequence, kv head, split) ---------------------------------------
+
+template <int D_, int G_, bool GATHER_>
+struct SuffixCfg {
+    static constexpr int D = D_, G = G_, HG = 1, NWC = D == 256 ? 2 : 4, BT = D == 256 ? 32 : 64, NS = 3, MINB = 2;
+    static constexpr bool GATHER = GATHER_, SWZ = true;
+    static constexpr int KPW = BT / NWC;
+    static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
+    static constexpr int TILE_BYTES = BT * ROWB;
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int MRG_OFF = NS * STAGE_BYTES;
+    static constexpr int MRG_BYTES = NWC * G * (D / 2 + 2) * 4;
+    static constexpr int MISC_OFF = MRG_OFF + MRG_BYTES;
+    static constexpr int BAR_OFF = (MISC_OFF + 16 + 7) & ~7;
+    static constexpr int SMEM = BAR_OFF + 2 * NS * 8 + 1024;  // + slack to align the base
+    static constexpr int THREADS = (NWC + 1) * 32;
+};
+
+// The split kernel of dap_decode.cuh with a start position: the same producer and consumer.
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::MINB)
+    shared_suffix_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                         const SharedParams pp) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = aligned_smem<C>(smem_raw);
+    constexpr int G = C::G, NWC = C::NWC, BT = C::BT, NS = C::NS, D = C::D;
+    const SplitParams &p = pp.sp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = p.B * p.Hkv;
+    const int s = (int)(blockIdx.x / units);
+    const int rem = (int)(blockIdx.x - s * units);
+    const int b = rem / p.Hkv;
+    const int kvh = rem - b * p.Hkv;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + NS;
+    int *misc = reinterpret_cast<int *>(smem + C::MISC_OFF);  // [0] tiles issued, [1] abort
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], full_arrivals<C>());
+            mbar_init(&empty[i], NWC);
+        }
+        misc[0] = 0;
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    // With a prefix kernel before it, this grid starts once every CTA of that kernel has passed its
+    // own wait, so what came before is done; without one it waits itself.
+    if (pp.prefix_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool last = pp.prefix_splits > 0 && blockIdx.x == gridDim.x - 1;
+    unsigned int ignored = 0;
+    const Span span = seq_span(pp, b, &ignored);  // (the combine flags the lengths)
+    const int R = p.box_rows, a0 = suffix_start(pp, span.P);
+    const int nsplit = suffix_count(pp, span);
+    const int tok0 = a0 + s * p.chunk;
+    // (the last split takes what the rounding of a0 pushes past the others)
+    const int tok1 = s == p.num_splits - 1 ? span.L : min(span.L, tok0 + p.chunk);
+    const int ntiles = s < nsplit && tok1 > tok0 ? (tok1 - tok0 + BT - 1) / BT : 0;
+    __syncthreads();
+
+    if (ntiles > 0 && warp == NWC) {
+        const int32_t *table = p.block_table + (long long)b * p.max_pages;
+        int issued = 0;
+        if constexpr (C::GATHER) {  // ---- producer warp, row gather
+            RowPages<C> rp_next;
+            lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
+            for (int i = 0; i < ntiles; ++i) {
+                const int st = i % NS;
+                const RowPages<C> rp = rp_next;
+                const int t = tok0 + i * BT;
+                if (i + 1 < ntiles)
+                    lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
+                    misc[1] = 1;
+                    break;
+                }
+                fill_tile_rows<C>(smem + st * C::STAGE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &full[st],
+                                  lane);
+                issued = i + 1;
+            }
+        } else {  // ---- producer warp: page lookup + TMA issue
+            if (lane == 0) {
+                prefetch_tensormap(&mapK);
+                prefetch_tensormap(&mapV);
+            }
+            auto lookup = [&](int tile) -> int {
+                const int t = tok0 + tile * BT + lane * R;
+                if (lane * R >= BT || t >= tok1) return 0;
+                int pg = __ldg(table + t / p.page_size);
+                if (pg < 0 || pg >= p.num_pages) {
+                    flag_error(DAP_DEVERR_PAGE);
+                    pg = 0;
+                }
+                return pg;
+            };
+            int pg_next = lookup(0);
+            for (int i = 0; i < ntiles; ++i) {
+                const int st = i % NS;
+                const int pg = pg_next;
+                if (i + 1 < ntiles) pg_next = lookup(i + 1);
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
+                    misc[1] = 1;
+                    break;
+                }
+                const int t = tok0 + i * BT;
+                const int nbox = (min(BT, tok1 - t) + R - 1) / R;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
+                __syncwarp();
+                if (lane < nbox)
+                    issue_kv_box<C>(smem + st * C::STAGE_BYTES, lane, R, &mapK, &mapV, kvh,
+                                    (t + lane * R) % p.page_size, pg, &full[st]);
+                issued = i + 1;
+            }
+        }
+        if (lane == 0) misc[0] = issued;
+    }
+    int consumed = 0;
+    MmaConsumer<C> cs;
+    if (ntiles > 0 && warp < NWC) {  // ---- consumer warps
+        cs.init(warp, lane, smem, 31 - __clz(C::GATHER ? BT : R));
+        cs.reset();
+        cs.load_q(p.q + (long long)b * p.q_sb + (long long)kvh * G * p.q_sh, p.q_sh, p.qscale);
+        for (int i = 0; i < ntiles; ++i) {
+            const int st = i % NS;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / NS) & 1))) {
+                misc[1] = 1;
+                break;
+            }
+            cs.template tile<true>(smem + st * C::STAGE_BYTES, min(BT, tok1 - (tok0 + i * BT)),
+                                   i == 0 ? span.P - tok0 : 0);
+            if (lane == 0) mbar_arrive(&empty[st]);
+            consumed = i + 1;
+        }
+    }
+    __syncthreads();  // every consumer is done; the producer has finished issuing
+    if (ntiles > 0) {
+        if (misc[1]) {  // a wait timed out: drain the copies still in flight (bounded), write nothing
+            if (threadIdx.x == 0)
+                for (int i = consumed; i < misc[0]; ++i) (void)mbar_wait(&full[i % NS], (i / NS) & 1);
+        } else if (warp < NWC) {
+            cs.finish(reinterpret_cast<float *>(smem + C::MRG_OFF),
+                      [] { named_sync(1, NWC * 32); return true; },
+                      [&](int, int g, int d, float a0v, float a1v, float M, float lv) {
+                          const long long row =
+                              ((long long)b * pp.total_splits + pp.prefix_splits + s) * p.Hq + kvh * G + g;
+                          *reinterpret_cast<float2 *>(pp.o_part + row * D + d) = make_float2(a0v, a1v);
+                          if (d == 0) *reinterpret_cast<float2 *>(pp.ml_part + row * 2) = make_float2(M, lv);
+                      });
+        }
+    }
+    if (last) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---- host side -------------------------------------------------------------------------------------
+
+namespace {
+
+inline SharedParams shared_params(const SharedArgs &a, int box_rows) {
+    SharedParams p = {};
+    SplitParams &s = p.sp;
+    s.q = static_cast<const __nv_bfloat16 *>(a.q);
+    s.q_sb = a.q_sb;
+    s.q_sh = a.q_sh;
+    s.k_cache = static_cast<const __nv_bfloat16 *>(a.k);
+    s.v_cache = static_cast<const __nv_bfloat16 *>(a.v);
+    s.block_table = a.block_table;
+    s.max_pages = a.max_pages;
+    s.seq_lens = a.seq_lens;
+    s.B = a.B;
+    s.Hq = a.Hq;
+    s.Hkv = a.Hkv;
+    s.page_size = a.page_size;
+    s.num_pages = a.num_pages;
+    s.box_rows = box_rows;
+    s.num_splits = a.suffix_splits;
+    s.chunk = a.suffix_chunk;
+    s.qscale = a.scale * 1.4426950408889634f;
+    s.out = static_cast<__nv_bfloat16 *>(a.out);
+    s.o_sb = a.o_sb;
+    s.o_sh = a.o_sh;
+    p.prefix_lens = a.prefix_lens;
+    p.group_indptr = a.group_indptr;
+    p.seq_group = a.seq_group;
+    p.tile_group = a.tile_group;
+    p.tile_index = a.tile_index;
+    p.num_groups = a.num_groups;
+    p.num_tiles = a.num_tiles;
+    p.seqs_per_tile = a.seqs_per_tile;
+    p.max_prefix_len = a.max_prefix_len;
+    p.max_suffix_len = a.max_suffix_len;
+    p.prefix_splits = a.prefix_splits;
+    p.prefix_chunk = a.prefix_chunk;
+    p.total_splits = a.prefix_splits + a.suffix_splits;
+    p.o_part = static_cast<float *>(a.workspace);
+    p.ml_part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) +
+                                          partial_acc_bytes(a.B, a.Hq, a.D, p.total_splits));
+    return p;
+}
+
+// Rows of one TMA box of the suffix's tiles (1: row gather), which also aligns the suffix's start.
+inline int suffix_box_rows(const SharedArgs &a) {
+    return a.page_size % 8 != 0 ? 1 : gcd_int(a.page_size, a.D == 256 ? 32 : 64);
+}
+
+template <int D, int G, bool GATHER>
+dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream) {
+    using C = SuffixCfg<D, G, GATHER>;
+    const int R = suffix_box_rows(a);
+    CUtensorMap mk = {}, mv = {};
+    if (!GATHER && (!encode_cache_map<C>(&mk, a.k, a.D, a.Hkv, a.page_size, a.num_pages, R) ||
+                    !encode_cache_map<C>(&mv, a.v, a.D, a.Hkv, a.page_size, a.num_pages, R)))
+        return DAP_ERR_CUDA;
+    auto kern = shared_suffix_kernel<C>;
+    static PerDeviceOcc occ = {};
+    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ) <= 0) return DAP_ERR_CUDA;
+    const long long grid = (long long)a.B * a.Hkv * a.suffix_splits;
+    if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
+    const SharedParams p = shared_params(a, R);
+    return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p) ==
+                   cudaSuccess
+               ? DAP_OK
+               : DAP_ERR_CUDA;
+}
+
+template <int D, bool GATHER>
+dap_status suffix_groups(const SharedArgs &a, cudaStream_t stream) {
+    switch (a.Hq / a.Hkv) {
+        case 1: return launch_suffix<D, 1, GATHER>(a, stream);
+        case 2: return launch_suffix<D, 2, GATHER>(a, stream);
+        case 4: return launch_suffix<D, 4, GATHER>(a, stream);
+        case 8: return launch_suffix<D, 8, GATHER>(a, stream);
+    }
+    return DAP_ERR_UNSUPPORTED;
+}
+
+template <bool GATHER>
+dap_status suffix_dims(const SharedArgs &a, cudaStream_t stream) {
+    switch (a.D) {
+        case 64: return suffix_groups<64, GATHER>(a, stream);
+        case 128: return suffix_groups<128, GATHER>(a, stream);
+        case 256: return suffix_groups<256, GATHER>(a, stream);
+    }
+    return DAP_ERR_UNSUPPORTED;
+}
+
+inline bool read_tu_errors(unsigned int *flags, bool clear) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_device_errors, sizeof v) != cudaSuccess) return false;
+    if (clear) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbol(g_device_errors, &z, sizeof z) != cudaSuccess) return false;
+    }
+    *flags |= v;
+    return true;
+}
+
+}  // namespace
+}  // namespace dap

@@ -1,0 +1,606 @@
+// dap_shared_prefix.cu -- the prefix part of the shared-prefix decode on the tcgen05 tensor cores, and
+// the combine that merges prefix and suffix partials (dap_shared.cuh has the operation).
+//
+// One CTA takes a tile of up to 256 query rows of one kv head (row r: sequence r / G of the tile, head
+// r % G), or 128 at D = 256, against one chunk of the group's prefix.  Tensor memory (lane = row of a
+// stream):
+//   q  columns [x D/2, (x + 1) D/2)        of stream x, two bf16 per column, stored once;
+//   S  columns [128 + 64 e, 192 + 64 e)    fp32 scores of 64 keys in buffer e; P (bf16 pairs)
+//                                          overwrites the first 32 once they are read;
+//   O  columns [256 + x D, 256 + (x + 1) D) fp32 accumulator of stream x.
+// Two streams (D 64, 128) keep the tensor cores busy: while the softmax of one works on its scores the
+// products of the other run.  Stream x has rows [128 x, 128 x + 128) of the tile and every K/V tile;
+// with at most 128 rows both streams hold the same rows and take every other K/V tile, merged
+// through shared memory at the end.  At D = 256 one stream fills tensor memory (its O takes 256
+// columns) and alternates between two score buffers.
+// Warps: four softmax warps a stream (thread = row), a producer (K/V tiles by TMA or row gather,
+// column block major as in dap_multi_tc.cu), and two warps that issue products: one per stream, or one
+// for S and one for PV at D = 256.
+// Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
+// when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
+// weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
+#include "dap_shared.cuh"
+#include "dap_tc.cuh"
+
+namespace dap {
+
+namespace {
+
+template <int D_, bool GATHER_>
+struct PrefixCfg {
+    static constexpr bool GATHER = GATHER_, SWZ = true;
+    static constexpr int D = D_, BT = 64;
+    static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
+    static constexpr int TILE_BYTES = BT * ROWB, STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int NSTREAM = D == 256 ? 1 : 2, SBUF = 2 / NSTREAM;  // score buffers per stream
+    static constexpr int NS = D == 64 ? 6 : 3;
+    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 3) * 32;
+    static constexpr int TS = 128, TO = 256, TMEM_COLS = 512;
+    // barriers: full[NS], empty[NS], s_done[2], p_ready[2], pv_done[2], q_ready[2], fin[2], tail
+    static constexpr int BAR_OFF = NS * STAGE_BYTES, NBAR = 2 * NS + 11;
+    static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr int USED = MISC_OFF + 32 + 1024;  // + slack to align the base to 1024
+    // D <= 128: more than half an SM's shared memory, so that two prefix CTAs never share an SM (the
+    // second would wait for tensor memory) and one suffix CTA fits beside the one there is
+    static constexpr int SMEM = D == 256 ? USED : 116 * 1024;
+    static constexpr int MRG_STRIDE = D + 4;  // floats of a row in the streams' merge
+    static_assert(USED <= SMEM && SMEM <= 227 * 1024, "shared memory");
+    static_assert(NSTREAM == 1 || 128 * MRG_STRIDE * 4 <= NS * STAGE_BYTES, "the merge fits the stage ring");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                         const SharedParams pp, const int G) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = aligned_smem<C>(smem_raw);
+    constexpr int BT = C::BT, NS = C::NS, D = C::D;
+    const SplitParams &p = pp.sp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + NS, *s_done = empty + NS, *p_ready = s_done + 2, *pv_done = p_ready + 2;
+    uint64_t *q_ready = pv_done + 2, *fin = q_ready + 2, *tail = fin + 2;
+    // [0] tiles issued, [1] abort, [2], [3] tiles landed (seen by each issuer), [4] tensor memory
+    volatile int *misc = reinterpret_cast<volatile int *>(smem + C::MISC_OFF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
+
+    const int units = pp.num_tiles * p.Hkv;
+    const int s = (int)(blockIdx.x / units);
+    const int rem = (int)(blockIdx.x - s * units);
+    const int w = rem / p.Hkv;
+    const int kvh = rem - w * p.Hkv;
+
+    // Tensor memory touches nothing the previous kernel writes: it is allocated before the wait.
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // Nothing global is read before the wait; the suffix kernel may start after it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int g = __ldg(pp.tile_group + w), wi = __ldg(pp.tile_index + w);
+    int first = 0, nseq = 0, q0 = 0, P = 0;
+    if (g >= 0 && g < pp.num_groups && wi >= 0) {
+        q0 = __ldg(pp.group_indptr + g);
+        const int q1 = __ldg(pp.group_indptr + g + 1);
+        const long long f = q0 + (long long)wi * pp.seqs_per_tile;
+        if (q0 >= 0 && q1 <= p.B && f < q1) {
+            first = (int)f;
+            nseq = min(pp.seqs_per_tile, q1 - first);
+            P = group_prefix(pp, g);
+        }
+    }
+    if (nseq == 0 && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
+    const int nrows = nseq * G;
+    const int tok0 = min(P, s * pp.prefix_chunk), tok1 = min(P, tok0 + pp.prefix_chunk);
+    const int J = (tok1 - tok0 + BT - 1) / BT;  // K/V tiles of this CTA
+    const bool work = nrows > 0 && J > 0;
+    const bool both = C::NSTREAM == 2 && nrows > 128;   // the streams have rows of their own
+    // K/V tiles of stream x: all of them, or tiles x, x + 2, ...
+    auto tiles_of = [&](int x) { return both || C::NSTREAM == 1 ? J : (J - x + 1) / 2; };
+    auto tile_at = [&](int x, int n) { return both || C::NSTREAM == 1 ? n : 2 * n + x; };
+    auto rows_of = [&](int x) { return both ? min(128, nrows - 128 * x) : nrows; };
+    auto buf_of = [](int x, int n) { return C::SBUF == 1 ? x : (n & 1); };
+    auto phase_of = [](int n) { return (uint32_t)((C::SBUF == 1 ? n : n >> 1) & 1); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], full_arrivals<C>());
+            mbar_init(&empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
+        }
+        for (int e = 0; e < 2; ++e) {
+            const int x = C::NSTREAM == 2 ? e : 0;
+            mbar_init(&s_done[e], 1);
+            mbar_init(&p_ready[e], (uint32_t)max(1, (rows_of(x) + 31) / 32));  // one per warp with rows
+            mbar_init(&pv_done[e], 1);
+            mbar_init(&q_ready[e], 4);
+            mbar_init(&fin[e], 1);
+        }
+        mbar_init(tail, 1);
+        misc[0] = misc[1] = misc[2] = misc[3] = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();  // barriers and the tensor-memory address are visible
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t CS = BT * 128;  // bytes between column blocks of a tile
+    constexpr uint32_t idS = idesc_bf16(128, BT, 0), idO = idesc_bf16(128, D, 1);
+    const int nlast = tok1 - (tok0 + (J - 1) * BT);  // keys of the last tile
+    const bool ragged = work && nlast % 16 != 0;     // its V rows up to a multiple of 16 are zeroed
+
+    if (work && warp == C::PRODUCER) {
+        const int32_t *table = p.block_table + (long long)q0 * p.max_pages;
+        const int R = p.box_rows;
+        int issued = 0;
+        if constexpr (C::GATHER) {
+            RowPages<C> rp_next;
+            lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
+            for (int i = 0; i < J; ++i) {
+                const int st = i % NS;
+                const RowPages<C> rp = rp_next;
+                const int t = tok0 + i * BT;
+                if (i + 1 < J) lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
+                    misc[1] = 1;
+                    break;
+                }
+                fill_tile_rows<C>(smem + st * C::STAGE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &full[st],
+                                  lane);
+                issued = i + 1;
+            }
+        } else {
+            if (lane == 0) {
+                prefetch_tensormap(&mapK);
+                prefetch_tensormap(&mapV);
+            }
+            auto lookup = [&](int tile) -> int {  // page of this lane's box of R keys
+                const int t = tok0 + tile * BT + lane * R;
+                if (lane * R >= BT || t >= tok1) return 0;
+                int pg = __ldg(table + t / p.page_size);
+                if (pg < 0 || pg >= p.num_pages) {
+                    flag_error(DAP_DEVERR_PAGE);
+                    pg = 0;
+                }
+                return pg;
+            };
+            int pg_next = lookup(0);
+            for (int i = 0; i < J; ++i) {
+                const int st = i % NS;
+                const int pg = pg_next;
+                if (i + 1 < J) pg_next = lookup(i + 1);
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
+                    misc[1] = 1;
+                    break;
+                }
+                const int t = tok0 + i * BT;
+                const int nbox = (min(BT, tok1 - t) + R - 1) / R;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
+                __syncwarp();
+                // lane (box j, column block cb); the page of box j is in lane j
+                const int j = lane / C::NBLK, cb = lane % C::NBLK;
+                const int pj = __shfl_sync(0xFFFFFFFFu, pg, j & 31);
+                if (j < nbox) {
+                    uint8_t *dst = smem + st * C::STAGE_BYTES + cb * CS + j * R * 128;
+                    const int row = (t + j * R) % p.page_size;
+                    tma_load_5d(dst, &mapK, 0, row, cb, kvh, pj, &full[st]);
+                    tma_load_5d(dst + C::TILE_BYTES, &mapV, 0, row, cb, kvh, pj, &full[st]);
+                }
+                issued = i + 1;
+            }
+        }
+        if (lane == 0) misc[0] = issued;
+        __syncwarp();
+        if (ragged && issued == J) {
+            // V rows past the end enter the last product with weight zero, whatever the page holds
+            const int st = (J - 1) % NS;
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ((J - 1) / NS) & 1))) {
+                const int nz = 16 - nlast % 16;
+                for (int e = lane; e < nz * C::NBLK * C::CPB; e += 32)
+                    *reinterpret_cast<uint4 *>(smem + st * C::STAGE_BYTES + C::TILE_BYTES +
+                                               tile_off<C>(nlast + e / (C::NBLK * C::CPB), e % (C::NBLK * C::CPB), 6)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tail);
+            } else {
+                misc[1] = 1;
+            }
+        }
+    } else if (work && warp >= C::ISSUER) {
+        const int role = warp - C::ISSUER;
+        if (lane == 0) {
+            bool ok = true;
+            int landed = 0;
+            auto land = [&](int j) -> bool {  // K/V tile j has landed
+                if (j < landed) return true;
+                if (!mbar_wait(&full[j % NS], (j / NS) & 1)) return false;
+                if (C::GATHER) fence_async_smem();  // (its rows were copied by the generic proxy)
+                landed = j + 1;
+                return true;
+            };
+            auto scores = [&](int x, int n, int j) {
+                tc_fence_after();
+                const uint32_t sK = smem_addr(smem + (j % NS) * C::STAGE_BYTES);
+                const uint32_t tS = tmem + C::TS + 64 * buf_of(x, n), tQ = tmem + x * (D / 2);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    umma_bf16_tmem_a(tS, tQ + k * 8, sw128_desc(sK + (k >> 2) * CS + (k & 3) * 32, 16, 1024), idS,
+                                     k > 0);
+                umma_commit(&s_done[buf_of(x, n)]);
+            };
+            auto values = [&](int x, int n, int j) {
+                tc_fence_after();
+                const int nv = j == J - 1 ? nlast : BT;
+                const uint32_t sV = smem_addr(smem + (j % NS) * C::STAGE_BYTES + C::TILE_BYTES);
+                const uint32_t tP = tmem + C::TS + 64 * buf_of(x, n), tO = tmem + C::TO + x * D;
+#pragma unroll
+                for (int k = 0; k < BT / 16; ++k)
+                    if (k * 16 < nv)
+                        umma_bf16_tmem_a(tO, tP + k * 8, sw128_desc(sV + k * 2048, CS, 1024), idO, n > 0 || k > 0);
+                umma_commit(&empty[j % NS]);
+                umma_commit(&pv_done[buf_of(x, n)]);
+            };
+            if constexpr (C::NSTREAM == 2) {  // this warp issues all products of stream `role`
+                const int x = role, N = tiles_of(x);
+                ok = N == 0 || mbar_wait(&q_ready[x], 0);
+                for (int n = 0; ok && n < N; ++n) {
+                    const int j = tile_at(x, n);
+                    // (the scores take the place of P once the product that reads it is done)
+                    ok = land(j) && (n == 0 || mbar_wait(&pv_done[x], phase_of(n - 1)));
+                    if (!ok) break;
+                    scores(x, n, j);
+                    ok = mbar_wait(&p_ready[x], phase_of(n)) && (!(ragged && j == J - 1) || mbar_wait(tail, 0));
+                    if (ok) values(x, n, j);
+                }
+            } else if (role == 0) {  // the S warp
+                ok = mbar_wait(&q_ready[0], 0);
+                for (int n = 0; ok && n < J; ++n) {
+                    ok = (n < 2 || mbar_wait(&pv_done[n & 1], phase_of(n - 2))) && land(n);
+                    if (ok) scores(0, n, n);
+                }
+            } else {  // the PV warp
+                for (int n = 0; ok && n < J; ++n) {
+                    ok = mbar_wait(&p_ready[n & 1], phase_of(n)) && land(n) &&
+                         (!(ragged && n == J - 1) || mbar_wait(tail, 0));
+                    if (ok) values(0, n, n);
+                }
+            }
+            if (!ok) misc[1] = 1;
+            misc[2 + role] = landed;
+            umma_commit(&fin[role]);  // this thread's products are done when it completes
+        }
+        __syncwarp();
+    }
+
+    // ---- softmax warps: thread = row of a stream
+    const int x = warp >> 2;  // stream (warps below NWS)
+    const int r = threadIdx.x & 127;
+    const bool soft = work && warp < C::NWS;
+    const int nx = soft ? rows_of(x) : 0;      // rows of the stream
+    const bool rvalid = r < nx;
+    const bool active = (warp & 3) * 32 < nx;  // this warp holds rows
+    const int row = both ? 128 * x + r : r;    // row of the tile
+    const int seq = first + row / G, hq = kvh * G + row % G;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + C::TO + x * D + lane_base;
+    float m_ref = -INFINITY, l = 0.f;
+    const int N = soft ? tiles_of(x) : 0;
+    if (soft) {
+        {   // q row -> tensor memory (zeros for rows without a sequence)
+            const __nv_bfloat16 *src = p.q + (long long)seq * p.q_sb + (long long)hq * p.q_sh;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t y[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v =
+                        rvalid ? *reinterpret_cast<const uint4 *>(src + 32 * c + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+                    y[4 * j] = v.x;
+                    y[4 * j + 1] = v.y;
+                    y[4 * j + 2] = v.z;
+                    y[4 * j + 3] = v.w;
+                }
+                tmem_st16(tmem + x * (D / 2) + lane_base + 16 * c, y);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[x]);
+        }
+        // Rows are independent through both products: a warp without rows skips the tiles, and what
+        // its rows of P hold reaches only its own rows of O, which are never read.
+        for (int n = 0; n < (active ? N : 0); ++n) {
+            const int e = buf_of(x, n);
+            const uint32_t tS = tmem + C::TS + 64 * e + lane_base;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_done[e], phase_of(n)))) {
+                misc[1] = 1;
+                break;
+            }
+            tc_fence_after();
+            float2 sv[BT / 2];
+            {
+                uint32_t a[32], b[32];
+                tmem_ld32_issue(tS, a);
+                tmem_ld32_issue(tS + 32, b);
+                tmem_wait_ld();
+                const float2 qs = make_float2(p.qscale, p.qscale);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    sv[k] = __fmul2_rn(make_float2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])), qs);
+                    sv[16 + k] = __fmul2_rn(make_float2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])), qs);
+                }
+            }
+            if (tile_at(x, n) == J - 1 && nlast < BT) {
+#pragma unroll
+                for (int k = 0; k < BT / 2; ++k) {
+                    if (2 * k >= nlast) sv[k].x = -INFINITY;
+                    if (2 * k + 1 >= nlast) sv[k].y = -INFINITY;
+                }
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < BT / 2; ++k) m4[k & 3] = fmaxf(m4[k & 3], fmaxf(sv[k].x, sv[k].y));
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            float alpha = 1.f;
+            if (mx > m_ref) {
+                if (m_ref == -INFINITY) {
+                    m_ref = mx;
+                } else if (mx - m_ref > 8.f) {
+                    alpha = ex2(m_ref - mx);
+                    m_ref = mx;
+                    l *= alpha;
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+                // O holds the products up to the last tile's once that one is done
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&pv_done[buf_of(x, n - 1)], phase_of(n - 1)))) {
+                    misc[1] = 1;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(tO + c, o);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[16 * u + k] * alpha);
+                        tmem_st16(tO + c + 16 * u, y);
+                    }
+                }
+            }
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+            const float2 nm = make_float2(-mu, -mu);
+            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t y[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 v = __fadd2_rn(sv[16 * u + k], nm);
+                    v.x = ex2(v.x);
+                    v.y = ex2(v.y);
+                    l2[k & 1] = __fadd2_rn(l2[k & 1], v);
+                    y[k] = pack_bf16x2(v.x, v.y);
+                }
+                tmem_st16(tS + 16 * u, y);
+            }
+            l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[e]);
+        }
+    }
+    __syncthreads();
+    if (soft) {
+        // every product is done once both fin barriers have completed
+        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0));
+        tc_fence_after();
+        const bool good = done && misc[1] == 0;
+        float *mrg = reinterpret_cast<float *>(smem);
+        float other = 0.f;  // weight of stream 1's sums at the merge
+        const bool merge = C::NSTREAM == 2 && !both;
+        if (merge) {
+            // both streams hold the same rows: stream 1 leaves its sums in the (now idle) stage ring
+            float *mr = mrg + r * C::MRG_STRIDE;
+            if (x == 1 && active && good) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (N > 0) tmem_ld32(tO + c, o);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<float4 *>(mr + c + k) =
+                            N > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                *reinterpret_cast<float2 *>(mr + D) = make_float2(m_ref, l);
+            }
+            named_sync(1, C::NWS * 32);
+        }
+        if ((x == 0 || !merge) && active && good) {
+            const float *mr = mrg + r * C::MRG_STRIDE;
+            float mine = 1.f;
+            if (merge) {
+                const float2 ml = *reinterpret_cast<const float2 *>(mr + D);
+                const float m = fmaxf(m_ref, ml.x), mu = m == -INFINITY ? 0.f : m;
+                mine = ex2(m_ref - mu);
+                other = ex2(ml.x - mu);
+                m_ref = m;
+                l = l * mine + ml.y * other;
+            }
+            const long long prow = ((long long)seq * pp.total_splits + s) * p.Hq + hq;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(tO + c, o);
+                if (merge) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(mr + c + k);
+                        o[k] = o[k] * mine + v.x * other;
+                        o[k + 1] = o[k + 1] * mine + v.y * other;
+                        o[k + 2] = o[k + 2] * mine + v.z * other;
+                        o[k + 3] = o[k + 3] * mine + v.w * other;
+                    }
+                }
+                if (rvalid) {
+                    float *dst = pp.o_part + prow * D + c;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<float4 *>(dst + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+            }
+            if (rvalid) *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
+        }
+        if (threadIdx.x == 0 && misc[1]) {
+            // a wait gave up: the copies still in flight land (bounded) before the shared memory goes
+            for (int i = min(misc[2], misc[3]); i < misc[0]; ++i) (void)mbar_wait(&full[i % NS], (i / NS) & 1);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// Merge of a row's prefix and suffix partials, in that order; W warps a row, warp w taking partials
+// w, w + W, ... and the warps' sums added in warp order.
+template <int D, int W>
+__global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams pp) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int DPV = D / 32;
+    __shared__ float red[W > 1 ? 8 : 1][W > 1 ? D + 1 : 1];
+    const SplitParams &p = pp.sp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long gw = W == 8 ? (long long)blockIdx.x : (long long)blockIdx.x * 8 + warp;
+    if (gw >= (long long)p.B * p.Hq) return;
+    const int b = (int)(gw / p.Hq), hq = (int)(gw - (long long)b * p.Hq);
+    unsigned int flags = 0;
+    const Span span = seq_span(pp, b, &flags);
+    if (flags && hq == 0 && lane == 0 && (W == 1 || warp == 0)) flag_error(flags);
+    const int np = span.L > 0 && span.P > 0 ? (span.P + pp.prefix_chunk - 1) / pp.prefix_chunk : 0;
+    const int n = np + suffix_count(pp, span);
+    const long long row0 = (long long)b * pp.total_splits * p.Hq + hq;
+    auto row_of = [&](int i) { return row0 + (long long)(i < np ? i : i - np + pp.prefix_splits) * p.Hq; };
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, pp.ml_part[row_of(i) * 2]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    RowMerge<D> r;
+    r.begin(M);
+    const int w0 = W == 1 ? 0 : warp;
+    for (int i0 = w0; i0 < n; i0 += 8 * W) {
+        const float *o[8];
+        float2 ml[8];
+        const int m = min(8, (n - i0 + W - 1) / W);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const long long row = row_of(i0 + W * min(k, m - 1));
+            o[k] = pp.o_part + row * D;
+            ml[k] = *reinterpret_cast<const float2 *>(pp.ml_part + row * 2);
+        }
+        r.add_batch(o, ml, m, lane);
+    }
+    __nv_bfloat16 *out = p.out + (long long)b * p.o_sb + (long long)hq * p.o_sh;
+    if constexpr (W == 1) {
+        r.store(out, lane);
+    } else {
+#pragma unroll
+        for (int j = 0; j < DPV; ++j) red[warp][lane * DPV + j] = r.acc[j];
+        if (lane == 0) red[warp][D] = r.lsum;
+        __syncthreads();
+        if (threadIdx.x < D / 2) {
+            const int d = 2 * threadIdx.x;
+            float a0 = 0.f, a1 = 0.f, l = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                a0 += red[k][d];
+                a1 += red[k][d + 1];
+                l += red[k][D];
+            }
+            store_out_pair(out + d, a0, a1, l);
+        }
+    }
+}
+
+// The paged cache as [64 dims, rows, column block, kv head, page], a box of R rows of one column block.
+bool encode_block_map(CUtensorMap *map, const void *base, int D, int Hkv, int page_size, int num_pages, int R) {
+    const cuuint64_t dims[5] = {64u, (cuuint64_t)page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
+                                (cuuint64_t)num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)Hkv * D * 2, 128u, (cuuint64_t)D * 2,
+                                   (cuuint64_t)page_size * Hkv * D * 2};
+    const cuuint32_t box[5] = {64u, (cuuint32_t)R, 1u, 1u, 1u};
+    return encode_bf16(map, base, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, bool GATHER>
+dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
+    using C = PrefixCfg<D, GATHER>;
+    const int R = GATHER ? C::BT : gcd_int(a.page_size, C::BT);
+    CUtensorMap mk = {}, mv = {};
+    if (!GATHER && (!encode_block_map(&mk, a.k, a.D, a.Hkv, a.page_size, a.num_pages, R) ||
+                    !encode_block_map(&mv, a.v, a.D, a.Hkv, a.page_size, a.num_pages, R)))
+        return DAP_ERR_CUDA;
+    auto kern = shared_prefix_kernel<C>;
+    static PerDeviceOcc occ = {};
+    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ) <= 0) return DAP_ERR_CUDA;
+    const long long grid = (long long)a.num_tiles * a.Hkv * a.prefix_splits;
+    if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
+    const SharedParams p = shared_params(a, R);
+    return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p,
+                                 a.Hq / a.Hkv) == cudaSuccess
+               ? DAP_OK
+               : DAP_ERR_CUDA;
+}
+
+template <bool GATHER>
+dap_status prefix_dims(const SharedArgs &a, cudaStream_t stream) {
+    switch (a.D) {
+        case 64: return launch_prefix<64, GATHER>(a, stream);
+        case 128: return launch_prefix<128, GATHER>(a, stream);
+        case 256: return launch_prefix<256, GATHER>(a, stream);
+    }
+    return DAP_ERR_UNSUPPORTED;
+}
+
+template <int D>
+dap_status combine_d(const SharedArgs &a, cudaStream_t stream) {
+    const SharedParams p = shared_params(a, suffix_box_rows(a));
+    const long long rows = (long long)a.B * a.Hq;
+    if (rows > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
+    // (as launch_combine: a warp per row, or a CTA per row with more than 16 partials)
+    const cudaError_t e =
+        p.total_splits > 16
+            ? launch_dependent(shared_combine_kernel<D, 8>, dim3((unsigned)rows), dim3(256), stream, p)
+            : launch_dependent(shared_combine_kernel<D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), stream, p);
+    return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
+}
+
+}  // namespace
+
+dap_status launch_shared_prefix(const SharedArgs &a, cudaStream_t stream) {
+    return a.page_size % 8 != 0 ? prefix_dims<true>(a, stream) : prefix_dims<false>(a, stream);
+}
+
+dap_status launch_shared_combine(const SharedArgs &a, cudaStream_t stream) {
+    switch (a.D) {
+        case 64: return combine_d<64>(a, stream);
+        case 128: return combine_d<128>(a, stream);
+        case 256: return combine_d<256>(a, stream);
+    }
+    return DAP_ERR_UNSUPPORTED;
+}
+
+bool read_errors_shared_prefix(unsigned int *flags, bool clear) { return read_tu_errors(flags, clear); }
+
+}  // namespace dap

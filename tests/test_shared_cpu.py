@@ -1,0 +1,93 @@
+"""Host side of the shared-prefix decode, without a GPU: the work map, the planner, the workspace, and
+refusals that come back with the documented status before CUDA is touched."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_298_gb300 import binding
+
+FAKE = ctypes.c_void_p(1 << 20)   # never dereferenced: every call below fails validation first
+ODD = ctypes.c_void_p((1 << 20) + 2)
+NULL, SHAPE, UNSUPPORTED, WORKSPACE, ALIGN = 1, 2, 3, 4, 5
+
+
+def call(**kw):
+    a = dict(q=FAKE, qsb=32 * 128, qsh=128, k=FAKE, v=FAKE, P=64, ps=16, table=FAKE, maxp=64, lens=FAKE, plens=FAKE,
+             gi=FAKE, sg=FAKE, tg=FAKE, ti=FAKE, groups=1, tiles=1, spt=64, maxpre=500, maxsuf=100, B=4, Hq=32, Hkv=8, D=128,
+             scale=0.1, pre=2, suf=1, ws=None, wsb=0, out=FAKE, osb=32 * 128, osh=128)
+    a.update(kw)
+    return binding.load().decode_attn_paged_shared(
+        a["q"], a["qsb"], a["qsh"], a["k"], a["v"], a["P"], a["ps"], a["table"], a["maxp"], a["lens"], a["plens"], a["gi"],
+        a["sg"], a["tg"], a["ti"], a["groups"], a["tiles"], a["spt"], a["maxpre"], a["maxsuf"], a["B"], a["Hq"], a["Hkv"],
+        a["D"], a["scale"], a["pre"], a["suf"], a["ws"], a["wsb"], a["out"], a["osb"], a["osh"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), SHAPE), (dict(Hq=31), SHAPE), (dict(Hkv=0), SHAPE), (dict(scale=float("nan")), SHAPE),
+    (dict(scale=float("inf")), SHAPE), (dict(pre=-1), SHAPE), (dict(suf=-1), SHAPE), (dict(pre=70000), SHAPE),
+    (dict(suf=70000), SHAPE), (dict(maxpre=-1), SHAPE), (dict(maxsuf=-1), SHAPE), (dict(maxpre=64 * 16 + 1), SHAPE),
+    (dict(maxsuf=64 * 16 + 1), SHAPE), (dict(P=0), SHAPE), (dict(ps=0), SHAPE), (dict(maxp=0), SHAPE), (dict(groups=0), SHAPE),
+    (dict(tiles=0), SHAPE), (dict(tiles=5), SHAPE), (dict(spt=32), SHAPE), (dict(spt=0), SHAPE), (dict(qsb=-8), SHAPE),
+    (dict(qsb=0), SHAPE), (dict(osh=0), SHAPE),
+    (dict(D=32, qsb=1024, qsh=32), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(Hq=24), UNSUPPORTED),
+    (dict(Hq=128, spt=16), UNSUPPORTED),
+    (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(table=None), NULL), (dict(lens=None), NULL),
+    (dict(plens=None), NULL), (dict(gi=None), NULL), (dict(sg=None), NULL), (dict(tg=None), NULL), (dict(ti=None), NULL),
+    (dict(out=None), NULL),
+    (dict(q=ODD), ALIGN), (dict(k=ODD), ALIGN), (dict(out=ODD), ALIGN), (dict(table=ODD), ALIGN), (dict(plens=ODD), ALIGN),
+    (dict(gi=ODD), ALIGN), (dict(sg=ODD), ALIGN), (dict(tg=ODD), ALIGN), (dict(ti=ODD), ALIGN), (dict(qsh=132), ALIGN),
+    (dict(osb=4100), ALIGN),
+    (dict(), WORKSPACE), (dict(ws=FAKE, wsb=1000), WORKSPACE), (dict(ws=ODD, wsb=1 << 30), WORKSPACE),
+])
+def test_bad_arguments(kw, status):
+    assert call(**kw) == status
+
+
+def test_an_empty_batch_is_nothing_to_do():
+    assert call(B=0) == 0
+
+
+def test_map_covers_every_sequence_once():
+    for sizes in ([1], [64], [65], [3, 0, 200, 1], [0, 5], [128, 128]):
+        plan = binding.SharedPlan(sizes, 32, 8, 128, "cpu")
+        assert plan.seqs_per_tile == 64 and plan.B == sum(sizes)
+        assert plan.group_indptr.tolist() == [0] + list(np.cumsum(sizes))
+        assert plan.seq_group.tolist() == [g for g, n in enumerate(sizes) for _ in range(n)]
+        seen = []
+        for g, i in zip(plan.tile_group.tolist(), plan.tile_index.tolist()):
+            a, b = plan.group_indptr[g] + 64 * i, plan.group_indptr[g + 1]
+            seen += list(range(int(a), int(min(a + 64, b))))
+        assert seen == list(range(sum(sizes)))
+
+
+def test_plan_refuses():
+    for sizes, Hq, Hkv, D in (([], 32, 8, 128), ([-1, 2], 32, 8, 128), ([2], 24, 8, 128), ([2], 32, 8, 32), ([2], 33, 8, 128)):
+        with pytest.raises(ValueError):
+            binding.SharedPlan(sizes, Hq, Hkv, D, "cpu")
+    assert binding.load().dap_shared_seqs_per_tile(64, 8, 256) == 16
+    assert binding.load().dap_shared_seqs_per_tile(8, 8, 64) == 256
+    # the map without room for its tiles
+    n = torch.tensor([100], dtype=torch.int32)
+    out = [torch.zeros(200, dtype=torch.int32) for _ in range(4)]
+    assert binding.load().dap_shared_map(n.data_ptr(), 1, 64, *(t.data_ptr() for t in out), 1) == -1
+
+
+def test_prefix_splits_fill_the_device_and_cover_the_prefix():
+    f = binding.load().dap_shared_prefix_splits
+    for tiles in (1, 2, 3, 7, 20, 40):
+        for Hkv in (1, 2, 8):
+            for P in (1, 63, 64, 65, 1000, 8192, 32768):
+                S = f(152, tiles, Hkv, P)
+                assert 1 <= S <= -(-P // 64)
+                assert S * binding.chunk_tokens(P, S) >= P
+    assert f(152, 2, 8, 32768) == 9          # 144 CTAs on 152 SMs
+    assert f(0, 1, 1, 100) == f(152, 0, 8, 100) == f(152, 1, 8, 0) == 1
+
+
+def test_workspace():
+    w = binding.load().dap_workspace_bytes_shared
+    assert w(4, 32, 128, 0, 0) == 0
+    assert w(4, 32, 128, 2, 1) >= 4 * 3 * 32 * 130 * 4
+    assert w(0, 32, 128, 2, 1) == 0 and w(4, 32, 128, -1, 1) == 0
