@@ -1,4 +1,5 @@
-"""Thin Python binding of the C ABI in include/dap.h (ctypes; argument marshalling only).
+"""Thin Python binding of the C ABI in include/dap.h (argument marshalling only: ctypes, and the
+extension ``_dap_torch`` of csrc/dap_torch.cpp for the calls whose host time counts most).
 
 Every function here takes torch tensors, checks dtypes and devices, and passes raw
 pointers, sizes and the current CUDA stream to ``libdap.so``.  All arithmetic runs in the
@@ -8,6 +9,7 @@ library's CUDA kernels: there is no fallback, and a missing or unloadable librar
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -16,8 +18,10 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libdap.so")
+_EXT_PATH = os.path.join(_PKG, "_dap_torch.so")
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 DAP_OK = 0
 STATUS_NAMES = {0: "DAP_OK", 1: "DAP_ERR_NULL", 2: "DAP_ERR_SHAPE", 3: "DAP_ERR_UNSUPPORTED",
@@ -58,8 +62,10 @@ def library_path() -> str:
 
 
 def load(build_if_missing: bool = True):
-    """Load libdap.so (building it with nvcc when absent or stale, if allowed)."""
-    global _lib
+    """Load libdap.so and the extension beside it (building them when absent or stale, if allowed)."""
+    global _lib, _ext
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -68,10 +74,11 @@ def load(build_if_missing: bool = True):
             try:
                 _build.build()
             except Exception as e:  # no nvcc or a compile error: fail loudly
-                if not os.path.exists(_LIB_PATH):
+                if not (os.path.exists(_LIB_PATH) and os.path.exists(_EXT_PATH)):
                     raise RuntimeError(f"libdap.so is missing and could not be built: {e}") from e
-        if not os.path.exists(_LIB_PATH):
-            raise RuntimeError(f"libdap.so not found at {_LIB_PATH}; run __graft_entry__.build()")
+        for path in (_LIB_PATH, _EXT_PATH):
+            if not os.path.exists(path):
+                raise RuntimeError(f"{os.path.basename(path)} not found at {path}; run __graft_entry__.build()")
         lib = ctypes.CDLL(_LIB_PATH)
         P, I, LL, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
         lib.dap_status_string.argtypes = [I]
@@ -141,8 +148,22 @@ def load(build_if_missing: bool = True):
         lib.dap_get_device_errors.restype = I
         lib.dap_selftest_wait_timeout.argtypes = [ctypes.c_void_p]
         lib.dap_selftest_wait_timeout.restype = I
+        try:
+            spec = importlib.util.spec_from_file_location("_dap_torch", _EXT_PATH)
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+        except ImportError as e:  # built for another torch or Python
+            raise RuntimeError(f"{_EXT_PATH} cannot be loaded; run __graft_entry__.build(): {e}") from e
+        ext.set_error(DapError)
+        _ext = ext
         _lib = lib
         return lib
+
+
+def _native():
+    if _ext is None:
+        load()
+    return _ext
 
 
 def status_string(status: int) -> str:
@@ -177,15 +198,20 @@ def _device_of(what: str, first, **others) -> torch.device:
     return dev
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _on:
     """Makes `dev` the current device for the library call (skipped when it already is)."""
 
+    __slots__ = ("idx", "prev")
+
     def __init__(self, dev):
-        self.idx = dev.index
+        self.idx = dev if type(dev) is int else dev.index
         self.prev = None
 
     def __enter__(self):
-        cur = torch.cuda.current_device()
+        cur = _current_device()
         if cur != self.idx:
             self.prev = cur
             torch.cuda.set_device(self.idx)
@@ -199,15 +225,16 @@ class _on:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream, dev: torch.device):
-    """The stream handle for a call on `dev`: the given stream (which must belong to `dev`)
-    or that device's current stream."""
+def _stream(stream, dev):
+    """The stream handle for a call on `dev` (a device or its index): the given stream (which must
+    belong to it) or that device's current stream."""
+    idx = dev if type(dev) is int else dev.index
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(dev.index)
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device.index != dev.index:
-        raise DapError(None, f"the stream belongs to {stream.device}, the call's tensors to {dev}")
+            return _raw_stream(idx)
+        stream = torch.cuda.current_stream(idx)
+    elif stream.device.index != idx:
+        raise DapError(None, f"the stream belongs to {stream.device}, the call's tensors to cuda:{idx}")
     return stream.cuda_stream
 
 
@@ -285,8 +312,8 @@ def selftest_wait_timeout(stream=None) -> None:
 # ---- decode entry points ---------------------------------------------------------------
 
 def _bf16_3d(t, name):
-    _need(t.dtype == torch.bfloat16 and t.dim() == 3 and t.stride(2) == 1,
-          f"{name} must be a bf16 [*, *, D] tensor with unit stride in D")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a bf16 [*, *, D] tensor with unit stride in D")
 
 
 def _paged_cache(q, k_cache, v_cache, block_table, seq_lens, B):
@@ -298,7 +325,7 @@ def _paged_cache(q, k_cache, v_cache, block_table, seq_lens, B):
           and block_table.shape[0] == B, "block_table must be contiguous int32 [B, max_pages]")
     _need(seq_lens.dtype == torch.int32 and seq_lens.numel() == B and seq_lens.is_contiguous(),
           "seq_lens must be contiguous int32 [B]")
-    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    return k_cache.shape[:3]
 
 
 def decode_attn_paged(q, k_cache, v_cache, block_table, seq_lens, *, max_kv_len: int,
@@ -455,11 +482,11 @@ def _fp8kv_cache(k_codes, v_codes, k_scale, v_scale):
     _need(k_codes.dtype == torch.uint8 and k_codes.dim() == 4 and k_codes.is_contiguous()
           and v_codes.shape == k_codes.shape and v_codes.dtype == torch.uint8 and v_codes.is_contiguous(),
           "k_codes/v_codes must be contiguous uint8 [P, ps, Hkv, D]")
-    P, ps, Hkv, D = k_codes.shape
+    shape = P, ps, Hkv, D = k_codes.shape
     for f in (k_scale, v_scale):
-        _need(f.dtype == torch.bfloat16 and f.is_contiguous() and tuple(f.shape) == (P, Hkv, ps),
+        _need(f.dtype == torch.bfloat16 and f.is_contiguous() and f.shape == (P, Hkv, ps),
               "k_scale/v_scale must be contiguous bf16 [P, Hkv, ps]")
-    return P, ps, Hkv, D
+    return shape
 
 
 def decode_attn_paged_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, *, max_kv_len: int,
@@ -614,14 +641,28 @@ class SharedPlan:
         self.num_tiles = lib.dap_shared_map(_ptr(sizes), self.num_groups, self.seqs_per_tile, *(_ptr(x) for x in parts),
                                             cap)
         _need(self.num_tiles == cap, "invalid group_sizes")
+        self.map = host.to(device)   # group_indptr, seq_group, tile_group and tile_index, back to back
         self.group_indptr, self.seq_group, self.tile_group, self.tile_index = \
-            host.to(device).split([self.num_groups + 1, self.B, cap, cap])
+            self.map.split([self.num_groups + 1, self.B, cap, cap])
+        self.sizes = (self.B, self.Hq, self.Hkv, self.D, self.num_groups, self.num_tiles, self.seqs_per_tile)
+        self._last = (None, None)
 
     def splits(self, max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0, prefix_splits: int = 0,
-               suffix_splits: int = 0):
-        """The (prefix, suffix) split counts that a call with these bounds runs on the current device."""
+               suffix_splits: int = 0, device: int | None = None):
+        """The (prefix, suffix) split counts that a call with these bounds runs on a device (index;
+        default: the current one)."""
+        if device is None or device < 0:
+            device = _current_device() if torch.cuda.is_available() else -1
+        key = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
+        last, found = self._last
+        if last == key:
+            return found
         lib = load()
-        sms = lib.dap_device_sm_count()
+        if device >= 0:
+            with _on(device):
+                sms = lib.dap_device_sm_count()
+        else:
+            sms = 0
         ps, ss = 0, 0
         if max_prefix_len > 0:
             ps = prefix_splits or lib.dap_shared_prefix_splits(sms, self.num_tiles, self.Hkv, max_prefix_len)
@@ -629,6 +670,7 @@ class SharedPlan:
         if max_suffix_len > 0:
             ss = lib.dap_resolve_splits(suffix_splits, sms, self.B, self.Hq, self.Hkv, self.D, 1, max_suffix_len,
                                         total_suffix)
+        self._last = (key, (ps, ss))   # (steps of one batch often share their bounds)
         return ps, ss
 
 
@@ -649,36 +691,13 @@ def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_
     once, through the block table of its first sequence.  ``seq_lens`` [B] count the prefix;
     ``max_suffix_len`` bounds what a sequence has behind it; ``total_suffix`` is the host-known sum of
     that, which the planner uses when given.  Returns ``out`` [B, Hq, D]."""
-    _bf16_3d(q, "q")
-    B, Hq, D = q.shape
-    _need((B, Hq, D) == (plan.B, plan.Hq, plan.D), "q differs from the plan's batch, heads or head dim")
-    dev = _device_of("decode_attn_paged_shared", q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     seq_lens=seq_lens, prefix_lens=prefix_lens, plan=plan.group_indptr, workspace=workspace, out=out)
-    P, ps, Hkv = _paged_cache(q, k_cache, v_cache, block_table, seq_lens, B)
-    _need(Hkv == plan.Hkv, "the cache's kv heads differ from the plan's")
-    _need(prefix_lens.dtype == torch.int32 and prefix_lens.numel() == plan.num_groups and prefix_lens.is_contiguous(),
-          "prefix_lens must be contiguous int32 [num_groups]")
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
-    _bf16_3d(out, "out")
-    _need(out.shape == q.shape, "out must be [B, Hq, D]")
-    lib = load()
-    with _on(dev):
-        S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits),
-                        int(suffix_splits))
-        if workspace is None:
-            workspace = torch.empty(lib.dap_workspace_bytes_shared(B, Hq, D, *S), dtype=torch.uint8, device=dev)
-        st = lib.decode_attn_paged_shared(_ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), P, ps,
-                                          _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(prefix_lens),
-                                          _ptr(plan.group_indptr), _ptr(plan.seq_group), _ptr(plan.tile_group),
-                                          _ptr(plan.tile_index), plan.num_groups, plan.num_tiles, plan.seqs_per_tile,
-                                          int(max_prefix_len), int(max_suffix_len), B, Hq, Hkv, D, float(scale), *S,
-                                          _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
-                                          out.stride(0), out.stride(1), _stream(stream, dev))
-    _check(st, "decode_attn_paged_shared")
-    return out
+        scale = 1.0 / math.sqrt(plan.D)
+    dev = q.get_device()
+    S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits), int(suffix_splits), dev)
+    return _native().decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan.map, plan.sizes,
+                                   int(max_prefix_len), int(max_suffix_len), S, scale, workspace, out,
+                                   None if stream is None else _stream(stream, dev))
 
 
 # ---- cache writes ------------------------------------------------------------------------
@@ -752,16 +771,6 @@ def kv_append_paged_fp8(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_
 
 # ---- runs of tokens in the fp8 (e4m3) cache -----------------------------------------------
 
-def _runs(block_table, indptr, positions):
-    B = positions.numel()
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous()
-          and block_table.shape[0] == B, "block_table must be contiguous int32 [B, max_pages]")
-    _need(indptr.dtype == torch.int32 and indptr.numel() == B + 1 and indptr.is_contiguous(),
-          "indptr must be contiguous int32 [B + 1]")
-    _need(positions.dtype == torch.int32 and positions.is_contiguous(), "positions must be contiguous int32 [B]")
-    return B
-
-
 def kv_append_paged_fp8_multi(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, *,
                               stream=None):
     """Quantise runs of tokens into the e4m3 GQA cache (include/dap.h:
@@ -769,21 +778,8 @@ def kv_append_paged_fp8_multi(k_new, v_new, k_codes, v_codes, k_scale, v_scale, 
     sequences back to back (views of a fused projection will do), ``indptr`` [B + 1] the runs'
     boundaries and ``positions`` [B] the position of each run's first row.  Returns the four
     cache arrays, updated in place."""
-    dev = _device_of("kv_append_paged_fp8_multi", k_new, v_new=v_new, k_codes=k_codes, v_codes=v_codes,
-                     k_scale=k_scale, v_scale=v_scale, block_table=block_table, indptr=indptr, positions=positions)
-    _bf16_3d(k_new, "k_new")
-    _bf16_3d(v_new, "v_new")
-    T, Hkv, D = k_new.shape
-    P, ps, Hkv2, D2 = _fp8kv_cache(k_codes, v_codes, k_scale, v_scale)
-    _need(v_new.shape == k_new.shape and (Hkv2, D2) == (Hkv, D), "cache heads / dims differ from the new rows")
-    B = _runs(block_table, indptr, positions)
-    with _on(dev):
-        st = load().kv_append_paged_fp8_multi(_ptr(k_new), _ptr(v_new), k_new.stride(0), k_new.stride(1),
-                                              v_new.stride(0), v_new.stride(1), _ptr(k_codes), _ptr(v_codes),
-                                              _ptr(k_scale), _ptr(v_scale), P, ps, _ptr(block_table),
-                                              block_table.shape[1], _ptr(indptr), _ptr(positions), T, B, Hkv, D,
-                                              _stream(stream, dev))
-    _check(st, "kv_append_paged_fp8_multi")
+    _native().append_runs(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions,
+                          None if stream is None else _stream(stream, k_new.get_device()))
     return k_codes, v_codes, k_scale, v_scale
 
 
@@ -793,25 +789,5 @@ def kv_read_paged_fp8(k_codes, v_codes, k_scale, v_scale, block_table, indptr, p
     Runs as kv_append_paged_fp8_multi; ``total_tokens`` (the host's copy of indptr[B]) sizes the
     outputs when they are not given.  Returns (k_out, v_out) [total_tokens, Hkv, D]; rows outside
     every run are not written."""
-    dev = _device_of("kv_read_paged_fp8", k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale,
-                     block_table=block_table, indptr=indptr, positions=positions, k_out=k_out, v_out=v_out)
-    P, ps, Hkv, D = _fp8kv_cache(k_codes, v_codes, k_scale, v_scale)
-    B = _runs(block_table, indptr, positions)
-    if total_tokens is None:
-        _need(k_out is not None or v_out is not None, "total_tokens is needed when no output is given")
-        total_tokens = (k_out if k_out is not None else v_out).shape[0]
-    T = int(total_tokens)
-    if k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
-    if v_out is None:
-        v_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _bf16_3d(t, name)
-        _need(tuple(t.shape) == (T, Hkv, D), f"{name} must be [total_tokens, Hkv, D]")
-    with _on(dev):
-        st = load().kv_read_paged_fp8(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), P, ps,
-                                      _ptr(block_table), block_table.shape[1], _ptr(indptr), _ptr(positions), T, B,
-                                      Hkv, D, _ptr(k_out), _ptr(v_out), k_out.stride(0), k_out.stride(1),
-                                      v_out.stride(0), v_out.stride(1), _stream(stream, dev))
-    _check(st, "kv_read_paged_fp8")
-    return k_out, v_out
+    return _native().read_runs(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, total_tokens, k_out,
+                               v_out, None if stream is None else _stream(stream, k_codes.get_device()))

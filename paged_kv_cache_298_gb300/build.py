@@ -1,8 +1,9 @@
-"""Build the C-ABI CUDA library ``libdap.so`` in-tree for sm_103a with nvcc.
+"""Build the C-ABI CUDA library ``libdap.so`` in-tree for sm_103a with nvcc, and the Python
+extension ``_dap_torch.so`` (argument marshalling, csrc/dap_torch.cpp) with the host compiler.
 
-Each translation unit is compiled in parallel, then linked with ``nvcc -shared``.  The
-result lands next to this file; objects go to ``_build/``.  Rebuilds only when a source
-or header is newer than the library.
+Each translation unit is compiled in parallel, then linked.  The results land next to this
+file; objects go to ``_build/``.  Rebuilds only when a source or header is newer than a
+library, or when torch or Python are not those the extension was built for.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdap.so")
+EXT_SRC = os.path.join(CSRC, "dap_torch.cpp")
+EXT = os.path.join(PKG, "_dap_torch.so")
+EXT_FOR = os.path.join(BUILD, "_dap_torch.for")   # the torch and Python that EXT was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-O2", "-I", INCLUDE, "-I", CSRC]
@@ -37,14 +42,40 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [EXT_SRC, os.path.abspath(__file__)])
+
+
+def _ext_for() -> str:
+    import torch
+
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, Python {sys.version}"
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not all(os.path.exists(f) for f in (LIB, EXT, EXT_FOR)):
         return False
-    t = os.path.getmtime(LIB)
+    with open(EXT_FOR) as f:
+        if f.read() != _ext_for():
+            return False
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _ext_flags() -> tuple[list[str], list[str]]:
+    """Compile and link flags of the extension: torch's own headers and libraries."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda", "include"),
+           INCLUDE]
+    comp = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for d in inc:
+        comp += ["-isystem" if d != INCLUDE else "-I", d]
+    lib = os.path.join(root, "lib")
+    link = [f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{PKG}", "-l:libdap.so",
+            f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    return comp, link
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -54,18 +85,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     nvcc = _nvcc()
     flags = NVCC_FLAGS + (extra_flags or [])
 
+    cxx = os.environ.get("CXX", "g++")
+    ext_comp, ext_link = _ext_flags()
+
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc, *flags, "-c", src, "-o", obj]
+        cmd = [cxx, *ext_comp, "-c", src, "-o", obj] if src == EXT_SRC else [nvcc, *flags, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(compile_one, sources()))
+        *objs, ext_obj = ex.map(compile_one, sources() + [EXT_SRC])
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64",
            *objs, "-o", tmp]
@@ -73,6 +107,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = EXT + f".tmp{os.getpid()}"
+    r = subprocess.run([cxx, "-shared", ext_obj, "-o", tmp, *ext_link], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    with open(EXT_FOR, "w") as f:
+        f.write(_ext_for())
     return LIB
 
 
