@@ -22,10 +22,9 @@ namespace dap {
 
 namespace {
 
-// Both kernels are bound by memory (3 D + 2 bytes a row).  A CTA takes TT consecutive tokens x all kv
-// heads of K or of V (blockIdx.y), about BATCH rows, so that a token's codes (Hkv D bytes) are read or
-// written in one place and the factors of neighbouring slots meet in one store; all loads of a batch
-// are in flight before the first is used.
+// Both kernels are bound by memory (3 D + 2 bytes a row).  A CTA takes TT consecutive tokens x all kv heads of K
+// and V, so that a place is looked up once for 2 Hkv rows, a token's codes (Hkv D bytes) are read or written in
+// one place and the factors of neighbouring slots meet in one store.
 constexpr int kMaxTT = 64;
 
 // Sequence of packed row r, found by a whole warp that probes 32 boundaries at once (B up to 1024
@@ -43,8 +42,7 @@ __device__ __forceinline__ int find_run(const int32_t *indptr, int B, int r, int
 }
 
 // Slot of the pool (page * page_size + slot in the page) of tokens r0 .. r0 + n - 1, one per thread of the
-// first warps: -1 where the row is in no run, -2 where its position or page is outside (flagged once, by the
-// CTAs of K); and the slot in its page.
+// first warps: -1 where the row is in no run, -2 where its position or page is outside (flagged); and the slot in its page.
 struct Places {
     long long row[kMaxTT];
     int slot[kMaxTT];
@@ -76,8 +74,8 @@ __device__ __forceinline__ void find_places(const RunArgs &p, int r0, int n, Pla
             slot = (int)((uint32_t)pos - (uint32_t)pg * (uint32_t)p.page_size);
             const int page = __ldg(p.block_table + (long long)lo * p.max_pages + pg);
             if (page >= 0 && page < p.num_pages) row = (long long)page * p.page_size + slot;
-            else if (blockIdx.y == 0) flag_error(DAP_DEVERR_PAGE);
-        } else if (blockIdx.y == 0) {
+            else flag_error(DAP_DEVERR_PAGE);
+        } else {
             flag_error(DAP_DEVERR_SEQLEN);
         }
     }
@@ -110,8 +108,31 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// Write: D / 8 lanes a row, 8 values (16 bytes) each, U rows a lane in flight.  The rows are loaded before
-// their places are looked up (their address does not depend on them).
+__device__ __forceinline__ __nv_bfloat162 habs2(uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    return *reinterpret_cast<const __nv_bfloat162 *>(&w);
+}
+
+// Four values -> four codes, round to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+// 8 values divided by s by the hardware's rules (by value: the common path keeps its codes in registers).
+__device__ __noinline__ uint2 slow_codes(uint4 w, float s) {
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y), c = bf16x2_to_float2(w.z),
+                 d = bf16x2_to_float2(w.w);
+    return make_uint2(e4m3x4(make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s)),
+                             make_float2(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s))),
+                      e4m3x4(make_float2(__fdiv_rn(c.x, s), __fdiv_rn(c.y, s)),
+                             make_float2(__fdiv_rn(d.x, s), __fdiv_rn(d.y, s))));
+}
+
+// Write: D / 16 lanes a row, two chunks of 8 values (16 bytes) each; a lane takes the K row and the V row of
+// one (token, head), which share their place, and loads the next pair before it works on this one.  The first
+// rows are loaded before any place is looked up (their address does not depend on it).  The maximum is taken
+// on bf16 pairs, which is exact and skips NaN as fmaxf does.
 // A quotient x / y is one product with the approximate reciprocal and one correction step (q -= (q y - x) / y,
 // the remainder exact in a fused multiply-add): within 2^-44 of itself before its last rounding.  Code: a
 // quotient that binary32 holds (every tie between two codes is one) comes out exactly, and any other lies at
@@ -119,46 +140,55 @@ __device__ __forceinline__ float rcp(float x) {
 // from where its rounding changes.  Rows with a maximum outside [2^-90, 2^90], where the steps could leave the
 // normal range, are divided by the hardware's rules.
 template <int D>
-__global__ void __launch_bounds__(256) append_runs_kernel(const RunArgs p, const int TT) {
-    constexpr int LPR = D / 8, RPP = 256 / LPR, U = 4;
+__global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, const int TT) {
+    constexpr int LPR = D / 16, RPP = 256 / LPR;
     __shared__ Places place;
-    extern __shared__ __nv_bfloat16 factor[];  // [Hkv][TT]
+    extern __shared__ __nv_bfloat16 factor[];  // [2][Hkv][TT]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int kv = blockIdx.y;
-    const int r0 = blockIdx.x * TT, n = min(TT, p.T - r0), rows = n * p.Hkv;
-    const int sub = threadIdx.x / LPR, c = threadIdx.x % LPR;
-    const long long st = kv ? p.st[1] : p.st[0], sh = kv ? p.sh[1] : p.sh[0];
-    const __nv_bfloat16 *src = (kv ? p.rows[1] : p.rows[0]) + c * 8 + (long long)r0 * st;
-    uint8_t *codes = (kv ? p.codes[1] : p.codes[0]) + c * 8;
-    RowStep at(sub, RPP, p.Hkv);
-    for (int base = 0; base < rows; base += RPP * U) {
-        uint4 x[U];
-        int tok[U], head[U];
+    const int r0 = blockIdx.x * TT, n = min(TT, p.T - r0);
+    const int c = threadIdx.x % LPR;
+    const __nv_bfloat16 *ks = p.rows[0] + c * 8 + (long long)r0 * p.st[0];
+    const __nv_bfloat16 *vs = p.rows[1] + c * 8 + (long long)r0 * p.st[1];
+    RowStep at(threadIdx.x / LPR, RPP, p.Hkv);
+    uint4 next[4];
+    auto load = [&] {  // the K row and the V row at (at.tok, at.head)
+        if (at.tok < n) {
+            const __nv_bfloat16 *k = ks + at.tok * p.st[0] + at.head * p.sh[0];
+            const __nv_bfloat16 *v = vs + at.tok * p.st[1] + at.head * p.sh[1];
+            next[0] = *reinterpret_cast<const uint4 *>(k);
+            next[1] = *reinterpret_cast<const uint4 *>(k + D / 2);
+            next[2] = *reinterpret_cast<const uint4 *>(v);
+            next[3] = *reinterpret_cast<const uint4 *>(v + D / 2);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            tok[u] = at.tok;
-            head[u] = at.head;
-            at.next();
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (tok[u] < n) x[u] = *reinterpret_cast<const uint4 *>(src + tok[u] * st + head[u] * sh);
+            for (int u = 0; u < 4; ++u) next[u] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (base == 0) {
-            find_places(p, r0, n, place);
-            __syncthreads();
-        }
+    };
+    load();
+    find_places(p, r0, n, place);
+    __syncthreads();
+    while (__any_sync(0xFFFFFFFFu, at.tok < n)) {
+        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float2 f[4];
-            float amax = 0.f;
+        for (int u = 0; u < 4; ++u) x[u] = next[u];
+        const int tok = at.tok, head = at.head;
+        at.next();
+        load();
+        const bool live = tok < n;
+        const long long row = live ? place.row[tok] : -1;
+        const long long off = (row * p.Hkv + head) * D + c * 8;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f[k] = bf16x2_to_float2(w[k]);
-                amax = fmaxf(amax, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-            }
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t w[8] = {x[2 * kv].x,     x[2 * kv].y,     x[2 * kv].z,     x[2 * kv].w,
+                                   x[2 * kv + 1].x, x[2 * kv + 1].y, x[2 * kv + 1].z, x[2 * kv + 1].w};
+            __nv_bfloat162 m2 = habs2(w[0]);
 #pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            for (int k = 1; k < 8; ++k) m2 = __hmax2(m2, habs2(w[k]));
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) m2 = __hmax2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
+            const float amax = fmaxf(__bfloat162float(m2.x), __bfloat162float(m2.y));
+            uint32_t code[4];
             __nv_bfloat16 s16;
             if (amax >= 0x1p-90f && amax <= 0x1p90f) {
                 constexpr float c448 = 1.f / 448.f;
@@ -166,61 +196,61 @@ __global__ void __launch_bounds__(256) append_runs_kernel(const RunArgs p, const
                 s16 = __float2bfloat16_rn(fmaf(fmaf(q0, 448.f, -amax), -c448, q0));
                 const float s = __bfloat162float(s16), rc = rcp(s);
                 const float2 r2 = make_float2(rc, rc), n2 = make_float2(-rc, -rc), s2 = make_float2(s, s);
+                const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // (this order of signs keeps the sign of a zero)
-                    const float2 q = __fmul2_rn(f[k], r2);
-                    f[k] = __ffma2_rn(__ffma2_rn(q, s2, make_float2(-f[k].x, -f[k].y)), n2, q);
+                for (int k = 0; k < 8; k += 2) {  // (this order of signs keeps the sign of a zero)
+                    const float2 a = bf16x2_to_float2(w[k]), b = bf16x2_to_float2(w[k + 1]);
+                    const float2 qa = __fmul2_rn(a, r2), qb = __fmul2_rn(b, r2);
+                    code[k / 2] = e4m3x4(__ffma2_rn(__ffma2_rn(qa, s2, __fmul2_rn(a, minus)), n2, qa),
+                                         __ffma2_rn(__ffma2_rn(qb, s2, __fmul2_rn(b, minus)), n2, qb));
                 }
             } else {
                 s16 = __float2bfloat16_rn(amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f);
-                const float s = __bfloat162float(s16);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = make_float2(__fdiv_rn(f[k].x, s), __fdiv_rn(f[k].y, s));
+                const uint2 a = slow_codes(x[2 * kv], __bfloat162float(s16));
+                const uint2 b = slow_codes(x[2 * kv + 1], __bfloat162float(s16));
+                code[0] = a.x;
+                code[1] = a.y;
+                code[2] = b.x;
+                code[3] = b.y;
             }
-            uint32_t code[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                code[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(f[2 * k], __NV_SATFINITE, __NV_E4M3) |
-                          (uint32_t)__nv_cvt_float2_to_fp8x2(f[2 * k + 1], __NV_SATFINITE, __NV_E4M3) << 16;
-            if (tok[u] < n) {
-                const long long row = place.row[tok[u]];
-                if (row >= 0)
-                    *reinterpret_cast<uint2 *>(codes + (row * p.Hkv + head[u]) * D) = make_uint2(code[0], code[1]);
-                if (c == 0) factor[head[u] * TT + tok[u]] = s16;
+            if (row >= 0) {
+                uint8_t *dst = p.codes[kv] + off;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+                *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(code[2], code[3]);
             }
+            if (live && c == 0) factor[(kv * p.Hkv + head) * TT + tok] = s16;
         }
     }
     __syncthreads();
     // the factors head by head: neighbouring threads write neighbouring slots
-    __nv_bfloat16 *scale = kv ? p.scale[1] : p.scale[0];
-    for (int i = threadIdx.x; i < rows; i += 256) {
+    for (int i = threadIdx.x; i < n * p.Hkv; i += 256) {
         const int h = i / n, t = i - h * n;
         const long long row = place.row[t];
         const int slot = place.slot[t];
-        if (row >= 0) scale[(row - slot) * p.Hkv + (long long)h * p.page_size + slot] = factor[h * TT + t];
+        if (row >= 0) {
+            const long long at_page = (row - slot) * p.Hkv + (long long)h * p.page_size + slot;
+            p.scale[0][at_page] = factor[h * TT + t];
+            p.scale[1][at_page] = factor[(p.Hkv + h) * TT + t];
+        }
     }
 }
 
-// Read: D / 16 lanes a row, 16 codes (16 bytes) each.
+// Read: D / 16 lanes a row, two chunks of 8 codes (8 bytes read, 16 written) each, so that a warp's stores are
+// whole sectors; a lane takes the K row and the V row of one (token, head), U pairs in flight.
 template <int D>
-__global__ void __launch_bounds__(256) read_runs_kernel(const RunArgs p, const int TT) {
-    constexpr int LPR = D / 16, RPP = 256 / LPR, U = 4;
+__global__ void __launch_bounds__(256, 6) read_runs_kernel(const RunArgs p, const int TT) {
+    constexpr int LPR = D / 16, RPP = 256 / LPR, U = 2;
     __shared__ Places place;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int kv = blockIdx.y;
-    const int r0 = blockIdx.x * TT, n = min(TT, p.T - r0), rows = n * p.Hkv;
-    const int sub = threadIdx.x / LPR, c = threadIdx.x % LPR;
-    const long long st = kv ? p.st[1] : p.st[0], sh = kv ? p.sh[1] : p.sh[0];
-    __nv_bfloat16 *out = (kv ? p.rows[1] : p.rows[0]) + c * 16 + (long long)r0 * st;
-    const uint8_t *codes = (kv ? p.codes[1] : p.codes[0]) + c * 16;
-    const __nv_bfloat16 *scale = kv ? p.scale[1] : p.scale[0];
-    RowStep at(sub, RPP, p.Hkv);
+    const int r0 = blockIdx.x * TT, n = min(TT, p.T - r0);
+    const int c = threadIdx.x % LPR;
+    RowStep at(threadIdx.x / LPR, RPP, p.Hkv);
     find_places(p, r0, n, place);
     __syncthreads();
-    for (int base = 0; base < rows; base += RPP * U) {
-        uint4 x[U];
-        float s[U];
+    while (at.tok < n) {
+        uint2 x[U][2][2];
+        float s[U][2];
         int tok[U], head[U];
         bool run[U];
 #pragma unroll
@@ -228,38 +258,46 @@ __global__ void __launch_bounds__(256) read_runs_kernel(const RunArgs p, const i
             tok[u] = at.tok;
             head[u] = at.head;
             at.next();
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            s[u] = 0.f;
-            run[u] = false;
-            if (tok[u] < n) {
-                const long long row = place.row[tok[u]];
-                run[u] = row != -1;
-                if (row >= 0) {
-                    const int slot = place.slot[tok[u]];
-                    x[u] = *reinterpret_cast<const uint4 *>(codes + (row * p.Hkv + head[u]) * D);
-                    s[u] = __bfloat162float(scale[(row - slot) * p.Hkv + (long long)head[u] * p.page_size + slot]);
+            const long long row = tok[u] < n ? place.row[tok[u]] : -1;
+            run[u] = row != -1;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                x[u][kv][0] = x[u][kv][1] = make_uint2(0u, 0u);
+                s[u][kv] = 0.f;
+            }
+            if (row >= 0) {
+                const int slot = place.slot[tok[u]];
+                const long long off = (row * p.Hkv + head[u]) * D + c * 8;
+                const long long f = (row - slot) * p.Hkv + (long long)head[u] * p.page_size + slot;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    x[u][kv][0] = *reinterpret_cast<const uint2 *>(p.codes[kv] + off);
+                    x[u][kv][1] = *reinterpret_cast<const uint2 *>(p.codes[kv] + off + D / 2);
+                    s[u][kv] = __bfloat162float(p.scale[kv][f]);
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            uint32_t y[8];
-            const float2 s2 = make_float2(s[u], s[u]);
+            if (!run[u]) continue;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int kv = 0; kv < 2; ++kv) {
+                const float2 s2 = make_float2(s[u][kv], s[u][kv]);
+                __nv_bfloat16 *dst =
+                    p.rows[kv] + (long long)(r0 + tok[u]) * p.st[kv] + head[u] * p.sh[kv] + c * 8;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const __half2_raw h =
-                        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k] >> (16 * hf)), __NV_E4M3);
-                    const float2 f = __fmul2_rn(__half22float2(__half2(h)), s2);
-                    y[2 * k + hf] = pack_bf16x2(f.x, f.y);
+                    const uint32_t w[2] = {x[u][kv][hf].x, x[u][kv][hf].y};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __half2_raw h =
+                            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+                        const float2 f = __fmul2_rn(__half22float2(__half2(h)), s2);
+                        y[k] = pack_bf16x2(f.x, f.y);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + hf * (D / 2)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
-            }
-            if (run[u]) {
-                uint4 *dst = reinterpret_cast<uint4 *>(out + tok[u] * st + head[u] * sh);
-                dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
             }
         }
     }
@@ -267,14 +305,18 @@ __global__ void __launch_bounds__(256) read_runs_kernel(const RunArgs p, const i
 
 template <int D>
 dap_status launch_d(const RunArgs &a, bool write, cudaStream_t stream) {
-    const int batch = 4 * 256 / (write ? D / 8 : D / 16);  // rows of a CTA's batch of loads
-    const int TT = std::min(kMaxTT, std::max(1, batch / a.Hkv));
-    const size_t smem = write ? (size_t)a.Hkv * TT * sizeof(__nv_bfloat16) : 0;
-    if (smem > 40 * 1024) return DAP_ERR_UNSUPPORTED;  // (over 20,000 kv heads)
-    const dim3 grid((unsigned)((a.T + (long long)TT - 1) / TT), 2);
+    // Tokens of a CTA: a read, two passes of its lanes over the rows (all in flight at once); a write, whose loads
+    // run one pass ahead, one pass or up to eight while the grid stays above one wave of four CTAs per SM
+    constexpr int RPP = 256 * 16 / D;
+    const long long rows = (long long)a.T * a.Hkv, waves = (rows + RPP * 608LL - 1) / (RPP * 608LL);
+    const int passes = write ? (int)std::min<long long>(8, std::max<long long>(1, waves)) : 2;
+    const int TT = std::min(kMaxTT, std::max(1, passes * RPP / a.Hkv));
+    const dim3 grid((unsigned)((a.T + (long long)TT - 1) / TT));
+    const size_t smem = write ? (size_t)2 * a.Hkv * TT * sizeof(__nv_bfloat16) : 0;
+    if (smem > 40 * 1024) return DAP_ERR_UNSUPPORTED;  // (over 10,000 kv heads)
     const cudaError_t e =
         write ? launch_dependent_smem(append_runs_kernel<D>, grid, dim3(256), (int)smem, stream, a, TT)
-              : launch_dependent_smem(read_runs_kernel<D>, grid, dim3(256), 0, stream, a, TT);
+              : launch_dependent_smem(read_runs_kernel<D>, grid, dim3(256), (int)smem, stream, a, TT);
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
