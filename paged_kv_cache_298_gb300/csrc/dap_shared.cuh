@@ -66,7 +66,9 @@ __device__ __forceinline__ int suffix_count(const SharedParams &p, const Span &s
 
 template <int D_, int G_, bool GATHER_>
 struct SuffixCfg {
-    static constexpr int D = D_, G = G_, HG = 1, NWC = D == 256 ? 2 : 4, BT = D == 256 ? 32 : 64, NS = 3, MINB = 2;
+    // 32-key tiles and two consumer warps: 54 KB and three warps, so that one CTA fits beside a prefix CTA
+    // (164 KB, 11 warps) at D <= 128, and four share an SM without one
+    static constexpr int D = D_, G = G_, HG = 1, NWC = 2, BT = 32, NS = D == 64 ? 6 : 3, MINB = D == 256 ? 2 : 4;
     static constexpr bool GATHER = GATHER_, SWZ = true;
     static constexpr int KPW = BT / NWC;
     static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
@@ -263,7 +265,7 @@ inline SharedParams shared_params(const SharedArgs &a, int box_rows) {
 
 // Rows of one TMA box of the suffix's tiles (1: row gather), which also aligns the suffix's start.
 inline int suffix_box_rows(const SharedArgs &a) {
-    return a.page_size % 8 != 0 ? 1 : gcd_int(a.page_size, a.D == 256 ? 32 : 64);
+    return a.page_size % 8 != 0 ? 1 : gcd_int(a.page_size, 32);
 }
 
 template <int D, int G, bool GATHER>
@@ -276,7 +278,7 @@ dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream) {
         return DAP_ERR_CUDA;
     auto kern = shared_suffix_kernel<C>;
     static PerDeviceOcc occ = {};
-    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ) <= 0) return DAP_ERR_CUDA;
+    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
     const long long grid = (long long)a.B * a.Hkv * a.suffix_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);

@@ -2,20 +2,19 @@
 // the combine that merges prefix and suffix partials (dap_shared.cuh has the operation).
 //
 // One CTA takes a tile of up to 256 query rows of one kv head (row r: sequence r / G of the tile, head
-// r % G), or 128 at D = 256, against one chunk of the group's prefix.  Tensor memory (lane = row of a
-// stream):
-//   q  columns [x D/2, (x + 1) D/2)        of stream x, two bf16 per column, stored once;
-//   S  columns [128 + 64 e, 192 + 64 e)    fp32 scores of 64 keys in buffer e; P (bf16 pairs)
-//                                          overwrites the first 32 once they are read;
-//   O  columns [256 + x D, 256 + (x + 1) D) fp32 accumulator of stream x.
-// Two streams (D 64, 128) keep the tensor cores busy: while the softmax of one works on its scores the
-// products of the other run.  Stream x has rows [128 x, 128 x + 128) of the tile and every K/V tile;
-// with at most 128 rows both streams hold the same rows and take every other K/V tile, merged
-// through shared memory at the end.  At D = 256 one stream fills tensor memory (its O takes 256
-// columns) and alternates between two score buffers.
-// Warps: four softmax warps a stream (thread = row), a producer (K/V tiles by TMA or row gather,
-// column block major as in dap_multi_tc.cu), and two warps that issue products: one per stream, or one
-// for S and one for PV at D = 256.
+// r % G), or 128 at D = 256, against one chunk of the group's prefix.  Two streams of 128 rows (one at
+// D = 256) keep the tensor cores busy: stream x has rows [128 x, 128 x + 128) of the tile and every K/V
+// tile; with at most 128 rows both streams hold the same rows and take every other K/V tile, merged through
+// shared memory at the end.
+//   shared memory: q (128-byte swizzled, one TMA copy per 64 dims of 128 rows), a ring of K/V tiles of 64
+//                  keys, column block major as in dap_multi_tc.cu (TMA boxes or row gather);
+//   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
+//                                  P (bf16 pairs) overwrites the first 32 once they are read;
+//                               O  columns [256 + x D, + D)  fp32 accumulator.
+// Warps: four softmax warps a stream (thread = row), a producer, and a warp a stream that issues its products:
+// S(n + 2) as soon as the product with P(n), whose place it takes, is done, so the scores of the next tile
+// are there when the softmax of this one ends.  (With one score buffer a stream, and q in tensor memory
+// instead, a 64-key tile took 3130 cycles: every step of the chain S, softmax, PV waited for the last.)
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
 // when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
 // weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
@@ -31,38 +30,43 @@ struct PrefixCfg {
     static constexpr bool GATHER = GATHER_, SWZ = true;
     static constexpr int D = D_, BT = 64;
     static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
-    static constexpr int TILE_BYTES = BT * ROWB, STAGE_BYTES = 2 * TILE_BYTES;
-    static constexpr int NSTREAM = D == 256 ? 1 : 2, SBUF = 2 / NSTREAM;  // score buffers per stream
-    static constexpr int NS = D == 64 ? 6 : 3;
-    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 3) * 32;
-    static constexpr int TS = 128, TO = 256, TMEM_COLS = 512;
-    // barriers: full[NS], empty[NS], s_done[2], p_ready[2], pv_done[2], q_ready[2], fin[2], tail
-    static constexpr int BAR_OFF = NS * STAGE_BYTES, NBAR = 2 * NS + 11;
+    static constexpr int TILE_BYTES = BT * ROWB;              // K or V of one tile
+    static constexpr int NSTREAM = D == 256 ? 1 : 2;
+    static constexpr int NS = D == 64 ? 6 : D == 128 ? 3 : 2;  // K/V tiles in the ring
+    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 1 + NSTREAM) * 32;
+    static constexpr int TO = 256, TMEM_COLS = 512;
+    static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
+    static constexpr int RING_OFF = Q_BYTES, BAR_OFF = RING_OFF + NS * 2 * TILE_BYTES;
+    // barriers: k_full, k_empty, v_full, v_empty [NS], s_done, p_ready, pv_done [stream][buffer], q_full, fin[2], tail
+    static constexpr int NBAR = 4 * NS + 16;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr int USED = MISC_OFF + 32 + 1024;  // + slack to align the base to 1024
-    // D <= 128: more than half an SM's shared memory, so that two prefix CTAs never share an SM (the
-    // second would wait for tensor memory) and one suffix CTA fits beside the one there is
-    static constexpr int SMEM = D == 256 ? USED : 116 * 1024;
+    // more than half an SM's shared memory, so that two prefix CTAs never share an SM (the second would wait for
+    // tensor memory); at D <= 128 one suffix CTA fits beside the one there is
+    static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
     static constexpr int MRG_STRIDE = D + 4;  // floats of a row in the streams' merge
-    static_assert(USED <= SMEM && SMEM <= 227 * 1024, "shared memory");
-    static_assert(NSTREAM == 1 || 128 * MRG_STRIDE * 4 <= NS * STAGE_BYTES, "the merge fits the stage ring");
+    static_assert(SMEM <= (D == 256 ? 227 : 164) * 1024, "shared memory");
+    static_assert(NSTREAM == 1 || 128 * MRG_STRIDE * 4 <= NS * 2 * TILE_BYTES, "the merge fits the ring");
 };
 
+// (the bound of 512 threads holds the registers at 128, which leaves room for a suffix CTA's warps)
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-                         const SharedParams pp, const int G) {
+__global__ void __launch_bounds__(512, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                         const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = aligned_smem<C>(smem_raw);
     constexpr int BT = C::BT, NS = C::NS, D = C::D;
     const SplitParams &p = pp.sp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
-    uint64_t *empty = full + NS, *s_done = empty + NS, *p_ready = s_done + 2, *pv_done = p_ready + 2;
-    uint64_t *q_ready = pv_done + 2, *fin = q_ready + 2, *tail = fin + 2;
-    // [0] tiles issued, [1] abort, [2], [3] tiles landed (seen by each issuer), [4] tensor memory
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
+    uint64_t *s_done = v_empty + NS, *p_ready = s_done + 4, *pv_done = p_ready + 4;  // [2 stream + buffer]
+    uint64_t *q_full = pv_done + 4, *fin = q_full + 1, *tail = fin + 2;
+    // [0], [1] K and V tiles issued, [2] abort, [4] tensor memory
     volatile int *misc = reinterpret_cast<volatile int *>(smem + C::MISC_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
+    uint8_t *ring = smem + C::RING_OFF;
 
     const int units = pp.num_tiles * p.Hkv;
     const int s = (int)(blockIdx.x / units);
@@ -77,6 +81,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == C::PRODUCER && lane == 0) {
+        prefetch_tensormap(&mapQ);
+        if (!C::GATHER) {
+            prefetch_tensormap(&mapK);
+            prefetch_tensormap(&mapV);
+        }
+    }
     // Nothing global is read before the wait; the suffix kernel may start after it.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -86,11 +97,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (g >= 0 && g < pp.num_groups && wi >= 0) {
         q0 = __ldg(pp.group_indptr + g);
         const int q1 = __ldg(pp.group_indptr + g + 1);
+        P = group_prefix(pp, g);
         const long long f = q0 + (long long)wi * pp.seqs_per_tile;
         if (q0 >= 0 && q1 <= p.B && f < q1) {
             first = (int)f;
             nseq = min(pp.seqs_per_tile, q1 - first);
-            P = group_prefix(pp, g);
         }
     }
     if (nseq == 0 && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
@@ -103,23 +114,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto tiles_of = [&](int x) { return both || C::NSTREAM == 1 ? J : (J - x + 1) / 2; };
     auto tile_at = [&](int x, int n) { return both || C::NSTREAM == 1 ? n : 2 * n + x; };
     auto rows_of = [&](int x) { return both ? min(128, nrows - 128 * x) : nrows; };
-    auto buf_of = [](int x, int n) { return C::SBUF == 1 ? x : (n & 1); };
-    auto phase_of = [](int n) { return (uint32_t)((C::SBUF == 1 ? n : n >> 1) & 1); };
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], full_arrivals<C>());
-            mbar_init(&empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
+            mbar_init(&k_full[i], full_arrivals<C>());
+            mbar_init(&v_full[i], 1);
+            mbar_init(&k_empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
+            mbar_init(&v_empty[i], both ? 2 : 1);
         }
-        for (int e = 0; e < 2; ++e) {
-            const int x = C::NSTREAM == 2 ? e : 0;
+        for (int e = 0; e < 4; ++e) {
             mbar_init(&s_done[e], 1);
-            mbar_init(&p_ready[e], (uint32_t)max(1, (rows_of(x) + 31) / 32));  // one per warp with rows
+            mbar_init(&p_ready[e], (uint32_t)max(1, (rows_of(e >> 1) + 31) / 32));  // one per warp with rows
             mbar_init(&pv_done[e], 1);
-            mbar_init(&q_ready[e], 4);
-            mbar_init(&fin[e], 1);
         }
+        mbar_init(q_full, 1);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         mbar_init(tail, 1);
-        misc[0] = misc[1] = misc[2] = misc[3] = 0;
+        misc[0] = misc[1] = misc[2] = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -134,7 +145,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (work && warp == C::PRODUCER) {
         const int32_t *table = p.block_table + (long long)q0 * p.max_pages;
         const int R = p.box_rows;
-        int issued = 0;
+        if (lane == 0) {  // q: 64 dims of 128 rows a copy (rows past the tile's end are never read)
+            const int parts = both ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, (uint32_t)(parts * C::NBLK * C::QBLK));
+            for (int x = 0; x < parts; ++x)
+                for (int cb = 0; cb < C::NBLK; ++cb)
+                    tma_load_3d(smem + (x * C::NBLK + cb) * C::QBLK, &mapQ, cb * 64, kvh * G, first + x * (128 / G),
+                                q_full);
+        }
+        __syncwarp();
+        int ik = 0, iv = 0;
         if constexpr (C::GATHER) {
             RowPages<C> rp_next;
             lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
@@ -143,19 +163,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const RowPages<C> rp = rp_next;
                 const int t = tok0 + i * BT;
                 if (i + 1 < J) lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
-                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
-                    misc[1] = 1;
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[st], ((i / NS) - 1) & 1) &&
+                                                            mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
+                    misc[2] = 1;
                     break;
                 }
-                fill_tile_rows<C>(smem + st * C::STAGE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &full[st],
+                fill_tile_rows<C>(ring + st * 2 * C::TILE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &k_full[st],
                                   lane);
-                issued = i + 1;
+                ik = iv = i + 1;
             }
         } else {
-            if (lane == 0) {
-                prefetch_tensormap(&mapK);
-                prefetch_tensormap(&mapV);
-            }
             auto lookup = [&](int tile) -> int {  // page of this lane's box of R keys
                 const int t = tok0 + tile * BT + lane * R;
                 if (lane * R >= BT || t >= tok1) return 0;
@@ -171,106 +188,94 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int st = i % NS;
                 const int pg = pg_next;
                 if (i + 1 < J) pg_next = lookup(i + 1);
-                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
-                    misc[1] = 1;
-                    break;
-                }
                 const int t = tok0 + i * BT;
                 const int nbox = (min(BT, tok1 - t) + R - 1) / R;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
-                __syncwarp();
                 // lane (box j, column block cb); the page of box j is in lane j
                 const int j = lane / C::NBLK, cb = lane % C::NBLK;
                 const int pj = __shfl_sync(0xFFFFFFFFu, pg, j & 31);
-                if (j < nbox) {
-                    uint8_t *dst = smem + st * C::STAGE_BYTES + cb * CS + j * R * 128;
-                    const int row = (t + j * R) % p.page_size;
-                    tma_load_5d(dst, &mapK, 0, row, cb, kvh, pj, &full[st]);
-                    tma_load_5d(dst + C::TILE_BYTES, &mapV, 0, row, cb, kvh, pj, &full[st]);
+                const int row = (t + j * R) % p.page_size;
+                uint8_t *dst = ring + st * 2 * C::TILE_BYTES + cb * CS + j * R * 128;
+                const uint32_t bytes = (uint32_t)(nbox * R * C::ROWB);
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[st], ((i / NS) - 1) & 1))) {
+                    misc[2] = 1;
+                    break;
                 }
-                issued = i + 1;
+                if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
+                __syncwarp();
+                if (j < nbox) tma_load_5d(dst, &mapK, 0, row, cb, kvh, pj, &k_full[st]);
+                ik = i + 1;
+                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
+                    misc[2] = 1;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&v_full[st], bytes);
+                __syncwarp();
+                if (j < nbox) tma_load_5d(dst + C::TILE_BYTES, &mapV, 0, row, cb, kvh, pj, &v_full[st]);
+                iv = i + 1;
             }
         }
-        if (lane == 0) misc[0] = issued;
+        if (lane == 0) {
+            misc[0] = ik;
+            misc[1] = iv;
+        }
         __syncwarp();
-        if (ragged && issued == J) {
+        if (ragged && iv == J) {
             // V rows past the end enter the last product with weight zero, whatever the page holds
             const int st = (J - 1) % NS;
-            if (__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ((J - 1) / NS) & 1))) {
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(C::GATHER ? &k_full[st] : &v_full[st], ((J - 1) / NS) & 1))) {
                 const int nz = 16 - nlast % 16;
                 for (int e = lane; e < nz * C::NBLK * C::CPB; e += 32)
-                    *reinterpret_cast<uint4 *>(smem + st * C::STAGE_BYTES + C::TILE_BYTES +
+                    *reinterpret_cast<uint4 *>(ring + (st * 2 + 1) * C::TILE_BYTES +
                                                tile_off<C>(nlast + e / (C::NBLK * C::CPB), e % (C::NBLK * C::CPB), 6)) =
                         make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tail);
             } else {
-                misc[1] = 1;
+                misc[2] = 1;
             }
         }
     } else if (work && warp >= C::ISSUER) {
-        const int role = warp - C::ISSUER;
+        const int x = warp - C::ISSUER;  // the stream whose products this warp issues
         if (lane == 0) {
-            bool ok = true;
-            int landed = 0;
-            auto land = [&](int j) -> bool {  // K/V tile j has landed
-                if (j < landed) return true;
-                if (!mbar_wait(&full[j % NS], (j / NS) & 1)) return false;
-                if (C::GATHER) fence_async_smem();  // (its rows were copied by the generic proxy)
-                landed = j + 1;
-                return true;
-            };
-            auto scores = [&](int x, int n, int j) {
+            const int N = tiles_of(x);
+            const uint32_t sQ = smem_addr(smem) + (both ? x * C::NBLK * C::QBLK : 0);
+            const uint32_t tO = tmem + C::TO + x * D;
+            auto scores = [&](int n) -> bool {
+                const int j = tile_at(x, n), st = j % NS, e = 2 * x + (n & 1);
+                // (the scores take the place of P(n - 2) once the product that reads it is done)
+                if (!mbar_wait(&k_full[st], (j / NS) & 1) || (n >= 2 && !mbar_wait(&pv_done[e], ((n - 2) >> 1) & 1)))
+                    return false;
+                if (C::GATHER) fence_async_smem();  // (the tile's rows were copied by the generic proxy)
                 tc_fence_after();
-                const uint32_t sK = smem_addr(smem + (j % NS) * C::STAGE_BYTES);
-                const uint32_t tS = tmem + C::TS + 64 * buf_of(x, n), tQ = tmem + x * (D / 2);
+                const uint32_t sK = smem_addr(ring + st * 2 * C::TILE_BYTES), tS = tmem + 64 * e;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_bf16_tmem_a(tS, tQ + k * 8, sw128_desc(sK + (k >> 2) * CS + (k & 3) * 32, 16, 1024), idS,
-                                     k > 0);
-                umma_commit(&s_done[buf_of(x, n)]);
+                    umma_bf16(tS, sw128_desc(sQ + (k >> 2) * C::QBLK + (k & 3) * 32, 16, 1024),
+                              sw128_desc(sK + (k >> 2) * CS + (k & 3) * 32, 16, 1024), idS, k > 0);
+                umma_commit(&s_done[e]);
+                umma_commit(&k_empty[st]);
+                return true;
             };
-            auto values = [&](int x, int n, int j) {
+            bool ok = N == 0 || (mbar_wait(q_full, 0) && scores(0) && (N == 1 || scores(1)));
+            for (int n = 0; ok && n < N; ++n) {
+                const int j = tile_at(x, n), st = j % NS, e = 2 * x + (n & 1);
+                ok = mbar_wait(&p_ready[e], (n >> 1) & 1) && (C::GATHER || mbar_wait(&v_full[st], (j / NS) & 1)) &&
+                     (!(ragged && j == J - 1) || mbar_wait(tail, 0));
+                if (!ok) break;
                 tc_fence_after();
                 const int nv = j == J - 1 ? nlast : BT;
-                const uint32_t sV = smem_addr(smem + (j % NS) * C::STAGE_BYTES + C::TILE_BYTES);
-                const uint32_t tP = tmem + C::TS + 64 * buf_of(x, n), tO = tmem + C::TO + x * D;
+                const uint32_t sV = smem_addr(ring + (st * 2 + 1) * C::TILE_BYTES), tP = tmem + 64 * e;
 #pragma unroll
                 for (int k = 0; k < BT / 16; ++k)
                     if (k * 16 < nv)
                         umma_bf16_tmem_a(tO, tP + k * 8, sw128_desc(sV + k * 2048, CS, 1024), idO, n > 0 || k > 0);
-                umma_commit(&empty[j % NS]);
-                umma_commit(&pv_done[buf_of(x, n)]);
-            };
-            if constexpr (C::NSTREAM == 2) {  // this warp issues all products of stream `role`
-                const int x = role, N = tiles_of(x);
-                ok = N == 0 || mbar_wait(&q_ready[x], 0);
-                for (int n = 0; ok && n < N; ++n) {
-                    const int j = tile_at(x, n);
-                    // (the scores take the place of P once the product that reads it is done)
-                    ok = land(j) && (n == 0 || mbar_wait(&pv_done[x], phase_of(n - 1)));
-                    if (!ok) break;
-                    scores(x, n, j);
-                    ok = mbar_wait(&p_ready[x], phase_of(n)) && (!(ragged && j == J - 1) || mbar_wait(tail, 0));
-                    if (ok) values(x, n, j);
-                }
-            } else if (role == 0) {  // the S warp
-                ok = mbar_wait(&q_ready[0], 0);
-                for (int n = 0; ok && n < J; ++n) {
-                    ok = (n < 2 || mbar_wait(&pv_done[n & 1], phase_of(n - 2))) && land(n);
-                    if (ok) scores(0, n, n);
-                }
-            } else {  // the PV warp
-                for (int n = 0; ok && n < J; ++n) {
-                    ok = mbar_wait(&p_ready[n & 1], phase_of(n)) && land(n) &&
-                         (!(ragged && n == J - 1) || mbar_wait(tail, 0));
-                    if (ok) values(0, n, n);
-                }
+                umma_commit(&pv_done[e]);
+                umma_commit(&v_empty[st]);
+                if (n + 2 < N) ok = scores(n + 2);
             }
-            if (!ok) misc[1] = 1;
-            misc[2 + role] = landed;
-            umma_commit(&fin[role]);  // this thread's products are done when it completes
+            if (!ok) misc[2] = 1;
+            umma_commit(&fin[x]);  // this thread's products are done when it completes
         }
         __syncwarp();
     }
@@ -289,34 +294,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     float m_ref = -INFINITY, l = 0.f;
     const int N = soft ? tiles_of(x) : 0;
     if (soft) {
-        {   // q row -> tensor memory (zeros for rows without a sequence)
-            const __nv_bfloat16 *src = p.q + (long long)seq * p.q_sb + (long long)hq * p.q_sh;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t y[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v =
-                        rvalid ? *reinterpret_cast<const uint4 *>(src + 32 * c + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
-                    y[4 * j] = v.x;
-                    y[4 * j + 1] = v.y;
-                    y[4 * j + 2] = v.z;
-                    y[4 * j + 3] = v.w;
-                }
-                tmem_st16(tmem + x * (D / 2) + lane_base + 16 * c, y);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_ready[x]);
-        }
         // Rows are independent through both products: a warp without rows skips the tiles, and what
         // its rows of P hold reaches only its own rows of O, which are never read.
         for (int n = 0; n < (active ? N : 0); ++n) {
-            const int e = buf_of(x, n);
-            const uint32_t tS = tmem + C::TS + 64 * e + lane_base;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_done[e], phase_of(n)))) {
-                misc[1] = 1;
+            const int e = 2 * x + (n & 1);
+            const uint32_t tS = tmem + 64 * e + lane_base;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_done[e], (n >> 1) & 1))) {
+                misc[2] = 1;
                 break;
             }
             tc_fence_after();
@@ -356,8 +340,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
                 // O holds the products up to the last tile's once that one is done
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&pv_done[buf_of(x, n - 1)], phase_of(n - 1)))) {
-                    misc[1] = 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&pv_done[2 * x + ((n - 1) & 1)], ((n - 1) >> 1) & 1))) {
+                    misc[2] = 1;
                     break;
                 }
                 tc_fence_after();
@@ -399,11 +383,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     __syncthreads();
     if (soft) {
-        // every product is done once both fin barriers have completed
-        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0));
+        // every product is done once the fin barriers have completed
+        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && (C::NSTREAM == 1 || mbar_wait(&fin[1], 0)));
         tc_fence_after();
-        const bool good = done && misc[1] == 0;
-        float *mrg = reinterpret_cast<float *>(smem);
+        const bool good = done && misc[2] == 0;
+        float *mrg = reinterpret_cast<float *>(ring);
         float other = 0.f;  // weight of stream 1's sums at the merge
         const bool merge = C::NSTREAM == 2 && !both;
         if (merge) {
@@ -458,9 +442,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (rvalid) *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
         }
-        if (threadIdx.x == 0 && misc[1]) {
+        if (threadIdx.x == 0 && misc[2]) {
             // a wait gave up: the copies still in flight land (bounded) before the shared memory goes
-            for (int i = min(misc[2], misc[3]); i < misc[0]; ++i) (void)mbar_wait(&full[i % NS], (i / NS) & 1);
+            (void)mbar_wait(q_full, 0);
+            for (int i = max(0, misc[0] - NS); i < misc[0]; ++i) (void)mbar_wait(&k_full[i % NS], (i / NS) & 1);
+            for (int i = max(0, misc[1] - NS); !C::GATHER && i < misc[1]; ++i)
+                (void)mbar_wait(&v_full[i % NS], (i / NS) & 1);
         }
     }
     tc_fence_before();
@@ -543,21 +530,35 @@ bool encode_block_map(CUtensorMap *map, const void *base, int D, int Hkv, int pa
     return encode_bf16(map, base, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// q as [D, Hq, B] with its strides, a box of 64 dims x the G heads of a kv head x 128 / G sequences: 128 rows of
+// 128 bytes, in the tile's row order.
+bool encode_q_rows(CUtensorMap *map, const SharedArgs &a) {
+    const int G = a.Hq / a.Hkv;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.B};
+    // a stride over an extent of 1 is never used; give TMA a valid one
+    const long long sh = a.Hq > 1 ? a.q_sh : a.D;
+    const long long sb = a.B > 1 ? a.q_sb : (long long)a.Hq * sh;
+    const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    return encode_bf16(map, a.q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <int D, bool GATHER>
 dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     using C = PrefixCfg<D, GATHER>;
     const int R = GATHER ? C::BT : gcd_int(a.page_size, C::BT);
-    CUtensorMap mk = {}, mv = {};
+    CUtensorMap mq, mk = {}, mv = {};
+    if (!encode_q_rows(&mq, a)) return DAP_ERR_CUDA;
     if (!GATHER && (!encode_block_map(&mk, a.k, a.D, a.Hkv, a.page_size, a.num_pages, R) ||
                     !encode_block_map(&mv, a.v, a.D, a.Hkv, a.page_size, a.num_pages, R)))
         return DAP_ERR_CUDA;
     auto kern = shared_prefix_kernel<C>;
     static PerDeviceOcc occ = {};
-    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ) <= 0) return DAP_ERR_CUDA;
+    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
     const long long grid = (long long)a.num_tiles * a.Hkv * a.prefix_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);
-    return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p,
+    return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p,
                                  a.Hq / a.Hkv) == cudaSuccess
                ? DAP_OK
                : DAP_ERR_CUDA;

@@ -411,14 +411,19 @@ struct PerDeviceOcc {
 };
 
 // Raise the dynamic shared-memory limit of `kern` once per device (the current one), and
-// return its resident CTAs per SM there (0 on failure).
+// return its resident CTAs per SM there (0 on failure).  `carveout`: percent of the SM's memory that it
+// wants as shared memory (-1: the driver's choice; kernels that are to share an SM ask for all of it, as an
+// SM cannot change the split while CTAs run on it).
 template <class K>
-int prepare_kernel(K kern, int threads, int smem, PerDeviceOcc *cache) {
+int prepare_kernel(K kern, int threads, int smem, PerDeviceOcc *cache, int carveout = -1) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     std::lock_guard<std::mutex> lock(g_attr_mu);
     if (cache->occ[dev] > 0) return cache->occ[dev];
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+    if (carveout >= 0 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout) != cudaSuccess)
+        return 0;
     int occ = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem) != cudaSuccess) return 0;
     cache->occ[dev] = occ;
