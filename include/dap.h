@@ -386,17 +386,17 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
  *
  * Groups are runs of consecutive sequences.  dap_shared_map builds the work map on the host:
  *   group_sizes   host int32 [num_groups], each >= 0 (a sequence that shares nothing: a group of 1).
- *   group_indptr  host int32 [num_groups + 1], seq_group  host int32 [sum of the sizes],
- *   tile_group, tile_index  host int32 [max_tiles] (written): tile w covers the seqs_per_tile sequences
- *                 from tile_index[w] * seqs_per_tile on of group tile_group[w].
+ *   seq_group     host int32 [sum of the sizes] (written): the group of each sequence.
+ *   tiles         host int32 [max_tiles][4] (written): (group, first sequence of the group, first sequence of
+ *                 the tile, its sequences, at most seqs_per_tile).
  * Returns the number of tiles, or -1 when max_tiles is too small or an input is invalid.
  * dap_shared_seqs_per_tile: 256 / G (128 / G at D = 256), 0 for unsupported heads.
  * dap_shared_prefix_splits: the planner's splits of the prefix for sm_count SMs (each split is one CTA
  * per tile and kv head).  Pure host functions; no CUDA call.
  */
 int dap_shared_seqs_per_tile(int Hq, int Hkv, int D);
-int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *group_indptr,
-                   int32_t *seq_group, int32_t *tile_group, int32_t *tile_index, int max_tiles);
+int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *seq_group,
+                   int32_t *tiles, int max_tiles);
 int dap_shared_prefix_splits(int sm_count, int num_tiles, int Hkv, int max_prefix_len);
 
 /* Workspace bytes of decode_attn_paged_shared for the split counts that a call runs: room for
@@ -411,8 +411,9 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
  *                 zero row, one past the bound is lowered to it; both set DAP_DEVERR_SEQLEN.
  *   prefix_lens   device int32 [num_groups], each in [0, max_prefix_len] (else clamped and flagged).  A
  *                 prefix need not end with a page: the page that it ends in may be each sequence's own.
- *   group_indptr, seq_group, tile_group, tile_index: device copies of dap_shared_map's output.  An entry out
- *                 of range leaves its tile or sequence out (DAP_DEVERR_QMAP; a zero row).
+ *   seq_group, tiles  device copies of dap_shared_map's output (tiles 16-byte aligned; seq_group is not read
+ *                 when num_groups is 1).  A sequence whose group is out of range gives a zero row, a tile out of
+ *                 range leaves its sequences' results undefined; both set DAP_DEVERR_QMAP.
  *   max_prefix_len, max_suffix_len  host: upper bounds of prefix_lens[g] and seq_lens[b] - prefix_lens[g].
  *   prefix_splits, suffix_splits    0: the planner's (dap_shared_prefix_splits(SMs, num_tiles, Hkv,
  *                 max_prefix_len); dap_resolve_splits(0, SMs, B, Hq, Hkv, D, page_size, max_suffix_len, 0));
@@ -426,9 +427,7 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
                                     const void *k_cache, const void *v_cache, int num_pages,
                                     int page_size, const int32_t *block_table, int max_pages,
                                     const int32_t *seq_lens, const int32_t *prefix_lens,
-                                    const int32_t *group_indptr, const int32_t *seq_group,
-                                    const int32_t *tile_group, const int32_t *tile_index,
-                                    int num_groups, int num_tiles, int seqs_per_tile,
+                                    const int32_t *seq_group, const int32_t *tiles, int num_groups, int num_tiles, int seqs_per_tile,
                                     int max_prefix_len, int max_suffix_len, int B, int Hq, int Hkv,
                                     int D, float scale, int prefix_splits, int suffix_splits,
                                     void *workspace, size_t workspace_bytes, void *out,

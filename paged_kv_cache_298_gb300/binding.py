@@ -133,13 +133,13 @@ def load(build_if_missing: bool = True):
         lib.kv_read_paged_fp8.restype = I
         lib.dap_shared_seqs_per_tile.argtypes = [I, I, I]
         lib.dap_shared_seqs_per_tile.restype = I
-        lib.dap_shared_map.argtypes = [P, I, I, P, P, P, P, I]
+        lib.dap_shared_map.argtypes = [P, I, I, P, P, I]
         lib.dap_shared_map.restype = I
         lib.dap_shared_prefix_splits.argtypes = [I, I, I, I]
         lib.dap_shared_prefix_splits.restype = I
         lib.dap_workspace_bytes_shared.argtypes = [I, I, I, I, I]
         lib.dap_workspace_bytes_shared.restype = SZ
-        lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I,
+        lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I,
                                                  F, I, I, P, SZ, P, LL, LL, P]
         lib.decode_attn_paged_shared.restype = I
         lib.dap_set_trace_events.argtypes = [P, P, P]
@@ -636,14 +636,12 @@ class SharedPlan:
         _need(sizes.numel() > 0 and int(sizes.min()) >= 0, "group_sizes must be one or more counts >= 0")
         self.B, self.num_groups = int(sizes.sum(dtype=torch.int64)), sizes.numel()
         cap = sum(-(-n // self.seqs_per_tile) for n in sizes.tolist())
-        host = torch.zeros(self.num_groups + 1 + self.B + 2 * cap, dtype=torch.int32)
-        parts = host.split([self.num_groups + 1, self.B, cap, cap])
-        self.num_tiles = lib.dap_shared_map(_ptr(sizes), self.num_groups, self.seqs_per_tile, *(_ptr(x) for x in parts),
-                                            cap)
+        host = torch.zeros(4 * cap + self.B, dtype=torch.int32)
+        self.num_tiles = lib.dap_shared_map(_ptr(sizes), self.num_groups, self.seqs_per_tile, _ptr(host[4 * cap:]),
+                                            _ptr(host), cap)
         _need(self.num_tiles == cap, "invalid group_sizes")
-        self.map = host.to(device)   # group_indptr, seq_group, tile_group and tile_index, back to back
-        self.group_indptr, self.seq_group, self.tile_group, self.tile_index = \
-            self.map.split([self.num_groups + 1, self.B, cap, cap])
+        self.map = host.to(device)   # the tiles, then the sequences' groups
+        self.tiles, self.seq_group = self.map[:4 * cap].view(cap, 4), self.map[4 * cap:]
         self.sizes = (self.B, self.Hq, self.Hkv, self.D, self.num_groups, self.num_tiles, self.seqs_per_tile)
         self._last = (None, None)
 

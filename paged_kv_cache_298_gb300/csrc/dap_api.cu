@@ -506,13 +506,25 @@ int dap_shared_seqs_per_tile(int Hq, int Hkv, int D) {
     return (D == 256 ? 128 : 256) / (Hq / Hkv);
 }
 
-int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *group_indptr,
-                   int32_t *seq_group, int32_t *tile_group, int32_t *tile_index, int max_tiles) {
-    const int n = dap_q_tile_map(group_sizes, num_groups, seqs_per_tile, group_indptr, tile_group, tile_index, max_tiles);
-    if (n > 0 && !seq_group) return -1;
-    if (n > 0)
-        for (int g = 0; g < num_groups; ++g)
-            for (int b = group_indptr[g]; b < group_indptr[g + 1]; ++b) seq_group[b] = g;
+int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *seq_group, int32_t *tiles,
+                   int max_tiles) {
+    if (num_groups < 0 || seqs_per_tile < 1 || max_tiles < 0 || (num_groups > 0 && !group_sizes)) return -1;
+    long long first = 0;
+    int n = 0;
+    for (int g = 0; g < num_groups; ++g) {
+        const int size = group_sizes[g];
+        if (size < 0 || first + size > 0x7FFFFFFFLL || (size > 0 && (!seq_group || !tiles))) return -1;
+        for (int i = 0; i < size; ++i) seq_group[first + i] = g;
+        for (long long i = 0; i < size; i += seqs_per_tile) {
+            if (n >= max_tiles) return -1;
+            tiles[4 * n] = g;
+            tiles[4 * n + 1] = (int32_t)first;
+            tiles[4 * n + 2] = (int32_t)(first + i);
+            tiles[4 * n + 3] = (int32_t)std::min<long long>(seqs_per_tile, size - i);
+            ++n;
+        }
+        first += size;
+    }
     return n;
 }
 
@@ -544,9 +556,7 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
 dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long long q_stride_h, const void *k_cache,
                                     const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
                                     int max_pages, const int32_t *seq_lens, const int32_t *prefix_lens,
-                                    const int32_t *group_indptr, const int32_t *seq_group,
-                                    const int32_t *tile_group, const int32_t *tile_index, int num_groups,
-                                    int num_tiles, int seqs_per_tile, int max_prefix_len, int max_suffix_len, int B,
+                                    const int32_t *seq_group, const int32_t *tiles, int num_groups, int num_tiles, int seqs_per_tile, int max_prefix_len, int max_suffix_len, int B,
                                     int Hq, int Hkv, int D, float scale, int prefix_splits, int suffix_splits,
                                     void *workspace, size_t workspace_bytes, void *out, long long out_stride_b,
                                     long long out_stride_h, void *stream) {
@@ -561,14 +571,12 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
         (long long)max_suffix_len > (long long)max_pages * page_size || num_groups < 1 || num_tiles < 1 ||
         num_tiles > B)
         return DAP_ERR_SHAPE;
-    if (!k_cache || !v_cache || !block_table || !prefix_lens || !group_indptr || !seq_group || !tile_group ||
-        !tile_index)
-        return DAP_ERR_NULL;
+    if (!k_cache || !v_cache || !block_table || !prefix_lens || !seq_group || !tiles) return DAP_ERR_NULL;
     const int per_tile = dap_shared_seqs_per_tile(Hq, Hkv, D);
     if (per_tile == 0) return DAP_ERR_UNSUPPORTED;
     if (seqs_per_tile != per_tile) return DAP_ERR_SHAPE;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(prefix_lens) ||
-        !aligned4(group_indptr) || !aligned4(seq_group) || !aligned4(tile_group) || !aligned4(tile_index))
+        !aligned4(seq_group) || !aligned16(tiles))
         return DAP_ERR_ALIGN;
     // every row ends in the combine; a part whose bound is 0 has no splits
     if (max_prefix_len == 0) {
@@ -602,10 +610,8 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
     a.max_pages = max_pages;
     a.seq_lens = seq_lens;
     a.prefix_lens = prefix_lens;
-    a.group_indptr = group_indptr;
     a.seq_group = seq_group;
-    a.tile_group = tile_group;
-    a.tile_index = tile_index;
+    a.tiles = tiles;
     a.num_groups = num_groups;
     a.num_tiles = num_tiles;
     a.seqs_per_tile = seqs_per_tile;

@@ -120,7 +120,7 @@ struct SharedArgs {
     const int32_t *block_table;
     int max_pages;
     const int32_t *seq_lens, *prefix_lens;
-    const int32_t *group_indptr, *seq_group, *tile_group, *tile_index;
+    const int32_t *seq_group, *tiles;
     int num_groups, num_tiles, seqs_per_tile;
     int max_prefix_len, max_suffix_len;
     int B, Hq, Hkv, D;

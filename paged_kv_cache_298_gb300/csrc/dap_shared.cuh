@@ -21,7 +21,7 @@ namespace dap {
 
 struct SharedParams {
     SplitParams sp;  // q, caches, table, lengths, sizes, out; num_splits / chunk are the suffix's
-    const int32_t *prefix_lens, *group_indptr, *seq_group, *tile_group, *tile_index;
+    const int32_t *prefix_lens, *seq_group, *tiles;
     int num_groups, num_tiles, seqs_per_tile, max_prefix_len, max_suffix_len;
     int prefix_splits, prefix_chunk, total_splits;
     float *o_part, *ml_part;
@@ -38,7 +38,8 @@ struct Span {
     int P, L;
 };
 __device__ __forceinline__ Span seq_span(const SharedParams &p, int b, unsigned int *flags) {
-    const int g = __ldg(p.seq_group + b), Lraw = __ldg(p.sp.seq_lens + b);
+    // (with one group its number need not be read)
+    const int g = p.num_groups == 1 ? 0 : __ldg(p.seq_group + b), Lraw = __ldg(p.sp.seq_lens + b);
     if (g < 0 || g >= p.num_groups) {
         *flags |= DAP_DEVERR_QMAP;
         return {0, 0};
@@ -245,10 +246,8 @@ inline SharedParams shared_params(const SharedArgs &a, int box_rows) {
     s.o_sb = a.o_sb;
     s.o_sh = a.o_sh;
     p.prefix_lens = a.prefix_lens;
-    p.group_indptr = a.group_indptr;
     p.seq_group = a.seq_group;
-    p.tile_group = a.tile_group;
-    p.tile_index = a.tile_index;
+    p.tiles = a.tiles;
     p.num_groups = a.num_groups;
     p.num_tiles = a.num_tiles;
     p.seqs_per_tile = a.seqs_per_tile;

@@ -11,10 +11,14 @@
 //   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
 //                                  P (bf16 pairs) overwrites the first 32 once they are read;
 //                               O  columns [256 + x D, + D)  fp32 accumulator.
-// Warps: four softmax warps a stream (thread = row), a producer, and a warp a stream that issues its products:
-// S(n + 2) as soon as the product with P(n), whose place it takes, is done, so the scores of the next tile
-// are there when the softmax of this one ends.  (With one score buffer a stream, and q in tensor memory
-// instead, a 64-key tile took 3130 cycles: every step of the chain S, softmax, PV waited for the last.)
+// Warps: four softmax warps a stream (thread = row), a producer, one that issues the scores of both streams in
+// turn and one that issues their products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the
+// scores are there when the softmax gets to them, and neither issuing warp waits for the other's step.
+// (Measured, D = 128, cycles of a 64-key tile of 256 rows, whose products take 1344: one score buffer a stream,
+// every step of the chain S, softmax, PV waiting for the last: 3130; two buffers and an issuing warp for each
+// stream: 2100, as PV(n) has to end before the same warp can go on to S(n + 2); one warp for everything in the
+// order PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as a wait on a barrier takes 60 cycles even when it is
+// complete and a commit 55, all of them in line.)
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
 // when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
 // weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
@@ -33,7 +37,7 @@ struct PrefixCfg {
     static constexpr int TILE_BYTES = BT * ROWB;              // K or V of one tile
     static constexpr int NSTREAM = D == 256 ? 1 : 2;
     static constexpr int NS = D == 64 ? 6 : D == 128 ? 3 : 2;  // K/V tiles in the ring
-    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 1 + NSTREAM) * 32;
+    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 3) * 32;
     static constexpr int TO = 256, TMEM_COLS = 512;
     static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
     static constexpr int RING_OFF = Q_BYTES, BAR_OFF = RING_OFF + NS * 2 * TILE_BYTES;
@@ -44,9 +48,9 @@ struct PrefixCfg {
     // more than half an SM's shared memory, so that two prefix CTAs never share an SM (the second would wait for
     // tensor memory); at D <= 128 one suffix CTA fits beside the one there is
     static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
-    static constexpr int MRG_STRIDE = D + 4;  // floats of a row in the streams' merge
+    static constexpr int ROW_F = D + 4;  // floats of a row of sums on its way out (the 4: no bank conflicts)
     static_assert(SMEM <= (D == 256 ? 227 : 164) * 1024, "shared memory");
-    static_assert(NSTREAM == 1 || 128 * MRG_STRIDE * 4 <= NS * 2 * TILE_BYTES, "the merge fits the ring");
+    static_assert(NSTREAM * 128 * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
 // (the bound of 512 threads holds the registers at 128, which leaves room for a suffix CTA's warps)
@@ -92,19 +96,17 @@ __global__ void __launch_bounds__(512, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int g = __ldg(pp.tile_group + w), wi = __ldg(pp.tile_index + w);
-    int first = 0, nseq = 0, q0 = 0, P = 0;
-    if (g >= 0 && g < pp.num_groups && wi >= 0) {
-        q0 = __ldg(pp.group_indptr + g);
-        const int q1 = __ldg(pp.group_indptr + g + 1);
-        P = group_prefix(pp, g);
-        const long long f = q0 + (long long)wi * pp.seqs_per_tile;
-        if (q0 >= 0 && q1 <= p.B && f < q1) {
-            first = (int)f;
-            nseq = min(pp.seqs_per_tile, q1 - first);
-        }
+    // (group, first sequence of the group, first sequence of the tile, sequences)
+    const int4 tl = __ldg(reinterpret_cast<const int4 *>(pp.tiles) + w);
+    const int q0 = tl.y, first = tl.z;
+    int nseq = 0, P = 0;
+    if (tl.x >= 0 && tl.x < pp.num_groups && q0 >= 0 && q0 < p.B && first >= 0 && tl.w >= 1 &&
+        tl.w <= pp.seqs_per_tile && tl.w <= p.B - first) {
+        nseq = tl.w;
+        P = group_prefix(pp, tl.x);
+    } else if (threadIdx.x == 0 && s == 0 && kvh == 0) {
+        flag_error(DAP_DEVERR_QMAP);
     }
-    if (nseq == 0 && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
     const int nrows = nseq * G;
     const int tok0 = min(P, s * pp.prefix_chunk), tok1 = min(P, tok0 + pp.prefix_chunk);
     const int J = (tok1 - tok0 + BT - 1) / BT;  // K/V tiles of this CTA
@@ -118,8 +120,8 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < NS; ++i) {
             mbar_init(&k_full[i], full_arrivals<C>());
             mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
-            mbar_init(&v_empty[i], both ? 2 : 1);
+            mbar_init(&k_empty[i], 1);  // a commit after the last product that reads the tile
+            mbar_init(&v_empty[i], 1);
         }
         for (int e = 0; e < 4; ++e) {
             mbar_init(&s_done[e], 1);
@@ -236,47 +238,70 @@ __global__ void __launch_bounds__(512, 1)
             }
         }
     } else if (work && warp >= C::ISSUER) {
-        const int x = warp - C::ISSUER;  // the stream whose products this warp issues
-        if (lane == 0) {
-            const int N = tiles_of(x);
-            const uint32_t sQ = smem_addr(smem) + (both ? x * C::NBLK * C::QBLK : 0);
-            const uint32_t tO = tmem + C::TO + x * D;
-            auto scores = [&](int n) -> bool {
-                const int j = tile_at(x, n), st = j % NS, e = 2 * x + (n & 1);
-                // (the scores take the place of P(n - 2) once the product that reads it is done)
-                if (!mbar_wait(&k_full[st], (j / NS) & 1) || (n >= 2 && !mbar_wait(&pv_done[e], ((n - 2) >> 1) & 1)))
-                    return false;
-                if (C::GATHER) fence_async_smem();  // (the tile's rows were copied by the generic proxy)
-                tc_fence_after();
-                const uint32_t sK = smem_addr(ring + st * 2 * C::TILE_BYTES), tS = tmem + 64 * e;
+        // The whole warp runs its loop with values that are the same in every lane (and known to be), one lane
+        // issues: descriptors then stay in uniform registers.  Two barriers are polled at a time, each by half the
+        // lanes.
+        auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        const bool pv = same(warp - C::ISSUER) != 0;
+        const int Ju = same(J), last = same(nlast);
+        const bool two = same(both) != 0, tailed = same(ragged) != 0;
+        const uint32_t tm = same(tmem);
+        const int step = two || C::NSTREAM == 1 ? 1 : 2;  // tile n of stream x is step * n + (step == 2 ? x : 0)
+        const uint32_t sQ = smem_addr(smem), sR = smem_addr(ring);
+        auto wait = [&](uint64_t *b0, int n0, uint64_t *b1, int n1) -> bool {
+            const bool odd = lane & 1;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(odd ? b1 : b0, (odd ? n1 : n0) & 1)) != 0;
+            if (C::GATHER) fence_async_smem();  // (K and V rows were copied by the generic proxy)
+            tc_fence_after();
+            return ok;
+        };
+        auto scores = [&](int x, int n) -> bool {
+            const int j = step * n + (step == 2 ? x : 0), st = j % NS, e = 2 * x + (n & 1);
+            uint64_t *k = &k_full[st];
+            if (!(n >= 2 ? wait(k, j / NS, &pv_done[e], (n - 2) >> 1) : wait(k, j / NS, q_full, 0))) return false;
+            const uint64_t dQ = sw128_desc(sQ + (two ? x * C::NBLK * C::QBLK : 0), 16, 1024);
+            const uint64_t dK = sw128_desc(sR + st * 2 * C::TILE_BYTES, 16, 1024);
+            const uint32_t tS = tm + 64 * e;
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    umma_bf16(tS, sw128_desc(sQ + (k >> 2) * C::QBLK + (k & 3) * 32, 16, 1024),
-                              sw128_desc(sK + (k >> 2) * CS + (k & 3) * 32, 16, 1024), idS, k > 0);
+                for (int i = 0; i < D / 16; ++i)
+                    umma_bf16(tS, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
+                              dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
                 umma_commit(&s_done[e]);
-                umma_commit(&k_empty[st]);
-                return true;
-            };
-            bool ok = N == 0 || (mbar_wait(q_full, 0) && scores(0) && (N == 1 || scores(1)));
-            for (int n = 0; ok && n < N; ++n) {
-                const int j = tile_at(x, n), st = j % NS, e = 2 * x + (n & 1);
-                ok = mbar_wait(&p_ready[e], (n >> 1) & 1) && (C::GATHER || mbar_wait(&v_full[st], (j / NS) & 1)) &&
-                     (!(ragged && j == J - 1) || mbar_wait(tail, 0));
-                if (!ok) break;
-                tc_fence_after();
-                const int nv = j == J - 1 ? nlast : BT;
-                const uint32_t sV = smem_addr(ring + (st * 2 + 1) * C::TILE_BYTES), tP = tmem + 64 * e;
-#pragma unroll
-                for (int k = 0; k < BT / 16; ++k)
-                    if (k * 16 < nv)
-                        umma_bf16_tmem_a(tO, tP + k * 8, sw128_desc(sV + k * 2048, CS, 1024), idO, n > 0 || k > 0);
-                umma_commit(&pv_done[e]);
-                umma_commit(&v_empty[st]);
-                if (n + 2 < N) ok = scores(n + 2);
+                if (!two || x == 1) umma_commit(&k_empty[st]);  // (a commit covers all products before it)
             }
-            if (!ok) misc[2] = 1;
-            umma_commit(&fin[x]);  // this thread's products are done when it completes
+            __syncwarp();
+            return true;
+        };
+        auto values = [&](int x, int n) -> bool {
+            const int j = step * n + (step == 2 ? x : 0), st = j % NS, e = 2 * x + (n & 1);
+            const bool end = j == Ju - 1;
+            uint64_t *landed = C::GATHER ? &k_full[st] : &v_full[st];
+            if (!(end && tailed ? wait(&p_ready[e], n >> 1, tail, 0) : wait(&p_ready[e], n >> 1, landed, j / NS)))
+                return false;
+            const int nv = end ? last : BT;
+            const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, CS, 1024);
+            const uint32_t tP = tm + 64 * e, tOx = tm + C::TO + x * D;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < BT / 16; ++i)
+                    if (i * 16 < nv)
+                        umma_bf16_tmem_a(tOx, tP + i * 8, dV + ((i * 2048) >> 4), idO, n > 0 || i > 0);
+                umma_commit(&pv_done[e]);
+                if (!two || x == 1) umma_commit(&v_empty[st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        const int N0 = (Ju + step - 1) / step, N1 = C::NSTREAM == 1 ? 0 : Ju / step;
+        bool ok = true;
+        if (pv) {
+            for (int n = 0; ok && n < N0; ++n) ok = values(0, n) && (n >= N1 || values(1, n));
+        } else {
+            for (int n = 0; ok && n < N0; ++n) ok = scores(0, n) && (n >= N1 || scores(1, n));
         }
+        if (!ok && lane == 0) misc[2] = 1;
+        if (elect_one()) umma_commit(&fin[pv ? 1 : 0]);  // this warp's products are done when it completes
         __syncwarp();
     }
 
@@ -383,16 +408,14 @@ __global__ void __launch_bounds__(512, 1)
     }
     __syncthreads();
     if (soft) {
-        // every product is done once the fin barriers have completed
-        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && (C::NSTREAM == 1 || mbar_wait(&fin[1], 0)));
+        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0));
         tc_fence_after();
         const bool good = done && misc[2] == 0;
-        float *mrg = reinterpret_cast<float *>(ring);
-        float other = 0.f;  // weight of stream 1's sums at the merge
-        const bool merge = C::NSTREAM == 2 && !both;
+        // q and the ring are idle now: the sums leave through them, a row a thread in, a row a warp out (a thread
+        // that wrote its row to global memory touched 32 lines with every store of the warp: 11,000 cycles)
+        float *mine = reinterpret_cast<float *>(smem) + (x * 128 + r) * C::ROW_F;
+        const bool merge = C::NSTREAM == 2 && !both;  // both streams hold the same rows: stream 0 adds stream 1's
         if (merge) {
-            // both streams hold the same rows: stream 1 leaves its sums in the (now idle) stage ring
-            float *mr = mrg + r * C::MRG_STRIDE;
             if (x == 1 && active && good) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -400,23 +423,23 @@ __global__ void __launch_bounds__(512, 1)
                     if (N > 0) tmem_ld32(tO + c, o);
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4 *>(mr + c + k) =
+                        *reinterpret_cast<float4 *>(mine + c + k) =
                             N > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-                *reinterpret_cast<float2 *>(mr + D) = make_float2(m_ref, l);
+                *reinterpret_cast<float2 *>(mine + D) = make_float2(m_ref, l);
             }
             named_sync(1, C::NWS * 32);
         }
         if ((x == 0 || !merge) && active && good) {
-            const float *mr = mrg + r * C::MRG_STRIDE;
-            float mine = 1.f;
+            const float *other = mine + 128 * C::ROW_F;
+            float f0 = 1.f, f1 = 0.f;
             if (merge) {
-                const float2 ml = *reinterpret_cast<const float2 *>(mr + D);
+                const float2 ml = *reinterpret_cast<const float2 *>(other + D);
                 const float m = fmaxf(m_ref, ml.x), mu = m == -INFINITY ? 0.f : m;
-                mine = ex2(m_ref - mu);
-                other = ex2(ml.x - mu);
+                f0 = ex2(m_ref - mu);
+                f1 = ex2(ml.x - mu);
                 m_ref = m;
-                l = l * mine + ml.y * other;
+                l = l * f0 + ml.y * f1;
             }
             const long long prow = ((long long)seq * pp.total_splits + s) * p.Hq + hq;
 #pragma unroll 1
@@ -426,21 +449,28 @@ __global__ void __launch_bounds__(512, 1)
                 if (merge) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(mr + c + k);
-                        o[k] = o[k] * mine + v.x * other;
-                        o[k + 1] = o[k + 1] * mine + v.y * other;
-                        o[k + 2] = o[k + 2] * mine + v.z * other;
-                        o[k + 3] = o[k + 3] * mine + v.w * other;
+                        const float4 v = *reinterpret_cast<const float4 *>(other + c + k);
+                        o[k] = o[k] * f0 + v.x * f1;
+                        o[k + 1] = o[k + 1] * f0 + v.y * f1;
+                        o[k + 2] = o[k + 2] * f0 + v.z * f1;
+                        o[k + 3] = o[k + 3] * f0 + v.w * f1;
                     }
                 }
-                if (rvalid) {
-                    float *dst = pp.o_part + prow * D + c;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4 *>(dst + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                }
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<float4 *>(mine + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
             if (rvalid) *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
+            __syncwarp();
+            const float *rows = mine - lane * C::ROW_F;
+            const int cnt = min(32, nx - (warp & 3) * 32);
+#pragma unroll 4
+            for (int i = 0; i < cnt; ++i) {
+                float *dst = pp.o_part + __shfl_sync(0xFFFFFFFFu, prow, i) * D;
+#pragma unroll
+                for (int c = lane * 4; c < D; c += 128)
+                    *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(rows + i * C::ROW_F + c);
+            }
         }
         if (threadIdx.x == 0 && misc[2]) {
             // a wait gave up: the copies still in flight land (bounded) before the shared memory goes

@@ -209,8 +209,7 @@ PyObject *read_runs(PyObject *const *a) {
     return both;
 }
 
-// decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, the plan's map [group_indptr, seq_group,
-// tile_group, tile_index back to back], (B, Hq, Hkv, D, groups, tiles, seqs_per_tile), max_prefix_len,
+// decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, the plan's map [tiles, then seq_group], (B, Hq, Hkv, D, groups, tiles, seqs_per_tile), max_prefix_len,
 // max_suffix_len, (prefix_splits, suffix_splits), scale, workspace, out, stream) -> out
 PyObject *decode_shared(PyObject *const *a) {
     const char *what = "decode_attn_paged_shared";
@@ -222,7 +221,7 @@ PyObject *decode_shared(PyObject *const *a) {
     int d[7];
     for (int i = 0; i < 7; ++i) d[i] = integer32(PyTuple_GET_ITEM(a[7], i));
     const int B = d[0], Hq = d[1], Hkv = d[2], D = d[3], groups = d[4], tiles = d[5];
-    if (!int32s(map) || map.numel() != (int64_t)groups + 1 + B + 2 * (int64_t)tiles)
+    if (!int32s(map) || map.numel() != 4 * (int64_t)tiles + B)
         value_error("the plan's map does not fit its sizes");
     rows3(q, "q must be a bf16 [*, *, D] tensor with unit stride in D");
     if (q.size(0) != B || q.size(1) != Hq || q.size(2) != D)
@@ -258,7 +257,7 @@ PyObject *decode_shared(PyObject *const *a) {
         q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), fit(k.size(0), "too many pages"),
         fit(k.size(1), "page size too large"), static_cast<const int32_t *>(bt.data_ptr()),
         fit(bt.size(1), "block_table too wide"), static_cast<const int32_t *>(sl.data_ptr()),
-        static_cast<const int32_t *>(pl.data_ptr()), m, m + groups + 1, m + groups + 1 + B, m + groups + 1 + B + tiles,
+        static_cast<const int32_t *>(pl.data_ptr()), m + 4 * (int64_t)tiles, m,
         groups, tiles, d[6], max_prefix, max_suffix, B, Hq, Hkv, D, (float)scale, pre, suf, ws.data_ptr(), ws.nbytes(),
         out.data_ptr(), out.stride(0), out.stride(1), stream);
     Py_END_ALLOW_THREADS;

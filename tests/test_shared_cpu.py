@@ -15,12 +15,12 @@ NULL, SHAPE, UNSUPPORTED, WORKSPACE, ALIGN = 1, 2, 3, 4, 5
 
 def call(**kw):
     a = dict(q=FAKE, qsb=32 * 128, qsh=128, k=FAKE, v=FAKE, P=64, ps=16, table=FAKE, maxp=64, lens=FAKE, plens=FAKE,
-             gi=FAKE, sg=FAKE, tg=FAKE, ti=FAKE, groups=1, tiles=1, spt=64, maxpre=500, maxsuf=100, B=4, Hq=32, Hkv=8, D=128,
+             sg=FAKE, tl=FAKE, groups=1, tiles=1, spt=64, maxpre=500, maxsuf=100, B=4, Hq=32, Hkv=8, D=128,
              scale=0.1, pre=2, suf=1, ws=None, wsb=0, out=FAKE, osb=32 * 128, osh=128)
     a.update(kw)
     return binding.load().decode_attn_paged_shared(
-        a["q"], a["qsb"], a["qsh"], a["k"], a["v"], a["P"], a["ps"], a["table"], a["maxp"], a["lens"], a["plens"], a["gi"],
-        a["sg"], a["tg"], a["ti"], a["groups"], a["tiles"], a["spt"], a["maxpre"], a["maxsuf"], a["B"], a["Hq"], a["Hkv"],
+        a["q"], a["qsb"], a["qsh"], a["k"], a["v"], a["P"], a["ps"], a["table"], a["maxp"], a["lens"], a["plens"],
+        a["sg"], a["tl"], a["groups"], a["tiles"], a["spt"], a["maxpre"], a["maxsuf"], a["B"], a["Hq"], a["Hkv"],
         a["D"], a["scale"], a["pre"], a["suf"], a["ws"], a["wsb"], a["out"], a["osb"], a["osh"], None)
 
 
@@ -34,10 +34,10 @@ def call(**kw):
     (dict(D=32, qsb=1024, qsh=32), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(Hq=24), UNSUPPORTED),
     (dict(Hq=128, spt=16), UNSUPPORTED),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(table=None), NULL), (dict(lens=None), NULL),
-    (dict(plens=None), NULL), (dict(gi=None), NULL), (dict(sg=None), NULL), (dict(tg=None), NULL), (dict(ti=None), NULL),
+    (dict(plens=None), NULL), (dict(sg=None), NULL), (dict(tl=None), NULL),
     (dict(out=None), NULL),
     (dict(q=ODD), ALIGN), (dict(k=ODD), ALIGN), (dict(out=ODD), ALIGN), (dict(table=ODD), ALIGN), (dict(plens=ODD), ALIGN),
-    (dict(gi=ODD), ALIGN), (dict(sg=ODD), ALIGN), (dict(tg=ODD), ALIGN), (dict(ti=ODD), ALIGN), (dict(qsh=132), ALIGN),
+    (dict(sg=ODD), ALIGN), (dict(tl=ODD), ALIGN), (dict(tl=ctypes.c_void_p((1 << 20) + 4)), ALIGN), (dict(qsh=132), ALIGN),
     (dict(osb=4100), ALIGN),
     (dict(), WORKSPACE), (dict(ws=FAKE, wsb=1000), WORKSPACE), (dict(ws=ODD, wsb=1 << 30), WORKSPACE),
 ])
@@ -53,12 +53,12 @@ def test_map_covers_every_sequence_once():
     for sizes in ([1], [64], [65], [3, 0, 200, 1], [0, 5], [128, 128]):
         plan = binding.SharedPlan(sizes, 32, 8, 128, "cpu")
         assert plan.seqs_per_tile == 64 and plan.B == sum(sizes)
-        assert plan.group_indptr.tolist() == [0] + list(np.cumsum(sizes))
         assert plan.seq_group.tolist() == [g for g, n in enumerate(sizes) for _ in range(n)]
+        starts = [0] + list(np.cumsum(sizes))
         seen = []
-        for g, i in zip(plan.tile_group.tolist(), plan.tile_index.tolist()):
-            a, b = plan.group_indptr[g] + 64 * i, plan.group_indptr[g + 1]
-            seen += list(range(int(a), int(min(a + 64, b))))
+        for g, q0, a, n in plan.tiles.tolist():
+            assert q0 == starts[g] and 1 <= n <= 64 and (a - q0) % 64 == 0 and a + n <= starts[g + 1]
+            seen += list(range(a, a + n))
         assert seen == list(range(sum(sizes)))
 
 
@@ -70,8 +70,12 @@ def test_plan_refuses():
     assert binding.load().dap_shared_seqs_per_tile(8, 8, 64) == 256
     # the map without room for its tiles
     n = torch.tensor([100], dtype=torch.int32)
-    out = [torch.zeros(200, dtype=torch.int32) for _ in range(4)]
-    assert binding.load().dap_shared_map(n.data_ptr(), 1, 64, *(t.data_ptr() for t in out), 1) == -1
+    out = [torch.zeros(200, dtype=torch.int32) for _ in range(2)]
+    f = binding.load().dap_shared_map
+    assert f(n.data_ptr(), 1, 64, out[0].data_ptr(), out[1].data_ptr(), 1) == -1
+    assert f(n.data_ptr(), 1, 64, out[0].data_ptr(), out[1].data_ptr(), 2) == 2
+    assert f(n.data_ptr(), 1, 0, out[0].data_ptr(), out[1].data_ptr(), 200) == -1
+    assert f(n.data_ptr(), 1, 64, None, out[1].data_ptr(), 2) == -1 and f(None, 1, 64, out[0].data_ptr(), out[1].data_ptr(), 2) == -1
 
 
 def test_prefix_splits_fill_the_device_and_cover_the_prefix():

@@ -75,7 +75,7 @@ class Case:
         """(out, A) in 64 bits."""
         out = torch.zeros((self.B, self.Hq, self.D), dtype=torch.float64, device="cuda")
         A = torch.zeros_like(out)
-        starts = self.plan.group_indptr.tolist()
+        starts = [sum(self.sizes[:i]) for i in range(len(self.sizes))]
         for b, n in enumerate(self.lens.tolist()):
             P = int(self.prefix[self.group[b]])
             if n == 0 or n < P:
@@ -237,11 +237,14 @@ def test_bad_lengths_groups_and_pages_are_flagged():
     assert bool((out[4:6] == 0).all())
     c.check(out, ref, rows=[0, 1, 2, 3, 6, 7, 8, 9, 10, 11])
     c.plan.seq_group.copy_(sg)
-    tg = c.plan.tile_group.clone()
-    c.plan.tile_group[1] = 5
-    c.run()
-    assert binding.get_device_errors() & binding.DEVERR_QMAP
-    c.plan.tile_group.copy_(tg)
+    tiles = c.plan.tiles.clone()
+    for at, bad in (((1, 0), 5), ((1, 0), -1), ((1, 1), 12), ((0, 2), -1), ((1, 2), 11), ((0, 3), 65), ((0, 3), 0)):
+        c.plan.tiles[at] = bad
+        c.run()
+        assert binding.get_device_errors() & binding.DEVERR_QMAP, (at, bad)
+        c.plan.tiles.copy_(tiles)
+    c.check(c.run(), ref)
+    assert binding.get_device_errors() == 0
     # pages outside the pool: read as page 0, and flagged; the other sequences keep their results
     c.table[6, 13] = c.k.shape[0]
     c.k[0], c.v[0] = torch.nan_to_num(c.k[0]), torch.nan_to_num(c.v[0])
