@@ -7,18 +7,23 @@
 // tile; with at most 128 rows both streams hold the same rows and take every other K/V tile, merged through
 // shared memory at the end.
 //   shared memory: q (128-byte swizzled, one TMA copy per 64 dims of 128 rows), a ring of K/V tiles of 64
-//                  keys, column block major as in dap_multi_tc.cu (TMA boxes or row gather);
+//                  keys.  K tiles are column block major, [D / 64][64 keys][128 bytes], as the product with
+//                  N = 64 keys wants its 8-key groups one stride apart: a copy per page run and column block (one in
+//                  all for page sizes that are multiples of 64).  V tiles are made of one box per page run,
+//                  [D / 64][R keys][128 bytes], since a product takes 16 keys of V at a time: half the copies, each
+//                  of which costs the TMA unit about 80 cycles beside one per 128 bytes (16 copies of a tile at a
+//                  page size of 16: 1600 cycles).  Row gather: both column block major;
 //   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
 //                                  P (bf16 pairs) overwrites the first 32 once they are read;
 //                               O  columns [256 + x D, + D)  fp32 accumulator.
-// Warps: four softmax warps a stream (thread = row), a producer, one that issues the scores of both streams in
-// turn and one that issues their products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the
-// scores are there when the softmax gets to them, and neither issuing warp waits for the other's step.
+// Warps: four softmax warps a stream (thread = row), a producer, one a stream that issues its scores and one that
+// issues the products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores are there when the
+// softmax gets to them.
 // (Measured, D = 128, cycles of a 64-key tile of 256 rows, whose products take 1344: one score buffer a stream,
-// every step of the chain S, softmax, PV waiting for the last: 3130; two buffers and an issuing warp for each
-// stream: 2100, as PV(n) has to end before the same warp can go on to S(n + 2); one warp for everything in the
-// order PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as a wait on a barrier takes 60 cycles even when it is
-// complete and a commit 55, all of them in line.)
+// every step of the chain S, softmax, PV waiting for the last: 3130; two buffers and one issuing warp a stream:
+// 2100, as PV(n) has to end before the same warp can go on to S(n + 2); one warp for everything in the order
+// PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as a wait on a barrier takes 60 cycles even when it is
+// complete and a commit 55, all of them in line; one warp for all scores: 2100, the same again.)
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
 // when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
 // weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
@@ -37,12 +42,13 @@ struct PrefixCfg {
     static constexpr int TILE_BYTES = BT * ROWB;              // K or V of one tile
     static constexpr int NSTREAM = D == 256 ? 1 : 2;
     static constexpr int NS = D == 64 ? 6 : D == 128 ? 3 : 2;  // K/V tiles in the ring
-    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, THREADS = (NWS + 3) * 32;
+    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, PV = ISSUER + NSTREAM,
+                         THREADS = (PV + 1) * 32;
     static constexpr int TO = 256, TMEM_COLS = 512;
     static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
     static constexpr int RING_OFF = Q_BYTES, BAR_OFF = RING_OFF + NS * 2 * TILE_BYTES;
-    // barriers: k_full, k_empty, v_full, v_empty [NS], s_done, p_ready, pv_done [stream][buffer], q_full, fin[2], tail
-    static constexpr int NBAR = 4 * NS + 16;
+    // barriers: k_full, k_empty, v_full, v_empty [NS], s_done, p_ready, pv_done [stream][buffer], q_full, fin[3], tail
+    static constexpr int NBAR = 4 * NS + 17;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr int USED = MISC_OFF + 32 + 1024;  // + slack to align the base to 1024
     // more than half an SM's shared memory, so that two prefix CTAs never share an SM (the second would wait for
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
     uint64_t *s_done = v_empty + NS, *p_ready = s_done + 4, *pv_done = p_ready + 4;  // [2 stream + buffer]
-    uint64_t *q_full = pv_done + 4, *fin = q_full + 1, *tail = fin + 2;
+    uint64_t *q_full = pv_done + 4, *fin = q_full + 1, *tail = fin + 3;
     // [0], [1] K and V tiles issued, [2] abort, [4] tensor memory
     volatile int *misc = reinterpret_cast<volatile int *>(smem + C::MISC_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
@@ -120,8 +126,8 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < NS; ++i) {
             mbar_init(&k_full[i], full_arrivals<C>());
             mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], 1);  // a commit after the last product that reads the tile
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&k_empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
+            mbar_init(&v_empty[i], 1);             // one after the last product that reads it
         }
         for (int e = 0; e < 4; ++e) {
             mbar_init(&s_done[e], 1);
@@ -129,8 +135,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&pv_done[e], 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(&fin[0], 1);
-        mbar_init(&fin[1], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
         mbar_init(tail, 1);
         misc[0] = misc[1] = misc[2] = 0;
         fence_barrier_init();
@@ -192,11 +197,12 @@ __global__ void __launch_bounds__(512, 1)
                 if (i + 1 < J) pg_next = lookup(i + 1);
                 const int t = tok0 + i * BT;
                 const int nbox = (min(BT, tok1 - t) + R - 1) / R;
-                // lane (box j, column block cb); the page of box j is in lane j
-                const int j = lane / C::NBLK, cb = lane % C::NBLK;
+                // K: lane (box j, column block cb), or whole tiles where a page has them; V: lane = box, all blocks
+                // (the page of box j is in lane j)
+                const int kb = R == BT ? 1 : C::NBLK;
+                const int j = lane / kb, cb = lane % kb;
                 const int pj = __shfl_sync(0xFFFFFFFFu, pg, j & 31);
-                const int row = (t + j * R) % p.page_size;
-                uint8_t *dst = ring + st * 2 * C::TILE_BYTES + cb * CS + j * R * 128;
+                uint8_t *dst = ring + st * 2 * C::TILE_BYTES;
                 const uint32_t bytes = (uint32_t)(nbox * R * C::ROWB);
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[st], ((i / NS) - 1) & 1))) {
                     misc[2] = 1;
@@ -204,7 +210,9 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
                 __syncwarp();
-                if (j < nbox) tma_load_5d(dst, &mapK, 0, row, cb, kvh, pj, &k_full[st]);
+                if (j < nbox)
+                    tma_load_5d(dst + cb * CS + j * R * 128, &mapK, 0, (t + j * R) % p.page_size, cb, kvh, pj,
+                                &k_full[st]);
                 ik = i + 1;
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
                     misc[2] = 1;
@@ -212,7 +220,9 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&v_full[st], bytes);
                 __syncwarp();
-                if (j < nbox) tma_load_5d(dst + C::TILE_BYTES, &mapV, 0, row, cb, kvh, pj, &v_full[st]);
+                if (lane < nbox)
+                    tma_load_5d(dst + C::TILE_BYTES + lane * R * C::ROWB, &mapV, 0, (t + lane * R) % p.page_size, 0, kvh,
+                                pg, &v_full[st]);
                 iv = i + 1;
             }
         }
@@ -228,7 +238,8 @@ __global__ void __launch_bounds__(512, 1)
                 const int nz = 16 - nlast % 16;
                 for (int e = lane; e < nz * C::NBLK * C::CPB; e += 32)
                     *reinterpret_cast<uint4 *>(ring + (st * 2 + 1) * C::TILE_BYTES +
-                                               tile_off<C>(nlast + e / (C::NBLK * C::CPB), e % (C::NBLK * C::CPB), 6)) =
+                                               tile_off<C>(nlast + e / (C::NBLK * C::CPB), e % (C::NBLK * C::CPB),
+                                                           31 - __clz(R))) =
                         make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
                 __syncwarp();
@@ -242,12 +253,18 @@ __global__ void __launch_bounds__(512, 1)
         // issues: descriptors then stay in uniform registers.  Two barriers are polled at a time, each by half the
         // lanes.
         auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-        const bool pv = same(warp - C::ISSUER) != 0;
+        const int role = same(warp - C::ISSUER);  // a stream's scores; NSTREAM: all products with V
         const int Ju = same(J), last = same(nlast);
         const bool two = same(both) != 0, tailed = same(ragged) != 0;
         const uint32_t tm = same(tmem);
         const int step = two || C::NSTREAM == 1 ? 1 : 2;  // tile n of stream x is step * n + (step == 2 ? x : 0)
         const uint32_t sQ = smem_addr(smem), sR = smem_addr(ring);
+        // A V tile is made of boxes [column block][vR keys][128 bytes]; byte offset of key 16 i and the strides of
+        // the product's blocks of 64 dims and groups of 8 keys.
+        const int vR = same(p.box_rows);
+        const uint32_t v_lbo = vR * 128, v_sbo = vR == 8 ? 8 * C::ROWB : 1024;
+        auto v_off = [&](int i) -> uint32_t { return i * 16 / vR * vR * C::ROWB + i * 16 % vR * 128; };
+        const uint32_t v1 = v_off(1) >> 4, v2 = v_off(2) >> 4, v3 = v_off(3) >> 4;
         auto wait = [&](uint64_t *b0, int n0, uint64_t *b1, int n1) -> bool {
             const bool odd = lane & 1;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(odd ? b1 : b0, (odd ? n1 : n0) & 1)) != 0;
@@ -268,7 +285,7 @@ __global__ void __launch_bounds__(512, 1)
                     umma_bf16(tS, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
                               dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
                 umma_commit(&s_done[e]);
-                if (!two || x == 1) umma_commit(&k_empty[st]);  // (a commit covers all products before it)
+                umma_commit(&k_empty[st]);
             }
             __syncwarp();
             return true;
@@ -280,28 +297,29 @@ __global__ void __launch_bounds__(512, 1)
             if (!(end && tailed ? wait(&p_ready[e], n >> 1, tail, 0) : wait(&p_ready[e], n >> 1, landed, j / NS)))
                 return false;
             const int nv = end ? last : BT;
-            const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, CS, 1024);
+            const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, v_lbo, v_sbo);
             const uint32_t tP = tm + 64 * e, tOx = tm + C::TO + x * D;
             if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < BT / 16; ++i)
                     if (i * 16 < nv)
-                        umma_bf16_tmem_a(tOx, tP + i * 8, dV + ((i * 2048) >> 4), idO, n > 0 || i > 0);
+                        umma_bf16_tmem_a(tOx, tP + i * 8, dV + (i == 0 ? 0u : i == 1 ? v1 : i == 2 ? v2 : v3), idO,
+                                         n > 0 || i > 0);
                 umma_commit(&pv_done[e]);
-                if (!two || x == 1) umma_commit(&v_empty[st]);
+                if (!two || x == 1) umma_commit(&v_empty[st]);  // (a commit covers all products before it)
             }
             __syncwarp();
             return true;
         };
         const int N0 = (Ju + step - 1) / step, N1 = C::NSTREAM == 1 ? 0 : Ju / step;
         bool ok = true;
-        if (pv) {
+        if (role == C::NSTREAM) {
             for (int n = 0; ok && n < N0; ++n) ok = values(0, n) && (n >= N1 || values(1, n));
         } else {
-            for (int n = 0; ok && n < N0; ++n) ok = scores(0, n) && (n >= N1 || scores(1, n));
+            for (int n = 0; ok && n < (role == 0 ? N0 : N1); ++n) ok = scores(role, n);
         }
         if (!ok && lane == 0) misc[2] = 1;
-        if (elect_one()) umma_commit(&fin[pv ? 1 : 0]);  // this warp's products are done when it completes
+        if (elect_one()) umma_commit(&fin[role]);  // this warp's products are done when it completes
         __syncwarp();
     }
 
@@ -408,7 +426,8 @@ __global__ void __launch_bounds__(512, 1)
     }
     __syncthreads();
     if (soft) {
-        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0));
+        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0) &&
+                                                         (C::NSTREAM == 1 || mbar_wait(&fin[2], 0)));
         tc_fence_after();
         const bool good = done && misc[2] == 0;
         // q and the ring are idle now: the sums leave through them, a row a thread in, a row a warp out (a thread
@@ -550,13 +569,14 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     }
 }
 
-// The paged cache as [64 dims, rows, column block, kv head, page], a box of R rows of one column block.
-bool encode_block_map(CUtensorMap *map, const void *base, int D, int Hkv, int page_size, int num_pages, int R) {
+// The paged cache as [64 dims, rows, column block, kv head, page], a box of R rows of `blocks` column blocks.
+bool encode_block_map(CUtensorMap *map, const void *base, int D, int Hkv, int page_size, int num_pages, int R,
+                      int blocks) {
     const cuuint64_t dims[5] = {64u, (cuuint64_t)page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
                                 (cuuint64_t)num_pages};
     const cuuint64_t strides[4] = {(cuuint64_t)Hkv * D * 2, 128u, (cuuint64_t)D * 2,
                                    (cuuint64_t)page_size * Hkv * D * 2};
-    const cuuint32_t box[5] = {64u, (cuuint32_t)R, 1u, 1u, 1u};
+    const cuuint32_t box[5] = {64u, (cuuint32_t)R, (cuuint32_t)blocks, 1u, 1u};
     return encode_bf16(map, base, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -579,8 +599,9 @@ dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     const int R = GATHER ? C::BT : gcd_int(a.page_size, C::BT);
     CUtensorMap mq, mk = {}, mv = {};
     if (!encode_q_rows(&mq, a)) return DAP_ERR_CUDA;
-    if (!GATHER && (!encode_block_map(&mk, a.k, a.D, a.Hkv, a.page_size, a.num_pages, R) ||
-                    !encode_block_map(&mv, a.v, a.D, a.Hkv, a.page_size, a.num_pages, R)))
+    if (!GATHER &&
+        (!encode_block_map(&mk, a.k, a.D, a.Hkv, a.page_size, a.num_pages, R, R == C::BT ? C::NBLK : 1) ||
+         !encode_block_map(&mv, a.v, a.D, a.Hkv, a.page_size, a.num_pages, R, C::NBLK)))
         return DAP_ERR_CUDA;
     auto kern = shared_prefix_kernel<C>;
     static PerDeviceOcc occ = {};
