@@ -110,6 +110,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         misc[1] = 0;
         fence_barrier_init();
     }
+    if (!C::GATHER && warp == NWC && lane == 0) {
+        prefetch_tensormap(&mapK);
+        prefetch_tensormap(&mapV);
+    }
     // With a prefix kernel before it, this grid starts once every CTA of that kernel has passed its
     // own wait, so what came before is done; without one it waits itself.
     if (pp.prefix_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -146,36 +150,41 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 issued = i + 1;
             }
         } else {  // ---- producer warp: page lookup + TMA issue
-            if (lane == 0) {
-                prefetch_tensormap(&mapK);
-                prefetch_tensormap(&mapV);
-            }
-            auto lookup = [&](int tile) -> int {
-                const int t = tok0 + tile * BT + lane * R;
-                if (lane * R >= BT || t >= tok1) return 0;
-                int pg = __ldg(table + t / p.page_size);
-                if (pg < 0 || pg >= p.num_pages) {
-                    flag_error(DAP_DEVERR_PAGE);
-                    pg = 0;
+            // (page and row of box `lane` step from tile to tile; page ids are loaded two tiles ahead and looked at
+            // when they are used, as in the prefix kernel)
+            const int dq = BT / p.page_size, dr = BT % p.page_size;
+            int idx = (tok0 + lane * R) / p.page_size, row = (tok0 + lane * R) % p.page_size, next = row;
+            int t_ahead = tok0 + lane * R;
+            auto load_page = [&]() -> int {
+                const int pg = lane * R < BT && t_ahead < tok1 ? __ldg(table + idx) : 0;
+                t_ahead += BT;
+                idx += dq;
+                if ((next += dr) >= p.page_size) {
+                    next -= p.page_size;
+                    ++idx;
                 }
                 return pg;
             };
-            int pg_next = lookup(0);
+            int pg0 = load_page(), pg1 = load_page();
             for (int i = 0; i < ntiles; ++i) {
                 const int st = i % NS;
-                const int pg = pg_next;
-                if (i + 1 < ntiles) pg_next = lookup(i + 1);
+                int pg = pg0;
+                pg0 = pg1;
+                pg1 = load_page();
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
                     misc[1] = 1;
                     break;
                 }
-                const int t = tok0 + i * BT;
-                const int nbox = (min(BT, tok1 - t) + R - 1) / R;
+                const int nbox = (min(BT, tok1 - (tok0 + i * BT)) + R - 1) / R;
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
                 __syncwarp();
+                if (pg < 0 || pg >= p.num_pages) {
+                    flag_error(DAP_DEVERR_PAGE);
+                    pg = 0;
+                }
                 if (lane < nbox)
-                    issue_kv_box<C>(smem + st * C::STAGE_BYTES, lane, R, &mapK, &mapV, kvh,
-                                    (t + lane * R) % p.page_size, pg, &full[st]);
+                    issue_kv_box<C>(smem + st * C::STAGE_BYTES, lane, R, &mapK, &mapV, kvh, row, pg, &full[st]);
+                if ((row += dr) >= p.page_size) row -= p.page_size;
                 issued = i + 1;
             }
         }

@@ -16,6 +16,8 @@
 //   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
 //                                  P (bf16 pairs) overwrites the first 32 once they are read;
 //                               O  columns [256 + x D, + D)  fp32 accumulator.
+// Two CTAs whose tiles are of the same group form a cluster: one copies every K tile, the other every V tile, to
+// both (TMA multicast), so that each tile is read from L2 once for both.
 // Warps: four softmax warps a stream (thread = row), a producer, one a stream that issues its scores and one that
 // issues the products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores are there when the
 // softmax gets to them.
@@ -63,7 +65,7 @@ struct PrefixCfg {
 template <class C>
 __global__ void __launch_bounds__(512, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                         const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G) {
+                         const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G, const int cl) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = aligned_smem<C>(smem_raw);
     constexpr int BT = C::BT, NS = C::NS, D = C::D;
@@ -78,11 +80,15 @@ __global__ void __launch_bounds__(512, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
     uint8_t *ring = smem + C::RING_OFF;
 
-    const int units = pp.num_tiles * p.Hkv;
-    const int s = (int)(blockIdx.x / units);
-    const int rem = (int)(blockIdx.x - s * units);
-    const int w = rem / p.Hkv;
-    const int kvh = rem - w * p.Hkv;
+    // clusters of cl (1 or 2) CTAs: tiles cl i .. of one kv head and split
+    const int rank = cl == 2 ? (int)(blockIdx.x & 1) : 0;
+    const int units = (pp.num_tiles + cl - 1) / cl * p.Hkv;
+    const int cid = (int)(blockIdx.x / cl);
+    const int s = cid / units;
+    const int rem = cid - s * units;
+    const int wc = rem / p.Hkv;
+    const int kvh = rem - wc * p.Hkv;
+    const int w = wc * cl + rank;
 
     // Tensor memory touches nothing the previous kernel writes: it is allocated before the wait.
     if (warp == 0) {
@@ -103,16 +109,19 @@ __global__ void __launch_bounds__(512, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // (group, first sequence of the group, first sequence of the tile, sequences)
-    const int4 tl = __ldg(reinterpret_cast<const int4 *>(pp.tiles) + w);
-    const int q0 = tl.y, first = tl.z;
-    int nseq = 0, P = 0;
-    if (tl.x >= 0 && tl.x < pp.num_groups && q0 >= 0 && q0 < p.B && first >= 0 && tl.w >= 1 &&
-        tl.w <= pp.seqs_per_tile && tl.w <= p.B - first) {
-        nseq = tl.w;
-        P = group_prefix(pp, tl.x);
-    } else if (threadIdx.x == 0 && s == 0 && kvh == 0) {
-        flag_error(DAP_DEVERR_QMAP);
-    }
+    auto tile_of = [&](int i) -> int4 {
+        int4 t = i < pp.num_tiles ? __ldg(reinterpret_cast<const int4 *>(pp.tiles) + i) : make_int4(0, 0, 0, 0);
+        if (t.x < 0 || t.x >= pp.num_groups || t.y < 0 || t.y >= p.B || t.z < 0 || t.w < 1 || t.w > pp.seqs_per_tile ||
+            t.w > p.B - t.z)
+            t.w = 0;
+        return t;
+    };
+    const int4 tl = tile_of(w), buddy = cl == 2 ? tile_of(w ^ 1) : make_int4(0, 0, 0, 0);
+    const int q0 = tl.y, first = tl.z, nseq = tl.w;
+    const int P = nseq > 0 ? group_prefix(pp, tl.x) : 0;
+    // the cluster's CTAs share their K/V tiles
+    const bool paired = nseq > 0 && buddy.w > 0 && buddy.x == tl.x && buddy.y == q0;
+    if (nseq == 0 && w < pp.num_tiles && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
     const int nrows = nseq * G;
     const int tok0 = min(P, s * pp.prefix_chunk), tok1 = min(P, tok0 + pp.prefix_chunk);
     const int J = (tok1 - tok0 + BT - 1) / BT;  // K/V tiles of this CTA
@@ -126,8 +135,10 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < NS; ++i) {
             mbar_init(&k_full[i], full_arrivals<C>());
             mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], both ? 2 : 1);  // a commit of every stream that takes the tile
-            mbar_init(&v_empty[i], 1);             // one after the last product that reads it
+            // a commit of every stream that takes the K tile, one after the last product that reads the V tile
+            const int kb = C::NSTREAM == 2 && buddy.w * G > 128 ? 2 : 1;
+            mbar_init(&k_empty[i], (both ? 2 : 1) + (paired ? kb : 0));
+            mbar_init(&v_empty[i], paired ? 2 : 1);
         }
         for (int e = 0; e < 4; ++e) {
             mbar_init(&s_done[e], 1);
@@ -142,6 +153,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     tc_fence_before();
     __syncthreads();  // barriers and the tensor-memory address are visible
+    if (cl == 2) cluster_sync_all();  // (to the other CTA too)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t CS = BT * 128;  // bytes between column blocks of a tile
@@ -180,27 +192,39 @@ __global__ void __launch_bounds__(512, 1)
                 ik = iv = i + 1;
             }
         } else {
-            auto lookup = [&](int tile) -> int {  // page of this lane's box of R keys
-                const int t = tok0 + tile * BT + lane * R;
-                if (lane * R >= BT || t >= tok1) return 0;
-                int pg = __ldg(table + t / p.page_size);
+            // K: lane (box j, column block cb), or whole tiles where a page has them; V: lane = box, all blocks.  A
+            // lane steps the page and the row of its boxes from tile to tile (no division), and the page ids of box
+            // `lane` are loaded two tiles ahead and first looked at when they are used: one that was checked as it
+            // was loaded held the warp for the load's latency, 1350 (page size 64) to 2090 cycles a tile.
+            const int kb = R == BT ? 1 : C::NBLK;
+            const int j = lane / kb, cb = lane % kb;
+            const int dq = BT / p.page_size, dr = BT % p.page_size;
+            int idx = (tok0 + lane * R) / p.page_size, vrow = (tok0 + lane * R) % p.page_size;
+            int krow = (tok0 + j * R) % p.page_size;
+            int ahead = 0;  // tiles that idx is ahead of
+            auto load_page = [&]() -> int {  // the next tile's page of this lane's box
+                const int t = tok0 + ahead * BT + lane * R;
+                const int pg = lane * R < BT && t < tok1 ? __ldg(table + idx) : 0;
+                ++ahead;
+                idx += dq;
+                if ((vrow += dr) >= p.page_size) {
+                    vrow -= p.page_size;
+                    ++idx;
+                }
+                return pg;
+            };
+            int vr0 = vrow;  // row of box `lane` of tile i (vrow runs ahead)
+            int pg0 = load_page(), pg1 = load_page();
+            for (int i = 0; i < J; ++i) {
+                const int st = i % NS;
+                int pg = pg0;
+                pg0 = pg1;
+                pg1 = load_page();
+                const int nbox = (min(BT, tok1 - (tok0 + i * BT)) + R - 1) / R;
                 if (pg < 0 || pg >= p.num_pages) {
                     flag_error(DAP_DEVERR_PAGE);
                     pg = 0;
                 }
-                return pg;
-            };
-            int pg_next = lookup(0);
-            for (int i = 0; i < J; ++i) {
-                const int st = i % NS;
-                const int pg = pg_next;
-                if (i + 1 < J) pg_next = lookup(i + 1);
-                const int t = tok0 + i * BT;
-                const int nbox = (min(BT, tok1 - t) + R - 1) / R;
-                // K: lane (box j, column block cb), or whole tiles where a page has them; V: lane = box, all blocks
-                // (the page of box j is in lane j)
-                const int kb = R == BT ? 1 : C::NBLK;
-                const int j = lane / kb, cb = lane % kb;
                 const int pj = __shfl_sync(0xFFFFFFFFu, pg, j & 31);
                 uint8_t *dst = ring + st * 2 * C::TILE_BYTES;
                 const uint32_t bytes = (uint32_t)(nbox * R * C::ROWB);
@@ -210,9 +234,12 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
                 __syncwarp();
-                if (j < nbox)
-                    tma_load_5d(dst + cb * CS + j * R * 128, &mapK, 0, (t + j * R) % p.page_size, cb, kvh, pj,
-                                &k_full[st]);
+                // (each CTA awaits K and V of its own; in a pair rank 0 copies K, rank 1 V)
+                if (j < nbox) {
+                    uint8_t *to = dst + cb * CS + j * R * 128;
+                    if (!paired) tma_load_5d(to, &mapK, 0, krow, cb, kvh, pj, &k_full[st]);
+                    else if (rank == 0) tma_load_5d_multicast(to, &mapK, 0, krow, cb, kvh, pj, &k_full[st], 3);
+                }
                 ik = i + 1;
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
                     misc[2] = 1;
@@ -220,10 +247,14 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&v_full[st], bytes);
                 __syncwarp();
-                if (lane < nbox)
-                    tma_load_5d(dst + C::TILE_BYTES + lane * R * C::ROWB, &mapV, 0, (t + lane * R) % p.page_size, 0, kvh,
-                                pg, &v_full[st]);
+                if (lane < nbox) {
+                    uint8_t *to = dst + C::TILE_BYTES + lane * R * C::ROWB;
+                    if (!paired) tma_load_5d(to, &mapV, 0, vr0, 0, kvh, pg, &v_full[st]);
+                    else if (rank == 1) tma_load_5d_multicast(to, &mapV, 0, vr0, 0, kvh, pg, &v_full[st], 3);
+                }
                 iv = i + 1;
+                if ((krow += dr) >= p.page_size) krow -= p.page_size;
+                if ((vr0 += dr) >= p.page_size) vr0 -= p.page_size;
             }
         }
         if (lane == 0) {
@@ -248,6 +279,13 @@ __global__ void __launch_bounds__(512, 1)
                 misc[2] = 1;
             }
         }
+        // every commit on this CTA's barriers, the other CTA's too, has arrived before the CTA ends
+        for (int i = max(0, J - NS); i < J && iv == J; ++i)
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[i % NS], (i / NS) & 1) &&
+                                             mbar_wait(&v_empty[i % NS], (i / NS) & 1))) {
+                misc[2] = 1;
+                break;
+            }
     } else if (work && warp >= C::ISSUER) {
         // The whole warp runs its loop with values that are the same in every lane (and known to be), one lane
         // issues: descriptors then stay in uniform registers.  Two barriers are polled at a time, each by half the
@@ -255,7 +293,7 @@ __global__ void __launch_bounds__(512, 1)
         auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         const int role = same(warp - C::ISSUER);  // a stream's scores; NSTREAM: all products with V
         const int Ju = same(J), last = same(nlast);
-        const bool two = same(both) != 0, tailed = same(ragged) != 0;
+        const bool two = same(both) != 0, tailed = same(ragged) != 0, shared = same(paired) != 0;
         const uint32_t tm = same(tmem);
         const int step = two || C::NSTREAM == 1 ? 1 : 2;  // tile n of stream x is step * n + (step == 2 ? x : 0)
         const uint32_t sQ = smem_addr(smem), sR = smem_addr(ring);
@@ -285,7 +323,8 @@ __global__ void __launch_bounds__(512, 1)
                     umma_bf16(tS, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
                               dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
                 umma_commit(&s_done[e]);
-                umma_commit(&k_empty[st]);
+                if (shared) umma_commit_multicast(&k_empty[st], 3);
+                else umma_commit(&k_empty[st]);
             }
             __syncwarp();
             return true;
@@ -306,7 +345,10 @@ __global__ void __launch_bounds__(512, 1)
                         umma_bf16_tmem_a(tOx, tP + i * 8, dV + (i == 0 ? 0u : i == 1 ? v1 : i == 2 ? v2 : v3), idO,
                                          n > 0 || i > 0);
                 umma_commit(&pv_done[e]);
-                if (!two || x == 1) umma_commit(&v_empty[st]);  // (a commit covers all products before it)
+                if (!two || x == 1) {  // (a commit covers all products before it)
+                    if (shared) umma_commit_multicast(&v_empty[st], 3);
+                    else umma_commit(&v_empty[st]);
+                }
             }
             __syncwarp();
             return true;
@@ -501,6 +543,8 @@ __global__ void __launch_bounds__(512, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // (neither CTA of a cluster leaves while the other's copies and commits may still reach it)
+    if (cl == 2) cluster_sync_all();
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
@@ -606,13 +650,16 @@ dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     auto kern = shared_prefix_kernel<C>;
     static PerDeviceOcc occ = {};
     if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
-    const long long grid = (long long)a.num_tiles * a.Hkv * a.prefix_splits;
+    const int cl = !GATHER && a.num_tiles > 1 ? 2 : 1;
+    const long long grid = (long long)((a.num_tiles + cl - 1) / cl * cl) * a.Hkv * a.prefix_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);
-    return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p,
-                                 a.Hq / a.Hkv) == cudaSuccess
-               ? DAP_OK
-               : DAP_ERR_CUDA;
+    const cudaError_t e =
+        cl == 2 ? launch_cluster_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, 2, stream, mq, mk,
+                                                mv, p, a.Hq / a.Hkv, cl)
+                : launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p,
+                                        a.Hq / a.Hkv, cl);
+    return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
 template <bool GATHER>

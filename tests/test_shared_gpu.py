@@ -110,6 +110,10 @@ CASES = [
     ([33], [300], [i % 5 for i in range(33)], 4, 1, 128, 64),  # 132 rows: both streams, the second with 4 rows
     ([70], [513], [7] * 70, 8, 2, 128, 32),                    # 280 rows: two tiles
     ([40], [1000], [11] * 40, 8, 1, 64, 128),                  # G = 8, 320 rows
+    ([66], [333], [3] * 66, 8, 2, 128, 8),                     # 264 rows: the second tile of the pair has 8
+    ([200], [450], [2] * 200, 8, 2, 128, 64),                  # 800 rows: four tiles
+    ([130, 70, 3], [450, 100, 64], [2] * 203, 16, 4, 128, 16), # tiles 3 + 2 + 1: pairs across groups stay apart
+    ([90, 64], [129, 200], [1] * 154, 4, 1, 256, 32),          # D = 256: three tiles and two
     ([130], [190], [2] * 130, 1, 1, 64, 16),                   # G = 1
     ([20], [640], [i for i in range(20)], 16, 2, 256, 16),     # D = 256: 160 rows, two tiles of 128
     ([5], [129], [31, 0, 1, 64, 100], 4, 2, 256, 32),
