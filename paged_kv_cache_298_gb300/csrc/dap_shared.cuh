@@ -63,6 +63,31 @@ __device__ __forceinline__ int suffix_count(const SharedParams &p, const Span &s
     return min(p.sp.num_splits, (s.L - suffix_start(p, s.P) + p.sp.chunk - 1) / p.sp.chunk);
 }
 
+// Page ids of a producer warp: lane l holds entries base + l and base + 32 + l of the sequence's table row, so that a
+// load of 32 entries serves 32 pages and is in flight while the 32 before it are used.  (A load per tile, looked at
+// or only moved to another register a tile later, held the warp for its latency: 1370 cycles a tile.)
+struct PageWindow {
+    const int32_t *row;
+    int base, end, lane;
+    int cur, nxt;
+    __device__ __forceinline__ PageWindow(const int32_t *row_, int first, int max_pages, int lane_)
+        : row(row_), base(first), end(max_pages), lane(lane_) {
+        cur = get(first + lane);
+        nxt = get(first + 32 + lane);
+    }
+    __device__ __forceinline__ int get(int e) const { return e < end ? __ldg(row + e) : 0; }
+    // Entry e of each lane, first <= e < first + 32 (first: the same in every lane, never falling).
+    __device__ __forceinline__ int at(int e, int first) {
+        if (first >= base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = get(base + 32 + lane);
+        }
+        const int a = __shfl_sync(0xFFFFFFFFu, cur, e - base), b = __shfl_sync(0xFFFFFFFFu, nxt, e - base - 32);
+        return e - base < 32 ? a : b;
+    }
+};
+
 // ---- suffix kernel: one CTA per (sequence, kv head, split) ---------------------------------------
 
 template <int D_, int G_, bool GATHER_>
@@ -150,27 +175,15 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 issued = i + 1;
             }
         } else {  // ---- producer warp: page lookup + TMA issue
-            // (page and row of box `lane` step from tile to tile; page ids are loaded two tiles ahead and looked at
-            // when they are used, as in the prefix kernel)
+            // (entry and row of box `lane` step from tile to tile, without a division)
             const int dq = BT / p.page_size, dr = BT % p.page_size;
-            int idx = (tok0 + lane * R) / p.page_size, row = (tok0 + lane * R) % p.page_size, next = row;
-            int t_ahead = tok0 + lane * R;
-            auto load_page = [&]() -> int {
-                const int pg = lane * R < BT && t_ahead < tok1 ? __ldg(table + idx) : 0;
-                t_ahead += BT;
-                idx += dq;
-                if ((next += dr) >= p.page_size) {
-                    next -= p.page_size;
-                    ++idx;
-                }
-                return pg;
-            };
-            int pg0 = load_page(), pg1 = load_page();
+            int e0 = tok0 / p.page_size, row0 = tok0 % p.page_size;  // of the tile's first key
+            const int bo = lane * R < BT ? lane * R : 0;
+            int idx = (tok0 + bo) / p.page_size, row = (tok0 + bo) % p.page_size;
+            PageWindow pages(table, e0, p.max_pages, lane);
             for (int i = 0; i < ntiles; ++i) {
                 const int st = i % NS;
-                int pg = pg0;
-                pg0 = pg1;
-                pg1 = load_page();
+                int pg = pages.at(idx, e0);
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
                     misc[1] = 1;
                     break;
@@ -178,13 +191,23 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 const int nbox = (min(BT, tok1 - (tok0 + i * BT)) + R - 1) / R;
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
                 __syncwarp();
-                if (pg < 0 || pg >= p.num_pages) {
-                    flag_error(DAP_DEVERR_PAGE);
-                    pg = 0;
-                }
-                if (lane < nbox)
+                if (lane < nbox) {
+                    if (pg < 0 || pg >= p.num_pages) {
+                        flag_error(DAP_DEVERR_PAGE);
+                        pg = 0;
+                    }
                     issue_kv_box<C>(smem + st * C::STAGE_BYTES, lane, R, &mapK, &mapV, kvh, row, pg, &full[st]);
-                if ((row += dr) >= p.page_size) row -= p.page_size;
+                }
+                idx += dq;
+                if ((row += dr) >= p.page_size) {
+                    row -= p.page_size;
+                    ++idx;
+                }
+                e0 += dq;
+                if ((row0 += dr) >= p.page_size) {
+                    row0 -= p.page_size;
+                    ++e0;
+                }
                 issued = i + 1;
             }
         }

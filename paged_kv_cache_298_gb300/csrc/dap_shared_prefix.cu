@@ -43,8 +43,8 @@ struct PrefixCfg {
     static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
     static constexpr int TILE_BYTES = BT * ROWB;              // K or V of one tile
     static constexpr int NSTREAM = D == 256 ? 1 : 2;
-    static constexpr int NS = D == 64 ? 6 : D == 128 ? 3 : 2;  // K/V tiles in the ring
-    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 1, PV = ISSUER + NSTREAM,
+    static constexpr int NS = D == 64 ? 6 : D == 128 ? 4 : 2;  // K/V tiles in the ring
+    static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 2, PV = ISSUER + NSTREAM,
                          THREADS = (PV + 1) * 32;
     static constexpr int TO = 256, TMEM_COLS = 512;
     static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
@@ -57,13 +57,40 @@ struct PrefixCfg {
     // tensor memory); at D <= 128 one suffix CTA fits beside the one there is
     static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
     static constexpr int ROW_F = D + 4;  // floats of a row of sums on its way out (the 4: no bank conflicts)
-    static_assert(SMEM <= (D == 256 ? 227 : 164) * 1024, "shared memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(NSTREAM * 128 * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
-// (the bound of 512 threads holds the registers at 128, which leaves room for a suffix CTA's warps)
+// Row gather of one tensor: fill_tile_rows for K or V alone.
 template <class C>
-__global__ void __launch_bounds__(512, 1)
+__device__ __forceinline__ void fill_rows(uint8_t *tile, const __nv_bfloat16 *cache, const RowPages<C> &rp, int nvalid,
+                                          int kvh, const SplitParams &p, uint64_t *full, int lane) {
+    constexpr int CPR = C::ROWB / 16, N = RowPages<C>::N, RPI = 32 / CPR;
+    long long row[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int pg = rp.pg[k];
+        if (lane + 32 * k < nvalid && (pg < 0 || pg >= p.num_pages)) {
+            flag_error(DAP_DEVERR_PAGE);
+            pg = 0;
+        }
+        row[k] = (((long long)pg * p.page_size + rp.slot[k]) * p.Hkv + kvh) * C::D;
+    }
+    if (lane == 0) mbar_arrive(full);
+    const int c = lane % CPR, r0 = lane / CPR;
+    const uint32_t to = smem_addr(tile) + c / C::CPB * (C::BT * 128);
+    const __nv_bfloat16 *src = cache + c * 8;
+#pragma unroll
+    for (int it = 0; it < C::BT / RPI; ++it) {
+        const int r = r0 + RPI * it;
+        const long long off = __shfl_sync(0xFFFFFFFFu, row[(RPI * it) >> 5], r & 31);
+        if (r < nvalid) cp_async_16(to + (uint32_t)(r * 128 + ((c % C::CPB ^ (r & 7)) << 4)), src + off);
+    }
+    cp_async_mbar_arrive(full);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                          const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G, const int cl) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -134,7 +161,7 @@ __global__ void __launch_bounds__(512, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&k_full[i], full_arrivals<C>());
-            mbar_init(&v_full[i], 1);
+            mbar_init(&v_full[i], full_arrivals<C>());
             // a commit of every stream that takes the K tile, one after the last product that reads the V tile
             const int kb = C::NSTREAM == 2 && buddy.w * G > 128 ? 2 : 1;
             mbar_init(&k_empty[i], (both ? 2 : 1) + (paired ? kb : 0));
@@ -161,10 +188,15 @@ __global__ void __launch_bounds__(512, 1)
     const int nlast = tok1 - (tok0 + (J - 1) * BT);  // keys of the last tile
     const bool ragged = work && nlast % 16 != 0;     // its V rows up to a multiple of 16 are zeroed
 
-    if (work && warp == C::PRODUCER) {
+    if (work && (warp == C::PRODUCER || warp == C::PRODUCER + 1)) {
+        // A producer warp each for K and V.  (The chain of instructions of a tile, barrier, page, copy, takes a warp some
+        // 700 cycles a tensor, whatever the copies' size: one warp for both held a tile at 1370 to 1600 cycles.)
+        const int tensor = warp - C::PRODUCER;
         const int32_t *table = p.block_table + (long long)q0 * p.max_pages;
         const int R = p.box_rows;
-        if (lane == 0) {  // q: 64 dims of 128 rows a copy (rows past the tile's end are never read)
+        uint64_t *full = tensor ? v_full : k_full, *empty = tensor ? v_empty : k_empty;
+        uint8_t *place = ring + tensor * C::TILE_BYTES;
+        if (tensor == 0 && lane == 0) {  // q: 64 dims of 128 rows a copy (rows past the tile's end are never read)
             const int parts = both ? 2 : 1;
             mbar_arrive_expect_tx(q_full, (uint32_t)(parts * C::NBLK * C::QBLK));
             for (int x = 0; x < parts; ++x)
@@ -173,99 +205,66 @@ __global__ void __launch_bounds__(512, 1)
                                 q_full);
         }
         __syncwarp();
-        int ik = 0, iv = 0;
+        int done = 0;  // tiles issued
         if constexpr (C::GATHER) {
             RowPages<C> rp_next;
             lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
-            for (int i = 0; i < J; ++i) {
-                const int st = i % NS;
+            for (; done < J; ++done) {
+                const int st = done % NS, t = tok0 + done * BT;
                 const RowPages<C> rp = rp_next;
-                const int t = tok0 + i * BT;
-                if (i + 1 < J) lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
-                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[st], ((i / NS) - 1) & 1) &&
-                                                            mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
-                    misc[2] = 1;
-                    break;
-                }
-                fill_tile_rows<C>(ring + st * 2 * C::TILE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &k_full[st],
-                                  lane);
-                ik = iv = i + 1;
+                if (done + 1 < J) lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
+                if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
+                fill_rows<C>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, rp, min(BT, tok1 - t), kvh, p,
+                             &full[st], lane);
             }
         } else {
-            // K: lane (box j, column block cb), or whole tiles where a page has them; V: lane = box, all blocks.  A
-            // lane steps the page and the row of its boxes from tile to tile (no division), and the page ids of box
-            // `lane` are loaded two tiles ahead and first looked at when they are used: one that was checked as it
-            // was loaded held the warp for the load's latency, 1350 (page size 64) to 2090 cycles a tile.
-            const int kb = R == BT ? 1 : C::NBLK;
+            // K: lane = (box j, column block cb), or a whole tile where a page has one; V: lane = box, all blocks.  A
+            // lane steps the entry and the row of its box from tile to tile (no division).
+            const CUtensorMap *map = tensor ? &mapV : &mapK;
+            const int kb = tensor || R == BT ? 1 : C::NBLK;
             const int j = lane / kb, cb = lane % kb;
+            const int to = tensor ? j * R * C::ROWB : cb * (int)CS + j * R * 128;
             const int dq = BT / p.page_size, dr = BT % p.page_size;
-            int idx = (tok0 + lane * R) / p.page_size, vrow = (tok0 + lane * R) % p.page_size;
-            int krow = (tok0 + j * R) % p.page_size;
-            int ahead = 0;  // tiles that idx is ahead of
-            auto load_page = [&]() -> int {  // the next tile's page of this lane's box
-                const int t = tok0 + ahead * BT + lane * R;
-                const int pg = lane * R < BT && t < tok1 ? __ldg(table + idx) : 0;
-                ++ahead;
-                idx += dq;
-                if ((vrow += dr) >= p.page_size) {
-                    vrow -= p.page_size;
-                    ++idx;
-                }
-                return pg;
-            };
-            int vr0 = vrow;  // row of box `lane` of tile i (vrow runs ahead)
-            int pg0 = load_page(), pg1 = load_page();
-            for (int i = 0; i < J; ++i) {
-                const int st = i % NS;
-                int pg = pg0;
-                pg0 = pg1;
-                pg1 = load_page();
-                const int nbox = (min(BT, tok1 - (tok0 + i * BT)) + R - 1) / R;
-                if (pg < 0 || pg >= p.num_pages) {
-                    flag_error(DAP_DEVERR_PAGE);
-                    pg = 0;
-                }
-                const int pj = __shfl_sync(0xFFFFFFFFu, pg, j & 31);
-                uint8_t *dst = ring + st * 2 * C::TILE_BYTES;
-                const uint32_t bytes = (uint32_t)(nbox * R * C::ROWB);
-                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[st], ((i / NS) - 1) & 1))) {
-                    misc[2] = 1;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
+            const int tb = tok0 + (j * R < BT ? j * R : 0);  // (lanes without a box follow the tile's first)
+            int e0 = tok0 / p.page_size, row0 = tok0 % p.page_size, e = tb / p.page_size, row = tb % p.page_size;
+            // (each CTA awaits its own K and V; in a pair rank 0 copies K, rank 1 V)
+            const bool copies = !paired || rank == tensor;
+            PageWindow pages(table, e0, p.max_pages, lane);
+            for (; done < J; ++done) {
+                const int st = done % NS;
+                const int nbox = (min(BT, tok1 - (tok0 + done * BT)) + R - 1) / R;
+                int pg = pages.at(e, e0);
+                if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB));
                 __syncwarp();
-                // (each CTA awaits K and V of its own; in a pair rank 0 copies K, rank 1 V)
-                if (j < nbox) {
-                    uint8_t *to = dst + cb * CS + j * R * 128;
-                    if (!paired) tma_load_5d(to, &mapK, 0, krow, cb, kvh, pj, &k_full[st]);
-                    else if (rank == 0) tma_load_5d_multicast(to, &mapK, 0, krow, cb, kvh, pj, &k_full[st], 3);
+                if (j < nbox && copies) {
+                    if (pg < 0 || pg >= p.num_pages) {
+                        flag_error(DAP_DEVERR_PAGE);
+                        pg = 0;
+                    }
+                    uint8_t *dst = place + st * 2 * C::TILE_BYTES + to;
+                    if (paired) tma_load_5d_multicast(dst, map, 0, row, cb, kvh, pg, &full[st], 3);
+                    else tma_load_5d(dst, map, 0, row, cb, kvh, pg, &full[st]);
                 }
-                ik = i + 1;
-                if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[st], ((i / NS) - 1) & 1))) {
-                    misc[2] = 1;
-                    break;
+                e += dq;
+                if ((row += dr) >= p.page_size) {
+                    row -= p.page_size;
+                    ++e;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&v_full[st], bytes);
-                __syncwarp();
-                if (lane < nbox) {
-                    uint8_t *to = dst + C::TILE_BYTES + lane * R * C::ROWB;
-                    if (!paired) tma_load_5d(to, &mapV, 0, vr0, 0, kvh, pg, &v_full[st]);
-                    else if (rank == 1) tma_load_5d_multicast(to, &mapV, 0, vr0, 0, kvh, pg, &v_full[st], 3);
+                e0 += dq;
+                if ((row0 += dr) >= p.page_size) {
+                    row0 -= p.page_size;
+                    ++e0;
                 }
-                iv = i + 1;
-                if ((krow += dr) >= p.page_size) krow -= p.page_size;
-                if ((vr0 += dr) >= p.page_size) vr0 -= p.page_size;
             }
         }
-        if (lane == 0) {
-            misc[0] = ik;
-            misc[1] = iv;
-        }
+        if (done < J) misc[2] = 1;
+        if (lane == 0) misc[tensor] = done;
         __syncwarp();
-        if (ragged && iv == J) {
+        if (tensor == 1 && ragged && done == J) {
             // V rows past the end enter the last product with weight zero, whatever the page holds
             const int st = (J - 1) % NS;
-            if (__all_sync(0xFFFFFFFFu, mbar_wait(C::GATHER ? &k_full[st] : &v_full[st], ((J - 1) / NS) & 1))) {
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(&v_full[st], ((J - 1) / NS) & 1))) {
                 const int nz = 16 - nlast % 16;
                 for (int e = lane; e < nz * C::NBLK * C::CPB; e += 32)
                     *reinterpret_cast<uint4 *>(ring + (st * 2 + 1) * C::TILE_BYTES +
@@ -280,9 +279,8 @@ __global__ void __launch_bounds__(512, 1)
             }
         }
         // every commit on this CTA's barriers, the other CTA's too, has arrived before the CTA ends
-        for (int i = max(0, J - NS); i < J && iv == J; ++i)
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[i % NS], (i / NS) & 1) &&
-                                             mbar_wait(&v_empty[i % NS], (i / NS) & 1))) {
+        for (int i = max(0, J - NS); i < J && done == J; ++i)
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[i % NS], (i / NS) & 1))) {
                 misc[2] = 1;
                 break;
             }
@@ -332,8 +330,7 @@ __global__ void __launch_bounds__(512, 1)
         auto values = [&](int x, int n) -> bool {
             const int j = step * n + (step == 2 ? x : 0), st = j % NS, e = 2 * x + (n & 1);
             const bool end = j == Ju - 1;
-            uint64_t *landed = C::GATHER ? &k_full[st] : &v_full[st];
-            if (!(end && tailed ? wait(&p_ready[e], n >> 1, tail, 0) : wait(&p_ready[e], n >> 1, landed, j / NS)))
+            if (!(end && tailed ? wait(&p_ready[e], n >> 1, tail, 0) : wait(&p_ready[e], n >> 1, &v_full[st], j / NS)))
                 return false;
             const int nv = end ? last : BT;
             const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, v_lbo, v_sbo);
@@ -472,8 +469,8 @@ __global__ void __launch_bounds__(512, 1)
                                                          (C::NSTREAM == 1 || mbar_wait(&fin[2], 0)));
         tc_fence_after();
         const bool good = done && misc[2] == 0;
-        // q and the ring are idle now: the sums leave through them, a row a thread in, a row a warp out (a thread
-        // that wrote its row to global memory touched 32 lines with every store of the warp: 11,000 cycles)
+        // q and the ring are idle now: the sums leave through them, a row a thread, as one bulk copy each (rows written
+        // to global memory by their threads, 32 lines a store: 11,000 cycles; by warps, row after row: 5500)
         float *mine = reinterpret_cast<float *>(smem) + (x * 128 + r) * C::ROW_F;
         const bool merge = C::NSTREAM == 2 && !both;  // both streams hold the same rows: stream 0 adds stream 1's
         if (merge) {
@@ -521,23 +518,18 @@ __global__ void __launch_bounds__(512, 1)
                 for (int k = 0; k < 32; k += 4)
                     *reinterpret_cast<float4 *>(mine + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
-            if (rvalid) *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
-            __syncwarp();
-            const float *rows = mine - lane * C::ROW_F;
-            const int cnt = min(32, nx - (warp & 3) * 32);
-#pragma unroll 4
-            for (int i = 0; i < cnt; ++i) {
-                float *dst = pp.o_part + __shfl_sync(0xFFFFFFFFu, prow, i) * D;
-#pragma unroll
-                for (int c = lane * 4; c < D; c += 128)
-                    *reinterpret_cast<float4 *>(dst + c) = *reinterpret_cast<const float4 *>(rows + i * C::ROW_F + c);
+            if (rvalid) {
+                *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
+                fence_async_smem();
+                bulk_store(pp.o_part + prow * D, mine, D * 4);
+                bulk_store_wait();
             }
         }
         if (threadIdx.x == 0 && misc[2]) {
             // a wait gave up: the copies still in flight land (bounded) before the shared memory goes
             (void)mbar_wait(q_full, 0);
             for (int i = max(0, misc[0] - NS); i < misc[0]; ++i) (void)mbar_wait(&k_full[i % NS], (i / NS) & 1);
-            for (int i = max(0, misc[1] - NS); !C::GATHER && i < misc[1]; ++i)
+            for (int i = max(0, misc[1] - NS); i < misc[1]; ++i)
                 (void)mbar_wait(&v_full[i % NS], (i / NS) & 1);
         }
     }
