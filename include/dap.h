@@ -391,13 +391,17 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
  *                 the tile, its sequences, at most seqs_per_tile).
  * Returns the number of tiles, or -1 when max_tiles is too small or an input is invalid.
  * dap_shared_seqs_per_tile: 256 / G (128 / G at D = 256), 0 for unsupported heads.
- * dap_shared_prefix_splits: the planner's splits of the prefix for sm_count SMs (each split is one CTA
- * per tile and kv head).  Pure host functions; no CUDA call.
+ * dap_shared_plan: the split counts that a call runs.  A count that is 0 on entry is chosen so that the prefix's
+ * CTAs (one SM each, one per tile, kv head and split) and the suffix's (one per sequence, kv head and split, four
+ * to an SM) end together; one that is not is lowered as dap_resolve_splits does; the count of a part whose bound
+ * is 0 becomes 0.  total_suffix: the summed lengths behind the prefixes (0: unknown, B * max_suffix_len).
+ * Returns 0, or -1 for invalid arguments.  Pure host functions; no CUDA call.
  */
 int dap_shared_seqs_per_tile(int Hq, int Hkv, int D);
 int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile, int32_t *seq_group,
                    int32_t *tiles, int max_tiles);
-int dap_shared_prefix_splits(int sm_count, int num_tiles, int Hkv, int max_prefix_len);
+int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, int max_prefix_len,
+                    int max_suffix_len, long long total_suffix, int *prefix_splits, int *suffix_splits);
 
 /* Workspace bytes of decode_attn_paged_shared for the split counts that a call runs: room for
  * B * (prefix_splits + suffix_splits) * Hq partial rows of (D + 2) floats.  Pure host function. */
@@ -415,9 +419,8 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
  *                 when num_groups is 1).  A sequence whose group is out of range gives a zero row, a tile out of
  *                 range leaves its sequences' results undefined; both set DAP_DEVERR_QMAP.
  *   max_prefix_len, max_suffix_len  host: upper bounds of prefix_lens[g] and seq_lens[b] - prefix_lens[g].
- *   prefix_splits, suffix_splits    0: the planner's (dap_shared_prefix_splits(SMs, num_tiles, Hkv,
- *                 max_prefix_len); dap_resolve_splits(0, SMs, B, Hq, Hkv, D, page_size, max_suffix_len, 0));
- *                 >= 1: explicit; both lowered as dap_resolve_splits does.  A part whose bound is 0 runs none.
+ *   prefix_splits, suffix_splits    as dap_shared_plan on the device's SMs with total_suffix = 0 (0: the
+ *                 planner's, >= 1: explicit).
  *   workspace     device, >= dap_workspace_bytes_shared(B, Hq, D, the two counts run), 16-byte aligned.
  *   Supported: D in {64, 128, 256}; G in {1, 2, 4, 8}; any page_size >= 1.  seqs_per_tile as
  *   dap_shared_seqs_per_tile.  The summation order depends only on logical positions, the group sizes and the

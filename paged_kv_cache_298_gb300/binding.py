@@ -37,7 +37,7 @@ EXPORTS = ("dap_status_string", "dap_version", "dap_device_sm_count", "dap_plan_
            "dap_q_tile_map", "dap_workspace_bytes_multi", "decode_attn_paged_multi",
            "decode_attn_paged_fp8kv", "kv_append_paged_fp8", "decode_attn_paged_masked",
            "dap_selftest_wait_timeout", "kv_append_paged_fp8_multi", "kv_read_paged_fp8",
-           "decode_attn_paged_shared", "dap_shared_seqs_per_tile", "dap_shared_map", "dap_shared_prefix_splits",
+           "decode_attn_paged_shared", "dap_shared_seqs_per_tile", "dap_shared_map", "dap_shared_plan",
            "dap_workspace_bytes_shared")
 
 
@@ -135,8 +135,8 @@ def load(build_if_missing: bool = True):
         lib.dap_shared_seqs_per_tile.restype = I
         lib.dap_shared_map.argtypes = [P, I, I, P, P, I]
         lib.dap_shared_map.restype = I
-        lib.dap_shared_prefix_splits.argtypes = [I, I, I, I]
-        lib.dap_shared_prefix_splits.restype = I
+        lib.dap_shared_plan.argtypes = [I, I, I, I, I, I, I, I, LL, P, P]
+        lib.dap_shared_plan.restype = I
         lib.dap_workspace_bytes_shared.argtypes = [I, I, I, I, I]
         lib.dap_workspace_bytes_shared.restype = SZ
         lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I,
@@ -651,6 +651,9 @@ class SharedPlan:
         default: the current one)."""
         if device is None or device < 0:
             device = _current_device() if torch.cuda.is_available() else -1
+        # lengths that grow by a token a step keep their plan: rounded up to 64, or to an eighth of themselves
+        max_suffix_len, total_suffix = (n + -n % max(64, 1 << max(0, n.bit_length() - 4)) for n in
+                                        (max_suffix_len, total_suffix))
         key = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
         last, found = self._last
         if last == key:
@@ -661,13 +664,11 @@ class SharedPlan:
                 sms = lib.dap_device_sm_count()
         else:
             sms = 0
-        ps, ss = 0, 0
-        if max_prefix_len > 0:
-            ps = prefix_splits or lib.dap_shared_prefix_splits(sms, self.num_tiles, self.Hkv, max_prefix_len)
-            ps = lib.dap_resolve_splits(ps, sms, self.num_tiles, self.Hq, self.Hkv, self.D, 1, max_prefix_len, 0)
-        if max_suffix_len > 0:
-            ss = lib.dap_resolve_splits(suffix_splits, sms, self.B, self.Hq, self.Hkv, self.D, 1, max_suffix_len,
-                                        total_suffix)
+        pre, suf = ctypes.c_int(prefix_splits), ctypes.c_int(suffix_splits)
+        _need(lib.dap_shared_plan(sms, self.num_tiles, self.B, self.Hq, self.Hkv, self.D, max_prefix_len, max_suffix_len,
+                                  total_suffix, ctypes.byref(pre), ctypes.byref(suf)) == 0,
+              "bounds and split counts must be >= 0")
+        ps, ss = pre.value, suf.value
         self._last = (key, (ps, ss))   # (steps of one batch often share their bounds)
         return ps, ss
 

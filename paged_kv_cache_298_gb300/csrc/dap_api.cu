@@ -528,23 +528,70 @@ int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile
     return n;
 }
 
-int dap_shared_prefix_splits(int sm_count, int num_tiles, int Hkv, int max_prefix_len) {
-    if (sm_count <= 0 || num_tiles <= 0 || Hkv <= 0 || max_prefix_len <= 0) return 1;
-    // One CTA per SM.  The cost of S splits, in K/V tiles of one CTA: the waves of the grid times
-    // (a chunk's tiles and what a CTA takes to start and end, about 6), and half a tile for every
-    // partial that the combine reads.
-    const long long units = (long long)num_tiles * Hkv, tiles = ceil_div_ll(max_prefix_len, kTileTokens);
-    int best = 1;
-    double cost = 1e300;
-    for (long long S = 1; S <= std::min<long long>(tiles, std::max<long long>(1, 2 * sm_count / units)); ++S) {
-        const long long per = ceil_div_ll(tiles, S), n = ceil_div_ll(tiles, per);
-        const double c = (double)ceil_div_ll(units * n, sm_count) * (per + 6) + 0.5 * n;
-        if (c < cost) {
-            cost = c;
-            best = (int)n;
+int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, int max_prefix_len, int max_suffix_len,
+                    long long total_suffix, int *prefix_splits, int *suffix_splits) {
+    if (num_tiles < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || max_prefix_len < 0 || max_suffix_len < 0 ||
+        !prefix_splits || !suffix_splits || *prefix_splits < 0 || *suffix_splits < 0)
+        return -1;
+    const int sms = std::max(1, sm_count);
+    if (total_suffix <= 0) total_suffix = (long long)B * max_suffix_len;
+    if (max_prefix_len == 0) *prefix_splits = 0;
+    if (max_suffix_len == 0) *suffix_splits = 0;
+    const bool prefix = max_prefix_len > 0, suffix = max_suffix_len > 0;
+    if (prefix && (*prefix_splits == 0 || (suffix && *suffix_splits == 0))) {
+        // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM, run on the others meanwhile, and on all of
+        // them afterwards.  The pair of counts with the least time by this model, in microseconds, as measured: 8 to
+        // start and end a prefix CTA, 0.78 a 64-key tile (0.55 with at most 128 rows, 0.95 at D = 256); 4 to start
+        // and end a suffix CTA and 0.4 for 32 keys; suffix K/V at 0.066 MB/us an SM, 6.6 MB/us in all; partial rows
+        // through the workspace at 5 MB/us.
+        const double mb = 1e-6, per_sm = 0.066, all = 6.6;
+        const long long rows = num_tiles > 0 ? ((long long)B * (Hq / Hkv) + num_tiles - 1) / num_tiles : 1;
+        const double tile = D == 256 ? 0.95 : rows <= 128 ? 0.55 : 0.78;
+        const long long tiles = ceil_div_ll(max_prefix_len, kTileTokens);
+        const long long units = (num_tiles > 1 ? (num_tiles + 1LL) / 2 * 2 : 1) * Hkv;  // (pairs of tiles)
+        const double suffix_mb = (double)total_suffix * Hkv * D * 4 * mb, merge = (double)B * Hq * D * 8 * mb / 5.;
+        double best = 1e300;
+        int best_prefix = 1, best_suffix = suffix ? 1 : 0;
+        auto consider = [&](long long per) {
+            const long long n = ceil_div_ll(tiles, per), ctas = units * n, free = std::max<long long>(0, sms - ctas);
+            const double t = (double)ceil_div_ll(ctas, sms) * (8. + per * tile), rate = std::min(all, free * per_sm);
+            const double left = suffix_mb - rate * t, bandwidth = t + (left > 0. ? left / all : 0.);
+            for (int m = suffix ? 1 : 0;; m *= 2) {
+                if (suffix && *suffix_splits > 0) m = *suffix_splits;
+                double us = bandwidth;
+                if (suffix) {
+                    const double cta = 4. + 0.4 * (double)ceil_div_ll(ceil_div_ll(max_suffix_len, m), 32);
+                    const double waves = (double)B * Hkv * m / (4. * (double)(free > 0 ? free : sms));
+                    us = std::max(us, (free > 0 ? 0. : t) + cta * std::max(1., waves));
+                }
+                us += merge * (double)(n + m);
+                if (us < best) {
+                    best = us;
+                    best_prefix = (int)n;
+                    best_suffix = m;
+                }
+                if (!suffix || *suffix_splits > 0 || m >= 64 || (long long)m * kTileTokens >= max_suffix_len) break;
+            }
+        };
+        if (*prefix_splits > 0) {
+            consider(ceil_div_ll(tiles, std::min<long long>(*prefix_splits, tiles)));
+            best_prefix = *prefix_splits;
+        } else {
+            const long long most = std::min<long long>(tiles, std::max<long long>(1, sms / std::max(1LL, units)));
+            long long last = 0;
+            for (long long per = ceil_div_ll(tiles, most); per <= tiles; ++per) {
+                const long long n = ceil_div_ll(tiles, per);
+                if (n != last) consider(per);
+                last = n;
+                if (n == 1) break;
+            }
         }
+        *prefix_splits = best_prefix;
+        if (suffix) *suffix_splits = best_suffix;
     }
-    return best;
+    if (prefix) *prefix_splits = dap_resolve_splits(*prefix_splits, sms, B, Hq, Hkv, D, 1, max_prefix_len, 0);
+    if (suffix) *suffix_splits = dap_resolve_splits(*suffix_splits, sms, B, Hq, Hkv, D, 1, max_suffix_len, total_suffix);
+    return 0;
 }
 
 size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int suffix_splits) {
@@ -579,23 +626,14 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
         !aligned4(seq_group) || !aligned16(tiles))
         return DAP_ERR_ALIGN;
     // every row ends in the combine; a part whose bound is 0 has no splits
-    if (max_prefix_len == 0) {
-        prefix_splits = 0;
-    } else {
-        if (prefix_splits == 0) {
-            const int sms = dap_device_sm_count();
-            if (sms <= 0) return DAP_ERR_CUDA;
-            prefix_splits = dap_shared_prefix_splits(sms, num_tiles, Hkv, max_prefix_len);
-        }
-        prefix_splits = dap_resolve_splits(prefix_splits, 0, num_tiles, Hq, Hkv, D, page_size, max_prefix_len, 0);
+    int sms = 0;
+    if ((prefix_splits == 0 && max_prefix_len > 0) || (suffix_splits == 0 && max_suffix_len > 0)) {
+        sms = dap_device_sm_count();
+        if (sms <= 0) return DAP_ERR_CUDA;
     }
-    if (max_suffix_len == 0) {
-        suffix_splits = 0;
-    } else {
-        const int sms = suffix_splits == 0 ? dap_device_sm_count() : 0;
-        if (suffix_splits == 0 && sms <= 0) return DAP_ERR_CUDA;
-        suffix_splits = dap_resolve_splits(suffix_splits, sms, B, Hq, Hkv, D, page_size, max_suffix_len, 0);
-    }
+    if (dap_shared_plan(sms, num_tiles, B, Hq, Hkv, D, max_prefix_len, max_suffix_len, 0, &prefix_splits,
+                        &suffix_splits) != 0)
+        return DAP_ERR_SHAPE;
     const size_t need = dap_workspace_bytes_shared(B, Hq, D, prefix_splits, suffix_splits);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return DAP_ERR_WORKSPACE;
     SharedArgs a = {};

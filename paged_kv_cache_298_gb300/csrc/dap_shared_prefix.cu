@@ -196,19 +196,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int R = p.box_rows;
         uint64_t *full = tensor ? v_full : k_full, *empty = tensor ? v_empty : k_empty;
         uint8_t *place = ring + tensor * C::TILE_BYTES;
-        if (tensor == 0 && lane == 0) {  // q: 64 dims of 128 rows a copy (rows past the tile's end are never read)
-            const int parts = both ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, (uint32_t)(parts * C::NBLK * C::QBLK));
-            for (int x = 0; x < parts; ++x)
-                for (int cb = 0; cb < C::NBLK; ++cb)
-                    tma_load_3d(smem + (x * C::NBLK + cb) * C::QBLK, &mapQ, cb * 64, kvh * G, first + x * (128 / G),
-                                q_full);
-        }
-        __syncwarp();
         int done = 0;  // tiles issued
+        auto load_q = [&] {  // 64 dims of 128 rows a copy (rows past the tile's end are never read)
+            if (tensor == 0 && lane == 0) {
+                const int parts = both ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, (uint32_t)(parts * C::NBLK * C::QBLK));
+                for (int x = 0; x < parts; ++x)
+                    for (int cb = 0; cb < C::NBLK; ++cb)
+                        tma_load_3d(smem + (x * C::NBLK + cb) * C::QBLK, &mapQ, cb * 64, kvh * G, first + x * (128 / G),
+                                    q_full);
+            }
+            __syncwarp();
+        };
         if constexpr (C::GATHER) {
             RowPages<C> rp_next;
             lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
+            load_q();
             for (; done < J; ++done) {
                 const int st = done % NS, t = tok0 + done * BT;
                 const RowPages<C> rp = rp_next;
@@ -224,12 +227,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int kb = tensor || R == BT ? 1 : C::NBLK;
             const int j = lane / kb, cb = lane % kb;
             const int to = tensor ? j * R * C::ROWB : cb * (int)CS + j * R * 128;
-            const int dq = BT / p.page_size, dr = BT % p.page_size;
-            const int tb = tok0 + (j * R < BT ? j * R : 0);  // (lanes without a box follow the tile's first)
-            int e0 = tok0 / p.page_size, row0 = tok0 % p.page_size, e = tb / p.page_size, row = tb % p.page_size;
+            int e0 = tok0 / p.page_size, row0 = tok0 - e0 * p.page_size;
+            PageWindow pages(table, e0, p.max_pages, lane);
+            load_q();
+            const int dq = BT / p.page_size, dr = BT - dq * p.page_size;
+            int e = e0, row = row0 + (j * R < BT ? j * R : 0);  // (lanes without a box follow the tile's first)
+            for (; row >= p.page_size; ++e) row -= p.page_size;
             // (each CTA awaits its own K and V; in a pair rank 0 copies K, rank 1 V)
             const bool copies = !paired || rank == tensor;
-            PageWindow pages(table, e0, p.max_pages, lane);
             for (; done < J; ++done) {
                 const int st = done % NS;
                 const int nbox = (min(BT, tok1 - (tok0 + done * BT)) + R - 1) / R;
@@ -545,62 +550,89 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 // Merge of a row's prefix and suffix partials, in that order; W warps a row, warp w taking partials
-// w, w + W, ... and the warps' sums added in warp order.
+// w, w + W, ... and the warps' sums added in warp order.  A warp loads NB partials at a time, sums and maxima
+// together, and moves its running maximum between batches: one trip to memory for up to NB partials.
 template <int D, int W>
 __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams pp) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int DPV = D / 32;
-    __shared__ float red[W > 1 ? 8 : 1][W > 1 ? D + 1 : 1];
+    constexpr int DPV = D / 32, NB = 8;
+    __shared__ float red[W > 1 ? 8 : 1][W > 1 ? D + 2 : 1];
     const SplitParams &p = pp.sp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long gw = W == 8 ? (long long)blockIdx.x : (long long)blockIdx.x * 8 + warp;
-    if (gw >= (long long)p.B * p.Hq) return;
-    const int b = (int)(gw / p.Hq), hq = (int)(gw - (long long)b * p.Hq);
+    const bool live = gw < (long long)p.B * p.Hq;
+    const int b = live ? (int)(gw / p.Hq) : 0, hq = live ? (int)(gw - (long long)b * p.Hq) : 0;
     unsigned int flags = 0;
+    // The lengths were there before the prefix or suffix kernel read them, and this grid starts after those
+    // have: only without them it has to wait first.
+    if (pp.total_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     const Span span = seq_span(pp, b, &flags);
-    if (flags && hq == 0 && lane == 0 && (W == 1 || warp == 0)) flag_error(flags);
     const int np = span.L > 0 && span.P > 0 ? (span.P + pp.prefix_chunk - 1) / pp.prefix_chunk : 0;
     const int n = np + suffix_count(pp, span);
+    if (pp.total_splits != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!live) return;
+    if (flags && hq == 0 && lane == 0 && (W == 1 || warp == 0)) flag_error(flags);
     const long long row0 = (long long)b * pp.total_splits * p.Hq + hq;
-    auto row_of = [&](int i) { return row0 + (long long)(i < np ? i : i - np + pp.prefix_splits) * p.Hq; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, pp.ml_part[row_of(i) * 2]);
+    float M = -INFINITY, l = 0.f, acc[DPV];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    RowMerge<D> r;
-    r.begin(M);
-    const int w0 = W == 1 ? 0 : warp;
-    for (int i0 = w0; i0 < n; i0 += 8 * W) {
-        const float *o[8];
-        float2 ml[8];
-        const int m = min(8, (n - i0 + W - 1) / W);
+    for (int j = 0; j < DPV; ++j) acc[j] = 0.f;
+    for (int i0 = W == 1 ? 0 : warp; i0 < n; i0 += NB * W) {
+        float x[NB][DPV];
+        float2 ml[NB];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const long long row = row_of(i0 + W * min(k, m - 1));
-            o[k] = pp.o_part + row * D;
-            ml[k] = *reinterpret_cast<const float2 *>(pp.ml_part + row * 2);
+        for (int k = 0; k < NB; ++k) {
+            const int i = i0 + W * k;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i < n) {
+                const long long row = row0 + (long long)(i < np ? i : i - np + pp.prefix_splits) * p.Hq;
+                ml[k] = *reinterpret_cast<const float2 *>(pp.ml_part + row * 2);
+                load_row_part<DPV>(pp.o_part + row * D + lane * DPV, x[k]);
+            }
         }
-        r.add_batch(o, ml, m, lane);
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) m = fmaxf(m, ml[k].x);
+        const float mu = m == -INFINITY ? 0.f : m, old = ex2(M - mu);
+        M = m;
+        l *= old;
+#pragma unroll
+        for (int j = 0; j < DPV; ++j) acc[j] *= old;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            if (i0 + W * k < n) {
+                const float f = ex2(ml[k].x - mu);
+                l = fmaf(f, ml[k].y, l);
+#pragma unroll
+                for (int j = 0; j < DPV; ++j) acc[j] = fmaf(f, x[k][j], acc[j]);
+            }
+        }
     }
     __nv_bfloat16 *out = p.out + (long long)b * p.o_sb + (long long)hq * p.o_sh;
     if constexpr (W == 1) {
-        r.store(out, lane);
+        store_row_part<DPV>(out + lane * DPV, acc, l);
     } else {
 #pragma unroll
-        for (int j = 0; j < DPV; ++j) red[warp][lane * DPV + j] = r.acc[j];
-        if (lane == 0) red[warp][D] = r.lsum;
+        for (int j = 0; j < DPV; ++j) red[warp][lane * DPV + j] = acc[j];
+        if (lane == 0) {
+            red[warp][D] = l;
+            red[warp][D + 1] = M;
+        }
         __syncthreads();
         if (threadIdx.x < D / 2) {
             const int d = 2 * threadIdx.x;
-            float a0 = 0.f, a1 = 0.f, l = 0.f;
+            float m = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < W; ++k) m = fmaxf(m, red[k][D + 1]);
+            const float mu = m == -INFINITY ? 0.f : m;
+            float a0 = 0.f, a1 = 0.f, ls = 0.f;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                a0 += red[k][d];
-                a1 += red[k][d + 1];
-                l += red[k][D];
+                const float f = ex2(red[k][D + 1] - mu);
+                a0 = fmaf(f, red[k][d], a0);
+                a1 = fmaf(f, red[k][d + 1], a1);
+                ls = fmaf(f, red[k][D], ls);
             }
-            store_out_pair(out + d, a0, a1, l);
+            store_out_pair(out + d, a0, a1, ls);
         }
     }
 }

@@ -78,16 +78,32 @@ def test_plan_refuses():
     assert f(n.data_ptr(), 1, 64, None, out[1].data_ptr(), 2) == -1 and f(None, 1, 64, out[0].data_ptr(), out[1].data_ptr(), 2) == -1
 
 
-def test_prefix_splits_fill_the_device_and_cover_the_prefix():
-    f = binding.load().dap_shared_prefix_splits
-    for tiles in (1, 2, 3, 7, 20, 40):
-        for Hkv in (1, 2, 8):
-            for P in (1, 63, 64, 65, 1000, 8192, 32768):
-                S = f(152, tiles, Hkv, P)
-                assert 1 <= S <= -(-P // 64)
-                assert S * binding.chunk_tokens(P, S) >= P
-    assert f(152, 2, 8, 32768) == 9          # 144 CTAs on 152 SMs
-    assert f(0, 1, 1, 100) == f(152, 0, 8, 100) == f(152, 1, 8, 0) == 1
+def plan(tiles, B, Hq, Hkv, D, pre, suf, total=0, sms=152, want=(0, 0)):
+    a, b = ctypes.c_int(want[0]), ctypes.c_int(want[1])
+    r = binding.load().dap_shared_plan(sms, tiles, B, Hq, Hkv, D, pre, suf, total, ctypes.byref(a), ctypes.byref(b))
+    return (a.value, b.value) if r == 0 else None
+
+
+def test_plan_covers_both_parts():
+    for tiles, B, Hq, Hkv, D in ((1, 1, 8, 1, 128), (1, 16, 32, 8, 128), (2, 128, 32, 8, 128), (8, 64, 64, 8, 256), (40, 2000, 32, 8, 64)):
+        for P in (0, 1, 63, 64, 65, 1000, 8192, 32768, 10 ** 6):
+            for L in (0, 1, 64, 500, 30000):
+                for total in (0, B * L // 2):
+                    S, T = plan(tiles, B, Hq, Hkv, D, P, L, total)
+                    assert (S == 0) == (P == 0) and (T == 0) == (L == 0)
+                    assert P == 0 or (S <= -(-P // 64) and S * binding.chunk_tokens(P, S) >= P)
+                    assert L == 0 or (T <= -(-L // 64) and T * binding.chunk_tokens(L, T) >= L)
+    # explicit counts are kept, lowered where they cannot be filled
+    assert plan(2, 128, 32, 8, 128, 8192, 1024, want=(5, 3)) == (5, 3)
+    assert plan(2, 128, 32, 8, 128, 130, 10, want=(50, 3)) == (3, 1)
+    # a prefix alone fills the device; beside a large suffix it leaves SMs to it
+    alone, _ = plan(2, 128, 32, 8, 128, 8192, 0)
+    beside, _ = plan(2, 128, 32, 8, 128, 8192, 1024, 64000)
+    assert 7 <= alone <= 9 and beside < alone
+    for bad in ((-1, 4, 8, 2, 64, 10, 10), (1, -4, 8, 2, 64, 10, 10), (1, 4, 9, 2, 64, 10, 10), (1, 4, 8, 2, 64, -1, 10), (1, 4, 8, 2, 64, 10, -1)):
+        assert plan(*bad) is None
+    assert plan(1, 4, 8, 2, 64, 10, 10, want=(-1, 0)) is None
+    assert plan(1, 4, 8, 2, 64, 10, 10, sms=0) == (1, 1)
 
 
 def test_workspace():
