@@ -628,17 +628,17 @@ class SharedPlan:
     not part of it."""
 
     def __init__(self, group_sizes, Hq: int, Hkv: int, D: int, device):
-        sizes = torch.as_tensor(group_sizes, dtype=torch.int32).cpu().contiguous().reshape(-1)
+        sizes = [int(n) for n in (group_sizes.tolist() if isinstance(group_sizes, torch.Tensor) else group_sizes)]
         lib = load()
         self.Hq, self.Hkv, self.D = int(Hq), int(Hkv), int(D)
         self.seqs_per_tile = lib.dap_shared_seqs_per_tile(self.Hq, self.Hkv, self.D)
         _need(self.seqs_per_tile > 0, "Hq / Hkv must be 1, 2, 4 or 8 and D 64, 128 or 256")
-        _need(sizes.numel() > 0 and int(sizes.min()) >= 0, "group_sizes must be one or more counts >= 0")
-        self.B, self.num_groups = int(sizes.sum(dtype=torch.int64)), sizes.numel()
-        cap = sum(-(-n // self.seqs_per_tile) for n in sizes.tolist())
-        host = torch.zeros(4 * cap + self.B, dtype=torch.int32)
-        self.num_tiles = lib.dap_shared_map(_ptr(sizes), self.num_groups, self.seqs_per_tile, _ptr(host[4 * cap:]),
-                                            _ptr(host), cap)
+        _need(len(sizes) > 0 and min(sizes) >= 0 and sum(sizes) < 1 << 31, "group_sizes must be one or more counts >= 0")
+        self.B, self.num_groups = sum(sizes), len(sizes)
+        cap = sum(-(-n // self.seqs_per_tile) for n in sizes)
+        host = torch.empty(4 * cap + self.B, dtype=torch.int32)
+        self.num_tiles = lib.dap_shared_map((ctypes.c_int * len(sizes))(*sizes), self.num_groups, self.seqs_per_tile,
+                                            host.data_ptr() + 16 * cap, host.data_ptr(), cap)
         _need(self.num_tiles == cap, "invalid group_sizes")
         self.map = host.to(device)   # the tiles, then the sequences' groups
         self.tiles, self.seq_group = self.map[:4 * cap].view(cap, 4), self.map[4 * cap:]

@@ -280,6 +280,38 @@ def test_graph_replay_with_new_rows_and_runs():
     assert torch.equal(ko[:60], direct[:60]) and torch.equal(ko[60:], before)
 
 
+def test_binding_refuses():
+    k, v, codes, scale, table, indptr, pos = make([10, 20], [0, 4], 2, 64, 8, 48)
+    good = on(k, v, *codes, *scale, table, indptr, pos)
+    for i, bad in ((0, good[0].float()), (0, good[0][:-1]), (1, good[1][..., :32]), (2, good[2].float()), (3, good[3][:-1]),
+                   (4, good[4].float()), (5, good[5][:, :1]), (6, good[6].long()), (6, good[6][:1]), (7, good[7][:2]),
+                   (8, good[8].long())):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            binding.kv_append_paged_fp8_multi(*args)
+        if i >= 2:
+            with pytest.raises(ValueError):
+                binding.kv_read_paged_fp8(*args[2:], total_tokens=30)
+    for i in range(9):
+        args = list(good)
+        args[i] = args[i].cpu()
+        with pytest.raises(binding.DapError):
+            binding.kv_append_paged_fp8_multi(*args)
+    with pytest.raises(ValueError):
+        binding.kv_read_paged_fp8(*good[2:])
+    with pytest.raises(ValueError):
+        binding.kv_read_paged_fp8(*good[2:], total_tokens=-1)
+    with pytest.raises(ValueError):
+        binding.kv_read_paged_fp8(*good[2:], total_tokens=30, k_out=good[0][:-1])
+    # rows whose strides break the 16-byte rule
+    odd = torch.zeros((30, 2, 68), dtype=torch.bfloat16, device="cuda")[..., :64]
+    with pytest.raises(binding.DapError) as e:
+        binding.kv_append_paged_fp8_multi(odd, odd, *good[2:])
+    assert e.value.status == 5
+    assert binding.get_device_errors() == 0
+
+
 def test_two_streams_at_once():
     cases = [make([200, 300], [0, 5], 8, 128, 16, 46 + j) for j in range(2)]
     dev = [on(c[0], c[1], *c[2], *c[3], *c[4:]) for c in cases]

@@ -319,6 +319,59 @@ def test_append_then_decode_without_waiting():
     assert binding.get_device_errors() == 0
 
 
+def test_lengths_that_grow_in_place():
+    """One tensor of lengths, advanced on the device between calls that are queued without waiting: every kernel of a call
+    sees the lengths of its step."""
+    c = Case([16], [128], [90] * 16, 8, 2, 128, 16)
+    full = c.lens.clone()
+    c.lens.fill_(128)
+    outs = []
+    for _ in range(90):
+        c.lens += 1
+        outs.append(c.run(max_suffix_len=90))
+    torch.cuda.synchronize()
+    assert torch.equal(c.lens, full)
+    for i in (0, 1, 2, 30, 31, 32, 63, 64, 88, 89):
+        c.lens.fill_(128 + i + 1)
+        c.check(outs[i], c.plain(), f"step {i}")
+    assert binding.get_device_errors() == 0
+
+
+def test_binding_refuses():
+    c = Case([4], [40], [5] * 4, 8, 2, 64, 16)
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    bad = [dict(q=c.q.float()), dict(q=c.q[:3]), dict(q=c.q[..., ::2]), dict(k=c.k.float()), dict(v=c.v[:-1]),
+           dict(table=c.table.long()), dict(table=c.table[:3]), dict(lens=c.lens.long()), dict(lens=c.lens[:3].contiguous()),
+           dict(prefix=torch.zeros(2, dtype=torch.int32, device="cuda"))]
+    for change in bad:
+        kept = {n: getattr(c, n) for n in change}
+        for n, t in change.items():
+            setattr(c, n, t)
+        with pytest.raises(ValueError):
+            c.run()
+        for n, t in kept.items():
+            setattr(c, n, t)
+    for kw in (dict(out=torch.empty((4, 8, 32), dtype=torch.bfloat16, device="cuda")), dict(out=c.q.float()),
+               dict(workspace=torch.empty((1 << 16, 2), dtype=torch.uint8, device="cuda")[:, 0]), dict(max_prefix_len=-1),
+               dict(prefix_splits=-1)):
+        with pytest.raises(ValueError):
+            c.run(**kw)
+    for kw, status in ((dict(workspace=ws), 4), (dict(max_prefix_len=c.table.shape[1] * 16 + 1), 2),
+                       (dict(max_suffix_len=c.table.shape[1] * 16 + 1), 2), (dict(scale=float("inf")), 2)):
+        with pytest.raises(binding.DapError) as e:
+            c.run(**kw)
+        assert e.value.status == status
+    for n in ("q", "table", "lens"):
+        kept = getattr(c, n)
+        setattr(c, n, kept.cpu())
+        with pytest.raises(binding.DapError) as e:
+            c.run()
+        assert e.value.status is None
+        setattr(c, n, kept)
+    c.check(c.run(), c.plain())
+    assert binding.get_device_errors() == 0
+
+
 def test_graphs_that_share_a_workspace():
     """Two captured steps on one workspace, replayed with other lengths and prefixes than those captured, and on another
     stream; the bounds hold for all of them."""
