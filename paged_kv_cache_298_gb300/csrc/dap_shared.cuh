@@ -10,9 +10,13 @@
 //   * suffix: positions P_g .. L_b of each sequence, the split schedule of the single-token decode.
 // Each part is cut into splits that leave (acc, m, l) partials in the workspace, [B][prefix splits +
 // suffix splits][Hq][D] then [..][2], and a combine kernel merges a row's partials in that order.
-// The suffix kernel does not wait for the prefix kernel: it starts beside it as soon as every
-// prefix CTA runs (programmatic dependent launch), and one of its CTAs waits for the prefix
-// kernel's end before it exits, so that the combine, which waits for the suffix kernel, finds both.
+// The suffix kernel does not wait for the prefix kernel: it starts beside it, on the SMs that the prefix
+// leaves free, as soon as every prefix CTA runs (programmatic dependent launch), and one of its CTAs waits
+// for the prefix kernel's end before it exits, so that the combine, which waits for the suffix kernel, finds
+// both.  The prefix is bound by its products, the suffix by memory: run side by side they use both.  How many
+// SMs each gets is a matter of the prefix's split count, which dap_shared_plan chooses for both to end
+// together: 64 sequences behind 32768 shared keys, 64 .. 2048 of their own (64 query heads, 8 kv heads, D = 128),
+// 96 SMs and 56: 85 us; the prefix on all SMs, then the suffix: 110 us.
 #pragma once
 
 #include "dap_decode.cuh"
@@ -64,8 +68,8 @@ __device__ __forceinline__ int suffix_count(const SharedParams &p, const Span &s
 }
 
 // Page ids of a producer warp: lane l holds entries base + l and base + 32 + l of the sequence's table row, so that a
-// load of 32 entries serves 32 pages and is in flight while the 32 before it are used.  (A load per tile, looked at
-// or only moved to another register a tile later, held the warp for its latency: 1370 cycles a tile.)
+// load of 32 entries serves 32 pages and is in flight while the 32 before it are used.  (A page id that was loaded for
+// the next tile and range-checked at once held the warp for the load's latency: 0.3 us a tile.)
 struct PageWindow {
     const int32_t *row;
     int base, end, lane;
@@ -92,8 +96,9 @@ struct PageWindow {
 
 template <int D_, int G_, bool GATHER_>
 struct SuffixCfg {
-    // 32-key tiles and two consumer warps: 54 KB and three warps, so that one CTA fits beside a prefix CTA
-    // (164 KB, 11 warps) at D <= 128, and four share an SM without one
+    // 32-key tiles and two consumer warps, 54 KB: four CTAs share an SM (D = 256: two), so that one's start and end
+    // are covered by the others.  128 sequences of 16 .. 1024 keys, D = 128: 42.6 us (0.93 of the copy rate, combine
+    // included), against 58 us with 64-key tiles and two CTAs of 107 KB.
     static constexpr int D = D_, G = G_, HG = 1, NWC = 2, BT = 32, NS = D == 64 ? 6 : 3, MINB = D == 256 ? 2 : 4;
     static constexpr bool GATHER = GATHER_, SWZ = true;
     static constexpr int KPW = BT / NWC;

@@ -10,22 +10,27 @@
 //                  keys.  K tiles are column block major, [D / 64][64 keys][128 bytes], as the product with
 //                  N = 64 keys wants its 8-key groups one stride apart: a copy per page run and column block (one in
 //                  all for page sizes that are multiples of 64).  V tiles are made of one box per page run,
-//                  [D / 64][R keys][128 bytes], since a product takes 16 keys of V at a time: half the copies, each
-//                  of which costs the TMA unit about 80 cycles beside one per 128 bytes (16 copies of a tile at a
-//                  page size of 16: 1600 cycles).  Row gather: both column block major;
+//                  [D / 64][R keys][128 bytes], since a product takes 16 keys of V at a time: half the copies.
+//                  Row gather: both column block major;
 //   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
 //                                  P (bf16 pairs) overwrites the first 32 once they are read;
 //                               O  columns [256 + x D, + D)  fp32 accumulator.
 // Two CTAs whose tiles are of the same group form a cluster: one copies every K tile, the other every V tile, to
 // both (TMA multicast), so that each tile is read from L2 once for both.
-// Warps: four softmax warps a stream (thread = row), a producer, one a stream that issues its scores and one that
-// issues the products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores are there when the
-// softmax gets to them.
-// (Measured, D = 128, cycles of a 64-key tile of 256 rows, whose products take 1344: one score buffer a stream,
-// every step of the chain S, softmax, PV waiting for the last: 3130; two buffers and one issuing warp a stream:
-// 2100, as PV(n) has to end before the same warp can go on to S(n + 2); one warp for everything in the order
-// PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as a wait on a barrier takes 60 cycles even when it is
-// complete and a commit 55, all of them in line; one warp for all scores: 2100, the same again.)
+// Warps: four softmax warps a stream (thread = row), a producer each for K and V, one a stream that issues its
+// scores and one that issues all products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores
+// are there when the softmax gets to them.
+// Bound: the products.  At D = 128 those of a 64-key tile of 256 rows take 1344 cycles (a microbenchmark: 50 an S
+// product, N = 64, whose operands both come from shared memory, 66 a PV product, N = 128); a tile takes 1450
+// (0.77 us, 11 TFLOP/s an SM), with at most 128 rows 0.44 us at page sizes that are multiples of 64 and 0.65 at 16,
+// where the producers' copies bound it; 0.87 us at D = 256 (128 rows).
+// Why these warps (cycles of a tile at the time, D = 128): one score buffer a stream, every step of the chain S,
+// softmax, PV waiting for the last: 3130; two buffers, one issuing warp a stream: 2100, as PV(n) has to end before
+// the same warp can go on to S(n + 2); one warp for everything, PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as
+// a wait on a barrier takes 60 cycles even when it is complete and a commit 55, all of them in line; one warp for the
+// scores of both: 1990; one producer warp for K and V: 1800, and 0.72 us a tile whatever its rows.
+// L2 prefetch of later tiles, by TMA or by loads, measured slower (prefix alone 71 against 90 us): it takes the
+// producers' time, and the ring already covers the latency.
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
 // when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
 // weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
@@ -53,11 +58,12 @@ struct PrefixCfg {
     static constexpr int NBAR = 4 * NS + 17;
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr int USED = MISC_OFF + 32 + 1024;  // + slack to align the base to 1024
-    // more than half an SM's shared memory, so that two prefix CTAs never share an SM (the second would wait for
-    // tensor memory); at D <= 128 one suffix CTA fits beside the one there is
-    static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
+    // More than half an SM's shared memory, so that two prefix CTAs never share an SM (the second would wait for
+    // tensor memory).  A ring small enough for a suffix CTA beside it (three tiles at D = 128) measured slower: the
+    // two slow each other down by more than the suffix CTA gets done.
+    static constexpr int SMEM = USED;
     static constexpr int ROW_F = D + 4;  // floats of a row of sums on its way out (the 4: no bank conflicts)
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "shared memory");
     static_assert(NSTREAM * 128 * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
@@ -189,8 +195,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const bool ragged = work && nlast % 16 != 0;     // its V rows up to a multiple of 16 are zeroed
 
     if (work && (warp == C::PRODUCER || warp == C::PRODUCER + 1)) {
-        // A producer warp each for K and V.  (The chain of instructions of a tile, barrier, page, copy, takes a warp some
-        // 700 cycles a tensor, whatever the copies' size: one warp for both held a tile at 1370 to 1600 cycles.)
+        // A producer warp each for K and V: a tile's chain of barrier, page and copy takes a warp some 700 cycles a
+        // tensor, whatever the size of the copies.
         const int tensor = warp - C::PRODUCER;
         const int32_t *table = p.block_table + (long long)q0 * p.max_pages;
         const int R = p.box_rows;
