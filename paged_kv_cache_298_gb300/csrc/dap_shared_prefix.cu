@@ -215,13 +215,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
         };
         if constexpr (C::GATHER) {
-            RowPages<C> rp_next;
-            lookup_rows<C>(rp_next, table, tok0, min(BT, tok1 - tok0), p.page_size, lane);
+            RowWalk<C> walk(table, tok0, p, lane);
             load_q();
             for (; done < J; ++done) {
                 const int st = done % NS, t = tok0 + done * BT;
-                const RowPages<C> rp = rp_next;
-                if (done + 1 < J) lookup_rows<C>(rp_next, table, t + BT, min(BT, tok1 - t - BT), p.page_size, lane);
+                RowPages<C> rp;
+                walk.next(rp);
                 if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
                 fill_rows<C>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, rp, min(BT, tok1 - t), kvh, p,
                              &full[st], lane);
