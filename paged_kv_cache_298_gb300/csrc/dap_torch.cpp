@@ -159,7 +159,7 @@ void append_runs(PyObject *const *a) {
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     void *stream = stream_of(a[9], c.device);
     dap_status st;
-    Py_BEGIN_ALLOW_THREADS;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = kv_append_paged_fp8_multi(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                                    const_cast<uint8_t *>(r.codes[0]), const_cast<uint8_t *>(r.codes[1]), r.scale[0],
                                    r.scale[1], r.P, r.ps, r.table, r.max_pages, r.indptr, r.positions, T, r.B, r.Hkv,
@@ -181,6 +181,7 @@ PyObject *read_runs(PyObject *const *a) {
     else if (given[0] || given[1]) T = (given[0] ? given[0] : given[1])->size(0);
     else value_error("total_tokens is needed when no output is given");
     if (T < 0) value_error("total_tokens must not be negative");
+    fit(T, "too many tokens");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     for (int i = 0; i < 2; ++i) {
         if (given[i]) {
@@ -195,9 +196,9 @@ PyObject *read_runs(PyObject *const *a) {
     }
     void *stream = stream_of(a[10], c.device);
     dap_status st;
-    Py_BEGIN_ALLOW_THREADS;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = kv_read_paged_fp8(r.codes[0], r.codes[1], r.scale[0], r.scale[1], r.P, r.ps, r.table, r.max_pages, r.indptr,
-                           r.positions, fit(T, "too many tokens"), r.B, r.Hkv, r.D, out[0].data_ptr(),
+                           r.positions, (int)T, r.B, r.Hkv, r.D, out[0].data_ptr(),
                            out[1].data_ptr(), out[0].stride(0), out[0].stride(1), out[1].stride(0), out[1].stride(1),
                            stream);
     Py_END_ALLOW_THREADS;
@@ -233,6 +234,8 @@ PyObject *decode_shared(PyObject *const *a) {
     table_of(bt, B);
     if (!int32s(sl) || sl.numel() != B) value_error("seq_lens must be contiguous int32 [B]");
     if (!int32s(pl) || pl.numel() != groups) value_error("prefix_lens must be contiguous int32 [num_groups]");
+    const int P = fit(k.size(0), "too many pages"), ps = fit(k.size(1), "page size too large");
+    const int max_pages = fit(bt.size(1), "block_table too wide");
     const int max_prefix = integer32(a[8]), max_suffix = integer32(a[9]);
     const int pre = integer32(PyTuple_GET_ITEM(a[10], 0)), suf = integer32(PyTuple_GET_ITEM(a[10], 1));
     const double scale = PyFloat_AsDouble(a[11]);
@@ -252,13 +255,11 @@ PyObject *decode_shared(PyObject *const *a) {
     const int32_t *m = static_cast<const int32_t *>(map.data_ptr());
     void *stream = stream_of(a[14], c.device);
     dap_status st;
-    Py_BEGIN_ALLOW_THREADS;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = decode_attn_paged_shared(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), fit(k.size(0), "too many pages"),
-        fit(k.size(1), "page size too large"), static_cast<const int32_t *>(bt.data_ptr()),
-        fit(bt.size(1), "block_table too wide"), static_cast<const int32_t *>(sl.data_ptr()),
-        static_cast<const int32_t *>(pl.data_ptr()), m + 4 * (int64_t)tiles, m,
-        groups, tiles, d[6], max_prefix, max_suffix, B, Hq, Hkv, D, (float)scale, pre, suf, ws.data_ptr(), ws.nbytes(),
+        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), P, ps,
+        static_cast<const int32_t *>(bt.data_ptr()), max_pages, static_cast<const int32_t *>(sl.data_ptr()),
+        static_cast<const int32_t *>(pl.data_ptr()), m + 4 * (int64_t)tiles, m, groups, tiles, d[6], max_prefix, max_suffix, B, Hq, Hkv, D, (float)scale, pre, suf, ws.data_ptr(), ws.nbytes(),
         out.data_ptr(), out.stride(0), out.stride(1), stream);
     Py_END_ALLOW_THREADS;
     check_status(st, what);

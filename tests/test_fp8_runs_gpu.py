@@ -304,6 +304,13 @@ def test_binding_refuses():
         binding.kv_read_paged_fp8(*good[2:], total_tokens=-1)
     with pytest.raises(ValueError):
         binding.kv_read_paged_fp8(*good[2:], total_tokens=30, k_out=good[0][:-1])
+    # more rows than 32 bits count, refused before anything else happens
+    many = good[0][:1].expand(2 ** 31, 2, 64)
+    for call in (lambda: binding.kv_append_paged_fp8_multi(many, many, *good[2:]),
+                 lambda: binding.kv_read_paged_fp8(*good[2:], k_out=many, v_out=many),
+                 lambda: binding.kv_read_paged_fp8(*good[2:], total_tokens=2 ** 31)):
+        with pytest.raises(ValueError):
+            call()
     # rows whose strides break the 16-byte rule
     odd = torch.zeros((30, 2, 68), dtype=torch.bfloat16, device="cuda")[..., :64]
     with pytest.raises(binding.DapError) as e:

@@ -343,6 +343,8 @@ def test_binding_refuses():
     bad = [dict(q=c.q.float()), dict(q=c.q[:3]), dict(q=c.q[..., ::2]), dict(k=c.k.float()), dict(v=c.v[:-1]),
            dict(table=c.table.long()), dict(table=c.table[:3]), dict(lens=c.lens.long()), dict(lens=c.lens[:3].contiguous()),
            dict(prefix=torch.zeros(2, dtype=torch.int32, device="cuda"))]
+    empty = torch.empty((2 ** 31, 0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    bad.append(dict(k=empty, v=empty))   # more pages than 32 bits count
     for change in bad:
         kept = {n: getattr(c, n) for n in change}
         for n, t in change.items():
