@@ -85,13 +85,24 @@ int integer32(PyObject *o) {
     return (int)v;
 }
 
-// The given stream handle, or the device's current stream.
-void *stream_of(PyObject *o, int device) {
-    if (o == Py_None) return static_cast<void *>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
-    void *p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw Raised();
-    return p;
-}
+// The call's device and stream (a given handle, or the device's current stream) made current: what the call
+// allocates belongs to the stream that its kernels run on, so that a workspace freed here is not handed to another
+// stream while they run.
+struct On {
+    c10::cuda::CUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard given;
+    void *stream;
+    On(PyObject *o, int index) : device((c10::DeviceIndex)index) {
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+            return;
+        }
+        stream = PyLong_AsVoidPtr(o);
+        if (!stream && PyErr_Occurred()) throw Raised();
+        given.reset_stream(
+            c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)index));
+    }
+};
 
 int fit(int64_t n, const char *msg) {
     if (n > INT32_MAX) value_error(msg);
@@ -156,14 +167,13 @@ void append_runs(PyObject *const *a) {
     if (v.sizes() != k.sizes() || k.size(1) != r.Hkv || k.size(2) != r.D)
         value_error("cache heads / dims differ from the new rows");
     const int T = fit(k.size(0), "too many tokens");
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-    void *stream = stream_of(a[9], c.device);
+    const On on(a[9], c.device);
     dap_status st;
     Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = kv_append_paged_fp8_multi(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                                    const_cast<uint8_t *>(r.codes[0]), const_cast<uint8_t *>(r.codes[1]), r.scale[0],
                                    r.scale[1], r.P, r.ps, r.table, r.max_pages, r.indptr, r.positions, T, r.B, r.Hkv,
-                                   r.D, stream);
+                                   r.D, on.stream);
     Py_END_ALLOW_THREADS;
     check_status(st, what);
 }
@@ -182,7 +192,7 @@ PyObject *read_runs(PyObject *const *a) {
     else value_error("total_tokens is needed when no output is given");
     if (T < 0) value_error("total_tokens must not be negative");
     fit(T, "too many tokens");
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+    const On on(a[10], c.device);
     for (int i = 0; i < 2; ++i) {
         if (given[i]) {
             rows3(*given[i], "k_out and v_out must be bf16 [*, *, D] tensors with unit stride in D");
@@ -194,13 +204,12 @@ PyObject *read_runs(PyObject *const *a) {
                                at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, (c10::DeviceIndex)c.device));
         }
     }
-    void *stream = stream_of(a[10], c.device);
     dap_status st;
     Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = kv_read_paged_fp8(r.codes[0], r.codes[1], r.scale[0], r.scale[1], r.P, r.ps, r.table, r.max_pages, r.indptr,
                            r.positions, (int)T, r.B, r.Hkv, r.D, out[0].data_ptr(),
                            out[1].data_ptr(), out[0].stride(0), out[0].stride(1), out[1].stride(0), out[1].stride(1),
-                           stream);
+                           on.stream);
     Py_END_ALLOW_THREADS;
     check_status(st, what);
     PyObject *k = THPVariable_Wrap(out[0]), *v = THPVariable_Wrap(out[1]);
@@ -210,8 +219,9 @@ PyObject *read_runs(PyObject *const *a) {
     return both;
 }
 
-// decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, the plan's map [tiles, then seq_group], (B, Hq, Hkv, D, groups, tiles, seqs_per_tile), max_prefix_len,
-// max_suffix_len, (prefix_splits, suffix_splits), scale, workspace, out, stream) -> out
+// decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, the plan's map [tiles, then seq_group],
+// (B, Hq, Hkv, D, groups, tiles, seqs_per_tile), max_prefix_len, max_suffix_len, (prefix_splits, suffix_splits), scale,
+// workspace, out, stream) -> out
 PyObject *decode_shared(PyObject *const *a) {
     const char *what = "decode_attn_paged_shared";
     Call c{what};
@@ -240,27 +250,26 @@ PyObject *decode_shared(PyObject *const *a) {
     const int pre = integer32(PyTuple_GET_ITEM(a[10], 0)), suf = integer32(PyTuple_GET_ITEM(a[10], 1));
     const double scale = PyFloat_AsDouble(a[11]);
     if (scale == -1.0 && PyErr_Occurred()) throw Raised();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-    const at::TensorOptions on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)c.device);
+    const On on(a[14], c.device);
+    const at::TensorOptions opts = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)c.device);
     at::Tensor out, ws;
     if (og) {
         rows3(*og, "out must be a bf16 [*, *, D] tensor with unit stride in D");
         if (og->sizes() != q.sizes()) value_error("out must be [B, Hq, D]");
         out = *og;
     } else {
-        out = at::empty({B, Hq, D}, on.dtype(at::kBFloat16));
+        out = at::empty({B, Hq, D}, opts.dtype(at::kBFloat16));
     }
-    ws = wg ? *wg : at::empty({(int64_t)dap_workspace_bytes_shared(B, Hq, D, pre, suf)}, on.dtype(at::kByte));
+    ws = wg ? *wg : at::empty({(int64_t)dap_workspace_bytes_shared(B, Hq, D, pre, suf)}, opts.dtype(at::kByte));
     if (!ws.is_contiguous()) value_error("workspace must be contiguous");
     const int32_t *m = static_cast<const int32_t *>(map.data_ptr());
-    void *stream = stream_of(a[14], c.device);
     dap_status st;
     Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
     st = decode_attn_paged_shared(
         q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), P, ps,
         static_cast<const int32_t *>(bt.data_ptr()), max_pages, static_cast<const int32_t *>(sl.data_ptr()),
         static_cast<const int32_t *>(pl.data_ptr()), m + 4 * (int64_t)tiles, m, groups, tiles, d[6], max_prefix, max_suffix, B, Hq, Hkv, D, (float)scale, pre, suf, ws.data_ptr(), ws.nbytes(),
-        out.data_ptr(), out.stride(0), out.stride(1), stream);
+        out.data_ptr(), out.stride(0), out.stride(1), on.stream);
     Py_END_ALLOW_THREADS;
     check_status(st, what);
     return THPVariable_Wrap(out);

@@ -430,6 +430,32 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(o, alone[i % 2])
 
 
+def test_a_given_stream_keeps_what_the_call_allocates():
+    """The call's own workspace is not handed to the current stream while the given stream still uses it."""
+    c = Case([20], [300], [7 * j for j in range(20)], 8, 2, 128, 16, seed=6)
+    want = c.run()
+    n = binding.workspace_bytes_shared(c.plan, max_prefix_len=c.max_prefix, max_suffix_len=c.max_suffix)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)   # (some milliseconds)
+        got = c.run(stream=side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert torch.equal(got, want)
+        del junk
+
+
+def test_q_whose_heads_are_further_apart_than_its_sequences():
+    c = Case([40], [150], [3] * 40, 16, 2, 128, 16, seed=7)
+    want = c.run()
+    c.q = c.q.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    out = torch.empty((16, 40, 128), dtype=torch.bfloat16, device="cuda").permute(1, 0, 2)
+    assert torch.equal(c.run(out=out), want)
+
+
 def test_store_restore_and_decode():
     """The operators together: a prompt is quantised into the e4m3 cache, read back into a run of bf16 pages, and shared by a
     batch whose sequences append their own tokens behind it."""
