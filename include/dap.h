@@ -430,11 +430,12 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
                                     const void *k_cache, const void *v_cache, int num_pages,
                                     int page_size, const int32_t *block_table, int max_pages,
                                     const int32_t *seq_lens, const int32_t *prefix_lens,
-                                    const int32_t *seq_group, const int32_t *tiles, int num_groups, int num_tiles, int seqs_per_tile,
-                                    int max_prefix_len, int max_suffix_len, int B, int Hq, int Hkv,
-                                    int D, float scale, int prefix_splits, int suffix_splits,
-                                    void *workspace, size_t workspace_bytes, void *out,
-                                    long long out_stride_b, long long out_stride_h, void *stream);
+                                    const int32_t *seq_group, const int32_t *tiles, int num_groups,
+                                    int num_tiles, int seqs_per_tile, int max_prefix_len,
+                                    int max_suffix_len, int B, int Hq, int Hkv, int D, float scale,
+                                    int prefix_splits, int suffix_splits, void *workspace,
+                                    size_t workspace_bytes, void *out, long long out_stride_b,
+                                    long long out_stride_h, void *stream);
 
 /*
  * fp8 sliding-window latent decode, K = V [C].

@@ -633,7 +633,8 @@ class SharedPlan:
         self.Hq, self.Hkv, self.D = int(Hq), int(Hkv), int(D)
         self.seqs_per_tile = lib.dap_shared_seqs_per_tile(self.Hq, self.Hkv, self.D)
         _need(self.seqs_per_tile > 0, "Hq / Hkv must be 1, 2, 4 or 8 and D 64, 128 or 256")
-        _need(len(sizes) > 0 and min(sizes) >= 0 and sum(sizes) < 1 << 31, "group_sizes must be one or more counts >= 0")
+        _need(len(sizes) > 0 and min(sizes) >= 0 and sum(sizes) < 1 << 31,
+              "group_sizes must be one or more counts >= 0")
         self.B, self.num_groups = sum(sizes), len(sizes)
         cap = sum(-(-n // self.seqs_per_tile) for n in sizes)
         host = torch.empty(4 * cap + self.B, dtype=torch.int32)
@@ -654,6 +655,7 @@ class SharedPlan:
         # lengths that grow by a token a step keep their plan: rounded up to 64, or to an eighth of themselves
         max_suffix_len, total_suffix = (n + -n % max(64, 1 << max(0, n.bit_length() - 4)) for n in
                                         (max_suffix_len, total_suffix))
+        max_suffix_len = min(max_suffix_len, 0x7FFFFFFF)
         key = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
         last, found = self._last
         if last == key:
@@ -693,7 +695,8 @@ def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_
     if scale is None:
         scale = 1.0 / math.sqrt(plan.D)
     dev = q.get_device()
-    S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits), int(suffix_splits), dev)
+    S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits),
+                    int(suffix_splits), dev)
     return _native().decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan.map, plan.sizes,
                                    int(max_prefix_len), int(max_suffix_len), S, scale, workspace, out,
                                    None if stream is None else _stream(stream, dev))
@@ -782,8 +785,8 @@ def kv_append_paged_fp8_multi(k_new, v_new, k_codes, v_codes, k_scale, v_scale, 
     return k_codes, v_codes, k_scale, v_scale
 
 
-def kv_read_paged_fp8(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, *, total_tokens: int | None = None,
-                      k_out=None, v_out=None, stream=None):
+def kv_read_paged_fp8(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, *,
+                      total_tokens: int | None = None, k_out=None, v_out=None, stream=None):
     """Read runs of the e4m3 GQA cache back as bf16 rows (include/dap.h: kv_read_paged_fp8).
     Runs as kv_append_paged_fp8_multi; ``total_tokens`` (the host's copy of indptr[B]) sizes the
     outputs when they are not given.  Returns (k_out, v_out) [total_tokens, Hkv, D]; rows outside

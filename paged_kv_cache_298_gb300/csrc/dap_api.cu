@@ -530,8 +530,8 @@ int dap_shared_map(const int32_t *group_sizes, int num_groups, int seqs_per_tile
 
 int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, int max_prefix_len, int max_suffix_len,
                     long long total_suffix, int *prefix_splits, int *suffix_splits) {
-    if (num_tiles < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || max_prefix_len < 0 || max_suffix_len < 0 ||
-        !prefix_splits || !suffix_splits || *prefix_splits < 0 || *suffix_splits < 0)
+    if (num_tiles < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || max_prefix_len < 0 ||
+        max_suffix_len < 0 || !prefix_splits || !suffix_splits || *prefix_splits < 0 || *suffix_splits < 0)
         return -1;
     const int sms = std::max(1, sm_count);
     if (total_suffix <= 0) total_suffix = (long long)B * max_suffix_len;
@@ -603,8 +603,9 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
 dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long long q_stride_h, const void *k_cache,
                                     const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
                                     int max_pages, const int32_t *seq_lens, const int32_t *prefix_lens,
-                                    const int32_t *seq_group, const int32_t *tiles, int num_groups, int num_tiles, int seqs_per_tile, int max_prefix_len, int max_suffix_len, int B,
-                                    int Hq, int Hkv, int D, float scale, int prefix_splits, int suffix_splits,
+                                    const int32_t *seq_group, const int32_t *tiles, int num_groups, int num_tiles,
+                                    int seqs_per_tile, int max_prefix_len, int max_suffix_len, int B, int Hq, int Hkv,
+                                    int D, float scale, int prefix_splits, int suffix_splits,
                                     void *workspace, size_t workspace_bytes, void *out, long long out_stride_b,
                                     long long out_stride_h, void *stream) {
     if (prefix_splits < 0 || prefix_splits > 65536 || suffix_splits < 0 || num_groups < 0 || num_tiles < 0 ||

@@ -96,14 +96,6 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// Bring a 5-D tile into L2.
-__device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4) {
-    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-                 : "memory");
-}
-
 // The same to this place in every CTA of `mask` (cluster ranks), completing `bytes` on the barrier at `bar`'s
 // place in each.
 __device__ __forceinline__ void tma_load_5d_multicast(void *dst, const CUtensorMap *map, int c0, int c1, int c2,

@@ -44,7 +44,8 @@ __device__ __forceinline__ int find_run(const int32_t *indptr, int B, int r, int
 }
 
 // Slot of the pool (page * page_size + slot in the page) of tokens r0 .. r0 + n - 1, one per thread of the
-// first warps: -1 where the row is in no run, -2 where its position or page is outside (flagged); and the slot in its page.
+// first warps: -1 where the row is in no run, -2 where its position or page is outside (flagged); and the slot in
+// its page.
 struct Places {
     long long row[kMaxTT];
     int slot[kMaxTT];

@@ -92,9 +92,9 @@ struct PageWindow {
     }
 };
 
-// The rows of a row-gather tile by the same window: lane l holds rows l, l + 32, .. of tile after tile, with no division
-// after the first.  (A prefix tile at page size 12 against a table read a row: 0.65 us for 0.81 at D = 64, 1.27 for 1.35
-// at D = 256, 1.61 for 1.50 at D = 128.)
+// The rows of a row-gather tile by the same window: lane l holds rows l, l + 32, .. of tile after tile, with no
+// division after the first.  (A prefix tile at page size 12 against a table read a row: 0.65 us for 0.81 at D = 64,
+// 1.27 for 1.35 at D = 256, 1.61 for 1.50 at D = 128.)
 template <class C>
 struct RowWalk {
     static constexpr int N = RowPages<C>::N;

@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 RowPages<C> rp;
                 walk.next(rp);
                 if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
-                fill_rows<C>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, rp, min(BT, tok1 - t), kvh, p,
-                             &full[st], lane);
+                fill_rows<C>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, rp, min(BT, tok1 - t), kvh,
+                             p, &full[st], lane);
             }
         } else {
             // K: lane = (box j, column block cb), or a whole tile where a page has one; V: lane = box, all blocks.  A
@@ -684,8 +684,8 @@ dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);
     const cudaError_t e =
-        cl == 2 ? launch_cluster_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, 2, stream, mq, mk,
-                                                mv, p, a.Hq / a.Hkv, cl)
+        cl == 2 ? launch_cluster_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, 2, stream, mq,
+                                                mk, mv, p, a.Hq / a.Hkv, cl)
                 : launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p,
                                         a.Hq / a.Hkv, cl);
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;

@@ -106,6 +106,14 @@ def test_plan_covers_both_parts():
     assert plan(1, 4, 8, 2, 64, 10, 10, sms=0) == (1, 1)
 
 
+def test_bounds_up_to_32_bits():
+    p = binding.SharedPlan([2], 8, 2, 64, "cpu")
+    for n in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 30 + 1):
+        assert min(p.splits(64, n, prefix_splits=1, suffix_splits=1)) == 1
+    with pytest.raises(ValueError):
+        p.splits(-1, 64)
+
+
 def test_workspace():
     w = binding.load().dap_workspace_bytes_shared
     assert w(4, 32, 128, 0, 0) == 0
