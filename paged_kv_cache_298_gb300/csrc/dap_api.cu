@@ -539,7 +539,7 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
     if (max_suffix_len == 0) *suffix_splits = 0;
     const bool prefix = max_prefix_len > 0, suffix = max_suffix_len > 0;
     if (prefix && (*prefix_splits == 0 || (suffix && *suffix_splits == 0))) {
-        // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM, run on the others meanwhile, and on all of
+        // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM (two at D = 256), run on the others meanwhile, and on all of
         // them afterwards.  The pair of counts with the least time by this model, in microseconds, as measured: 8 to
         // start and end a prefix CTA, 0.78 a 64-key tile (0.55 with at most 128 rows, 0.95 at D = 256); 4 to start
         // and end a suffix CTA and 0.4 for 32 keys; suffix K/V at 0.066 MB/us an SM, 6.6 MB/us in all; partial rows
@@ -561,7 +561,7 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
                 double us = bandwidth;
                 if (suffix) {
                     const double cta = 4. + 0.4 * (double)ceil_div_ll(ceil_div_ll(max_suffix_len, m), 32);
-                    const double waves = (double)B * Hkv * m / (4. * (double)(free > 0 ? free : sms));
+                    const double waves = (double)B * Hkv * m / ((D == 256 ? 2. : 4.) * (double)(free > 0 ? free : sms));
                     us = std::max(us, (free > 0 ? 0. : t) + cta * std::max(1., waves));
                 }
                 us += merge * (double)(n + m);
@@ -671,8 +671,9 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
     a.o_sh = out_stride_h;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (prefix_splits > 0 && (st = launch_shared_prefix(a, cs)) != DAP_OK) return st;
-    if (suffix_splits > 0 && (st = launch_shared_suffix(a, cs)) != DAP_OK) return st;
-    return launch_shared_combine(a, cs);
+    bool merged = false;
+    if (suffix_splits > 0 && (st = launch_shared_suffix(a, cs, &merged)) != DAP_OK) return st;
+    return merged ? DAP_OK : launch_shared_combine(a, cs);
 }
 
 static dap_status fp8_runs(bool write, const void *k_rows, const void *v_rows, long long k_stride_t,

@@ -131,8 +131,9 @@ struct SharedArgs {
     long long o_sb, o_sh;
 };
 dap_status launch_shared_prefix(const SharedArgs &a, cudaStream_t stream);
-dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream);
-dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream);
+// (*merged: the kernel merges and writes the rows itself, no combine follows)
+dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream, bool *merged);
+dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream, bool *merged);
 dap_status launch_shared_combine(const SharedArgs &a, cudaStream_t stream);
 bool read_errors_shared_prefix(unsigned int *flags, bool clear);
 bool read_errors_shared_suffix(unsigned int *flags, bool clear);

@@ -19,6 +19,8 @@
 // 96 SMs and 56: 85 us; the prefix on all SMs, then the suffix: 110 us.
 #pragma once
 
+#include <algorithm>
+
 #include "dap_decode.cuh"
 
 namespace dap {
@@ -28,6 +30,7 @@ struct SharedParams {
     const int32_t *prefix_lens, *seq_group, *tiles;
     int num_groups, num_tiles, seqs_per_tile, max_prefix_len, max_suffix_len;
     int prefix_splits, prefix_chunk, total_splits;
+    int merge;  // the suffix kernel merges and writes the rows (no combine)
     float *o_part, *ml_part;
 };
 
@@ -150,7 +153,93 @@ struct SuffixCfg {
     static constexpr int BAR_OFF = (MISC_OFF + 16 + 7) & ~7;
     static constexpr int SMEM = BAR_OFF + 2 * NS * 8 + 1024;  // + slack to align the base
     static constexpr int THREADS = (NWC + 1) * 32;
+    // Merging: prefix partials that a warp has in flight for each of the G heads, 64 values a lane.
+    static constexpr int MERGE_FIT = 64 / (G * (D / 32)), MERGE_NB = MERGE_FIT < 1 ? 1 : MERGE_FIT > 8 ? 8 : MERGE_FIT;
 };
+
+// The prefix partials of the CTA's G heads, merged with its own sums (`sums` + 3 G (D + 2) floats, made by the
+// consumers when `mine`): warp w takes partials w, w + 3, ..., then the warps' sums and the suffix's are added.
+template <class C>
+__device__ __forceinline__ void merge_rows(const SharedParams &pp, float *sums, int b, int kvh, int np, bool mine) {
+    constexpr int G = C::G, D = C::D, DPV = D / 32, NB = C::MERGE_NB, W = C::NWC + 1, ROW = D + 2;
+    const SplitParams &p = pp.sp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row0 = (long long)b * pp.total_splits * p.Hq + kvh * G;
+    float M = -INFINITY, l = 0.f, acc[G][DPV];  // (lane: maximum and sum of head lane % G)
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < DPV; ++j) acc[g][j] = 0.f;
+    for (int i0 = warp; i0 < np; i0 += NB * W) {
+        float x[NB][G][DPV];
+        const int own = i0 + W * (lane / G);  // lane k G + g has partial k of head g
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < NB * G && own < np)
+            ml = *reinterpret_cast<const float2 *>(pp.ml_part + (row0 + (long long)own * p.Hq + lane % G) * 2);
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            if (i0 + W * k < np)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    load_row_part<DPV>(pp.o_part + (row0 + (long long)(i0 + W * k) * p.Hq + g) * D + lane * DPV, x[k][g]);
+        float m = fmaxf(M, ml.x);
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float mu = m == -INFINITY ? 0.f : m, old = ex2(M - mu), f = ex2(ml.x - mu);
+        float add = f * ml.y;
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, o);
+        M = m;
+        l = fmaf(l, old, add);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float og = __shfl_sync(0xFFFFFFFFu, old, g);
+#pragma unroll
+            for (int j = 0; j < DPV; ++j) acc[g][j] *= og;
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            if (i0 + W * k < np)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float fg = __shfl_sync(0xFFFFFFFFu, f, k * G + g);
+#pragma unroll
+                    for (int j = 0; j < DPV; ++j) acc[g][j] = fmaf(fg, x[k][g][j], acc[g][j]);
+                }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < DPV; ++j) sums[(warp * G + g) * ROW + lane * DPV + j] = acc[g][j];
+    if (lane < G) {
+        sums[(warp * G + lane) * ROW + D] = M;
+        sums[(warp * G + lane) * ROW + D + 1] = l;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * (D / 2); i += C::THREADS) {
+        const int g = i / (D / 2), d = 2 * (i - g * (D / 2));
+        float2 v[W + 1], ml[W + 1];
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k <= W; ++k) {
+            const float *from = sums + (k * G + g) * ROW;
+            const bool there = k < W || mine;
+            v[k] = there ? *reinterpret_cast<const float2 *>(from + d) : make_float2(0.f, 0.f);
+            ml[k] = there ? *reinterpret_cast<const float2 *>(from + D) : make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, ml[k].x);
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        float a0 = 0.f, a1 = 0.f, ls = 0.f;
+#pragma unroll
+        for (int k = 0; k <= W; ++k) {
+            const float f = ex2(ml[k].x - mu);
+            a0 = fmaf(f, v[k].x, a0);
+            a1 = fmaf(f, v[k].y, a1);
+            ls = fmaf(f, ml[k].y, ls);
+        }
+        store_out_pair(p.out + (long long)b * p.o_sb + (long long)(kvh * G + g) * p.o_sh + d, a0, a1, ls);
+    }
+}
 
 // The split kernel of dap_decode.cuh with a start position: the same producer and consumer.
 template <class C>
@@ -188,14 +277,17 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     if (pp.prefix_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool last = pp.prefix_splits > 0 && blockIdx.x == gridDim.x - 1;
-    unsigned int ignored = 0;
-    const Span span = seq_span(pp, b, &ignored);  // (the combine flags the lengths)
+    unsigned int flags = 0;
+    const Span span = seq_span(pp, b, &flags);  // (flagged by who writes the rows)
+    if (pp.merge && flags && kvh == 0 && threadIdx.x == 0) flag_error(flags);
     const int R = p.box_rows, a0 = suffix_start(pp, span.P);
     const int nsplit = suffix_count(pp, span);
     const int tok0 = a0 + s * p.chunk;
     // (the last split takes what the rounding of a0 pushes past the others)
     const int tok1 = s == p.num_splits - 1 ? span.L : min(span.L, tok0 + p.chunk);
     const int ntiles = s < nsplit && tok1 > tok0 ? (tok1 - tok0 + BT - 1) / BT : 0;
+    float *sums = reinterpret_cast<float *>(smem);  // (merging, when the ring is idle: [warps + 1][G][D + 2])
+    static_assert((NWC + 2) * G * (D + 2) * 4 <= C::MRG_OFF, "the sums fit the ring's place");
     __syncthreads();
 
     if (ntiles > 0 && warp == NWC) {
@@ -281,6 +373,16 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             cs.finish(reinterpret_cast<float *>(smem + C::MRG_OFF),
                       [] { named_sync(1, NWC * 32); return true; },
                       [&](int, int g, int d, float a0v, float a1v, float M, float lv) {
+                          if (pp.merge) {
+                              float *to = sums + ((NWC + 1) * G + g) * (D + 2);
+                              to[d] = a0v;
+                              to[d + 1] = a1v;
+                              if (d == 0) {
+                                  to[D] = M;
+                                  to[D + 1] = lv;
+                              }
+                              return;
+                          }
                           const long long row =
                               ((long long)b * pp.total_splits + pp.prefix_splits + s) * p.Hq + kvh * G + g;
                           *reinterpret_cast<float2 *>(pp.o_part + row * D + d) = make_float2(a0v, a1v);
@@ -288,10 +390,19 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                       });
         }
     }
-    if (last) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (last || pp.merge) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (pp.merge && (ntiles == 0 || !misc[1]))
+        merge_rows<C>(pp, sums, b, kvh, span.L > 0 ? (span.P + pp.prefix_chunk - 1) / pp.prefix_chunk : 0, ntiles > 0);
 }
 
 // ---- host side -------------------------------------------------------------------------------------
+
+// CTAs of a cluster of the prefix kernel, and of its grid.
+inline int prefix_cluster(const SharedArgs &a) { return a.page_size % 8 == 0 && a.num_tiles > 1 ? 2 : 1; }
+inline long long prefix_ctas(const SharedArgs &a) {
+    const int cl = prefix_cluster(a);
+    return (long long)((a.num_tiles + cl - 1) / cl * cl) * a.Hkv * a.prefix_splits;
+}
 
 namespace {
 
@@ -341,7 +452,7 @@ inline int suffix_box_rows(const SharedArgs &a) {
 }
 
 template <int D, int G, bool GATHER>
-dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream) {
+dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream, bool *merged) {
     using C = SuffixCfg<D, G, GATHER>;
     const int R = suffix_box_rows(a);
     CUtensorMap mk = {}, mv = {};
@@ -350,10 +461,19 @@ dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream) {
         return DAP_ERR_CUDA;
     auto kern = shared_suffix_kernel<C>;
     static PerDeviceOcc occ = {};
-    if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
+    const int per_sm = prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100), sms = dap_device_sm_count();
+    if (per_sm <= 0 || sms <= 0) return DAP_ERR_CUDA;
     const long long grid = (long long)a.B * a.Hkv * a.suffix_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
-    const SharedParams p = shared_params(a, R);
+    SharedParams p = shared_params(a, R);
+    // With one split a sequence's CTA can merge its rows itself, waiting for the prefix kernel where it is: a launch
+    // less (2 us on the host) and a hop less (16 sequences behind 2048 shared keys, 11 prefix partials: 11.7 us for
+    // 12.1).  It does where all CTAs are resident beside the prefix's (the wait of the first would hold the others
+    // back), and up to two trips to memory for the partials (128 partials of 8 heads x 64: 24.3 us against the
+    // combine's 11.9, which has a CTA a row for so many).
+    *merged = a.suffix_splits == 1 && a.prefix_splits <= 2 * C::MERGE_NB * (C::NWC + 1) &&
+              (a.prefix_splits == 0 || grid <= per_sm * std::max(0LL, sms - prefix_ctas(a)));
+    p.merge = *merged;
     return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p) ==
                    cudaSuccess
                ? DAP_OK
@@ -361,22 +481,22 @@ dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream) {
 }
 
 template <int D, bool GATHER>
-dap_status suffix_groups(const SharedArgs &a, cudaStream_t stream) {
+dap_status suffix_groups(const SharedArgs &a, cudaStream_t stream, bool *merged) {
     switch (a.Hq / a.Hkv) {
-        case 1: return launch_suffix<D, 1, GATHER>(a, stream);
-        case 2: return launch_suffix<D, 2, GATHER>(a, stream);
-        case 4: return launch_suffix<D, 4, GATHER>(a, stream);
-        case 8: return launch_suffix<D, 8, GATHER>(a, stream);
+        case 1: return launch_suffix<D, 1, GATHER>(a, stream, merged);
+        case 2: return launch_suffix<D, 2, GATHER>(a, stream, merged);
+        case 4: return launch_suffix<D, 4, GATHER>(a, stream, merged);
+        case 8: return launch_suffix<D, 8, GATHER>(a, stream, merged);
     }
     return DAP_ERR_UNSUPPORTED;
 }
 
 template <bool GATHER>
-dap_status suffix_dims(const SharedArgs &a, cudaStream_t stream) {
+dap_status suffix_dims(const SharedArgs &a, cudaStream_t stream, bool *merged) {
     switch (a.D) {
-        case 64: return suffix_groups<64, GATHER>(a, stream);
-        case 128: return suffix_groups<128, GATHER>(a, stream);
-        case 256: return suffix_groups<256, GATHER>(a, stream);
+        case 64: return suffix_groups<64, GATHER>(a, stream, merged);
+        case 128: return suffix_groups<128, GATHER>(a, stream, merged);
+        case 256: return suffix_groups<256, GATHER>(a, stream, merged);
     }
     return DAP_ERR_UNSUPPORTED;
 }

@@ -679,8 +679,8 @@ dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     auto kern = shared_prefix_kernel<C>;
     static PerDeviceOcc occ = {};
     if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
-    const int cl = !GATHER && a.num_tiles > 1 ? 2 : 1;
-    const long long grid = (long long)((a.num_tiles + cl - 1) / cl * cl) * a.Hkv * a.prefix_splits;
+    const int cl = prefix_cluster(a);
+    const long long grid = prefix_ctas(a);
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);
     const cudaError_t e =

@@ -4,9 +4,9 @@
 
 namespace dap {
 
-dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream) {
-    if (a.page_size % 8 != 0) return launch_shared_suffix_gather(a, stream);
-    return suffix_dims<false>(a, stream);
+dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream, bool *merged) {
+    if (a.page_size % 8 != 0) return launch_shared_suffix_gather(a, stream, merged);
+    return suffix_dims<false>(a, stream, merged);
 }
 
 bool read_errors_shared_suffix(unsigned int *flags, bool clear) { return read_tu_errors(flags, clear); }

@@ -4,7 +4,9 @@
 
 namespace dap {
 
-dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream) { return suffix_dims<true>(a, stream); }
+dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream, bool *merged) {
+    return suffix_dims<true>(a, stream, merged);
+}
 
 bool read_errors_shared_suffix_gather(unsigned int *flags, bool clear) { return read_tu_errors(flags, clear); }
 
