@@ -539,30 +539,33 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
     if (max_suffix_len == 0) *suffix_splits = 0;
     const bool prefix = max_prefix_len > 0, suffix = max_suffix_len > 0;
     if (prefix && (*prefix_splits == 0 || (suffix && *suffix_splits == 0))) {
-        // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM (two at D = 256), run on the others meanwhile, and on all of
-        // them afterwards.  The pair of counts with the least time by this model, in microseconds, as measured: 8 to
-        // start and end a prefix CTA, 0.78 a 64-key tile (0.55 with at most 128 rows, 0.95 at D = 256); 4 to start
-        // and end a suffix CTA and 0.4 for 32 keys; suffix K/V at 0.066 MB/us an SM, 6.6 MB/us in all; partial rows
-        // through the workspace at 5 MB/us.
-        const double mb = 1e-6, per_sm = 0.066, all = 6.6;
-        const long long rows = num_tiles > 0 ? ((long long)B * (Hq / Hkv) + num_tiles - 1) / num_tiles : 1;
-        const double tile = D == 256 ? 0.95 : rows <= 128 ? 0.55 : 0.78;
+        // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM (two at D = 256), run on the others meanwhile,
+        // and on all of them afterwards.  The pair of counts with the least time by this model, in microseconds, fitted
+        // to sweeps of both counts over 45 batches (1.8% above the best pair in the mean, 13% at most): 6 to start and
+        // end a prefix CTA, 0.85 a 64-key tile (0.45 with at most 128 rows, 0.95 at D = 256); 3 to start and end a
+        // suffix CTA and 0.4 for 32 keys (0.6 at D = 256); suffix K/V at 0.05 MB/us an SM, 6.6 MB/us in all; partial
+        // rows through the workspace at 8 MB/us, 0.5 for a combine of its own.
+        const double mb = 1e-6, per_sm = 0.05, all = 6.6;
+        const int G = Hq / Hkv, slots = D == 256 ? 2 : 4;
+        const long long rows = num_tiles > 0 ? ((long long)B * G + num_tiles - 1) / num_tiles : 1;
+        const double tile = D == 256 ? 0.95 : rows <= 128 ? 0.45 : 0.85, keys32 = D == 256 ? 0.6 : 0.4;
         const long long tiles = ceil_div_ll(max_prefix_len, kTileTokens);
         const long long units = (num_tiles > 1 ? (num_tiles + 1LL) / 2 * 2 : 1) * Hkv;  // (pairs of tiles)
-        const double suffix_mb = (double)total_suffix * Hkv * D * 4 * mb, merge = (double)B * Hq * D * 8 * mb / 5.;
+        const double suffix_mb = (double)total_suffix * Hkv * D * 4 * mb, merge = (double)B * Hq * D * 8 * mb / 8.;
         double best = 1e300;
         int best_prefix = 1, best_suffix = suffix ? 1 : 0;
         auto consider = [&](long long per) {
             const long long n = ceil_div_ll(tiles, per), ctas = units * n, free = std::max<long long>(0, sms - ctas);
-            const double t = (double)ceil_div_ll(ctas, sms) * (8. + per * tile), rate = std::min(all, free * per_sm);
+            const double t = (double)ceil_div_ll(ctas, sms) * (6. + per * tile), rate = std::min(all, free * per_sm);
             const double left = suffix_mb - rate * t, bandwidth = t + (left > 0. ? left / all : 0.);
             for (int m = suffix ? 1 : 0;; m *= 2) {
                 if (suffix && *suffix_splits > 0) m = *suffix_splits;
                 double us = bandwidth;
                 if (suffix) {
-                    const double cta = 4. + 0.4 * (double)ceil_div_ll(ceil_div_ll(max_suffix_len, m), 32);
-                    const double waves = (double)B * Hkv * m / ((D == 256 ? 2. : 4.) * (double)(free > 0 ? free : sms));
+                    const double cta = 3. + keys32 * (double)ceil_div_ll(ceil_div_ll(max_suffix_len, m), 32);
+                    const double waves = (double)B * Hkv * m / (slots * (double)(free > 0 ? free : sms));
                     us = std::max(us, (free > 0 ? 0. : t) + cta * std::max(1., waves));
+                    if (m > 1 || waves > 1. || n > shared_merge_most(G, D)) us += 0.5;
                 }
                 us += merge * (double)(n + m);
                 if (us < best) {

@@ -131,6 +131,12 @@ struct SharedArgs {
     long long o_sb, o_sh;
 };
 dap_status launch_shared_prefix(const SharedArgs &a, cudaStream_t stream);
+// Prefix partials that a warp of a merging suffix CTA has in flight for each of its G heads (64 values a lane); and how
+// many such a CTA takes at most: two trips of its three warps.
+constexpr int shared_merge_batch(int G, int D) {
+    return 2048 / (G * D) < 1 ? 1 : 2048 / (G * D) > 8 ? 8 : 2048 / (G * D);
+}
+constexpr int shared_merge_most(int G, int D) { return 2 * 3 * shared_merge_batch(G, D); }
 // (*merged: the kernel merges and writes the rows itself, no combine follows)
 dap_status launch_shared_suffix(const SharedArgs &a, cudaStream_t stream, bool *merged);
 dap_status launch_shared_suffix_gather(const SharedArgs &a, cudaStream_t stream, bool *merged);

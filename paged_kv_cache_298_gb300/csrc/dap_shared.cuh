@@ -153,8 +153,7 @@ struct SuffixCfg {
     static constexpr int BAR_OFF = (MISC_OFF + 16 + 7) & ~7;
     static constexpr int SMEM = BAR_OFF + 2 * NS * 8 + 1024;  // + slack to align the base
     static constexpr int THREADS = (NWC + 1) * 32;
-    // Merging: prefix partials that a warp has in flight for each of the G heads, 64 values a lane.
-    static constexpr int MERGE_FIT = 64 / (G * (D / 32)), MERGE_NB = MERGE_FIT < 1 ? 1 : MERGE_FIT > 8 ? 8 : MERGE_FIT;
+    static constexpr int MERGE_NB = shared_merge_batch(G, D);
 };
 
 // The prefix partials of the CTA's G heads, merged with its own sums (`sums` + 3 G (D + 2) floats, made by the
@@ -467,11 +466,11 @@ dap_status launch_suffix(const SharedArgs &a, cudaStream_t stream, bool *merged)
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     SharedParams p = shared_params(a, R);
     // With one split a sequence's CTA can merge its rows itself, waiting for the prefix kernel where it is: a launch
-    // less (2 us on the host) and a hop less (16 sequences behind 2048 shared keys, 11 prefix partials: 11.7 us for
+    // less (2 us on the host) and a hop less (16 sequences behind 2048 shared keys, 11 prefix partials: 11.0 us for
     // 12.1).  It does where all CTAs are resident beside the prefix's (the wait of the first would hold the others
     // back), and up to two trips to memory for the partials (128 partials of 8 heads x 64: 24.3 us against the
     // combine's 11.9, which has a CTA a row for so many).
-    *merged = a.suffix_splits == 1 && a.prefix_splits <= 2 * C::MERGE_NB * (C::NWC + 1) &&
+    *merged = a.suffix_splits == 1 && a.prefix_splits <= shared_merge_most(G, D) &&
               (a.prefix_splits == 0 || grid <= per_sm * std::max(0LL, sms - prefix_ctas(a)));
     p.merge = *merged;
     return launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p) ==
