@@ -97,7 +97,7 @@ struct PageWindow {
 
 // The rows of a row-gather tile by the same window: lane l holds rows l, l + 32, .. of tile after tile, with no
 // division after the first.  (A prefix tile at page size 12 against a table read a row: 0.65 us for 0.81 at D = 64,
-// 1.27 for 1.35 at D = 256, 1.61 for 1.50 at D = 128.)
+// 1.27 for 1.35 at D = 256.)
 template <class C>
 struct RowWalk {
     static constexpr int N = RowPages<C>::N;
@@ -133,6 +133,52 @@ struct RowWalk {
         }
     }
 };
+
+// Row gather of a tile of one tensor, or (BOTH) of K and V behind each other: fill_tile_rows with the source rows of
+// eight copies exchanged before the first of them is issued, since a copy's row otherwise costs it the latency of a
+// shuffle (a 64-key prefix tile at page size 12: 0.53 us for 0.65 at D = 64, 0.64 for 1.61 at D = 128, 1.00 for 1.27 at
+// D = 256).  A row's number fits 32 bits: 2^32 rows of 64 dims are 550 GB.
+template <class C, bool BOTH>
+__device__ __forceinline__ void gather_rows(uint8_t *tile, const __nv_bfloat16 *x, const __nv_bfloat16 *y,
+                                            const RowPages<C> &rp, int nvalid, int kvh, const SplitParams &p,
+                                            uint64_t *full, int lane) {
+    constexpr int CPR = C::ROWB / 16, N = RowPages<C>::N, RPI = 32 / CPR, U = 8;
+    static_assert(C::SWB == 128 && RPI <= 8 && C::BT % (RPI * U) == 0, "batches of whole rows");
+    uint32_t row[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int pg = rp.pg[k];
+        if (lane + 32 * k < nvalid && (pg < 0 || pg >= p.num_pages)) {
+            flag_error(DAP_DEVERR_PAGE);
+            pg = 0;
+        }
+        row[k] = (uint32_t)pg * (uint32_t)p.page_size + (uint32_t)rp.slot[k];
+    }
+    if (lane == 0) mbar_arrive(full);
+    const int c = lane % CPR, r0 = lane / CPR;
+    const uint32_t pitch = (uint32_t)(p.Hkv * C::D * 2);
+    const uint32_t to = smem_addr(tile) + c / C::CPB * (C::BT * 128) + r0 * 128 + ((c % C::CPB ^ r0) << 4);
+    const char *sx = reinterpret_cast<const char *>(x + (long long)kvh * C::D + c * 8);
+    const char *sy = BOTH ? reinterpret_cast<const char *>(y + (long long)kvh * C::D + c * 8) : nullptr;
+#pragma unroll
+    for (int i0 = 0; i0 < C::BT / RPI; i0 += U) {
+        uint32_t src[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            src[u] = __shfl_sync(0xFFFFFFFFu, row[(RPI * (i0 + u)) >> 5], (r0 + RPI * (i0 + u)) & 31);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = RPI * (i0 + u);  // (+ r0: the swizzle's chunk is c ^ r0 ^ r's low bits)
+            if (r0 + r < nvalid) {
+                const uint32_t dst = (to ^ ((r & 7) << 4)) + r * 128;
+                const unsigned long long off = (unsigned long long)src[u] * pitch;
+                cp_async_16(dst, sx + off);
+                if (BOTH) cp_async_16(dst + C::TILE_BYTES, sy + off);
+            }
+        }
+    }
+    cp_async_mbar_arrive(full);
+}
 
 // ---- suffix kernel: one CTA per (sequence, kv head, split) ---------------------------------------
 
@@ -302,8 +348,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     misc[1] = 1;
                     break;
                 }
-                fill_tile_rows<C>(smem + st * C::STAGE_BYTES, rp, min(BT, tok1 - t), kvh, p, 0u, [] {}, &full[st],
-                                  lane);
+                gather_rows<C, true>(smem + st * C::STAGE_BYTES, p.k_cache, p.v_cache, rp, min(BT, tok1 - t), kvh, p,
+                                     &full[st], lane);
                 issued = i + 1;
             }
         } else {  // ---- producer warp: page lookup + TMA issue

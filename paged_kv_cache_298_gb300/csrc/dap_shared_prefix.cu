@@ -67,34 +67,6 @@ struct PrefixCfg {
     static_assert(NSTREAM * 128 * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
-// Row gather of one tensor: fill_tile_rows for K or V alone.
-template <class C>
-__device__ __forceinline__ void fill_rows(uint8_t *tile, const __nv_bfloat16 *cache, const RowPages<C> &rp, int nvalid,
-                                          int kvh, const SplitParams &p, uint64_t *full, int lane) {
-    constexpr int CPR = C::ROWB / 16, N = RowPages<C>::N, RPI = 32 / CPR;
-    long long row[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        int pg = rp.pg[k];
-        if (lane + 32 * k < nvalid && (pg < 0 || pg >= p.num_pages)) {
-            flag_error(DAP_DEVERR_PAGE);
-            pg = 0;
-        }
-        row[k] = (((long long)pg * p.page_size + rp.slot[k]) * p.Hkv + kvh) * C::D;
-    }
-    if (lane == 0) mbar_arrive(full);
-    const int c = lane % CPR, r0 = lane / CPR;
-    const uint32_t to = smem_addr(tile) + c / C::CPB * (C::BT * 128);
-    const __nv_bfloat16 *src = cache + c * 8;
-#pragma unroll
-    for (int it = 0; it < C::BT / RPI; ++it) {
-        const int r = r0 + RPI * it;
-        const long long off = __shfl_sync(0xFFFFFFFFu, row[(RPI * it) >> 5], r & 31);
-        if (r < nvalid) cp_async_16(to + (uint32_t)(r * 128 + ((c % C::CPB ^ (r & 7)) << 4)), src + off);
-    }
-    cp_async_mbar_arrive(full);
-}
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -222,8 +194,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 RowPages<C> rp;
                 walk.next(rp);
                 if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
-                fill_rows<C>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, rp, min(BT, tok1 - t), kvh,
-                             p, &full[st], lane);
+                gather_rows<C, false>(place + st * 2 * C::TILE_BYTES, tensor ? p.v_cache : p.k_cache, nullptr, rp,
+                                      min(BT, tok1 - t), kvh, p, &full[st], lane);
             }
         } else {
             // K: lane = (box j, column block cb), or a whole tile where a page has one; V: lane = box, all blocks.  A
