@@ -24,10 +24,12 @@ namespace {
 
 // Both kernels are bound by memory (3 D + 2 bytes a row).  A CTA takes TT consecutive tokens x all kv heads of K
 // and V, so that a place is looked up once for 2 Hkv rows, a token's codes (Hkv D bytes) are read or written in
-// one place and the factors of neighbouring slots meet in one store.  Measured: 50,000 tokens of 8 kv heads x 128
-// written in 55 us (309 MB, 0.83 of the copy rate; what is left are the loads of a CTA's first pass and the
-// conversions, 40% of the issue slots), 40,000 read back in 40 us (249 MB, 0.91).
-constexpr int kMaxTT = 64;
+// one place and the factors of neighbouring slots meet in one store.  CTAs of four warps, so that the registers of
+// the loads ahead fit seven to an SM and the last ones fill it evenly.  Measured: 50,000 tokens of 8 kv heads x 128
+// written in 49.6 us (309 MB, 0.92 of the copy rate; with 256 threads, four CTAs to an SM and the addresses multiplied
+// out a row: 55 us), 40,000 read back in 40 us (249 MB, 0.91), 7700 written in 10.9 us and 8000 of 4 heads x 256 read in
+// 8.3, of which 3 are the launch.
+constexpr int kMaxTT = 64, kThreads = 128;
 
 // Sequence of packed row r, found by a whole warp that probes 32 boundaries at once (B up to 1024
 // takes two rounds); any contents of indptr keep the accesses inside it.
@@ -43,12 +45,10 @@ __device__ __forceinline__ int find_run(const int32_t *indptr, int B, int r, int
     return lo;
 }
 
-// Slot of the pool (page * page_size + slot in the page) of tokens r0 .. r0 + n - 1, one per thread of the
-// first warps: -1 where the row is in no run, -2 where its position or page is outside (flagged); and the slot in
-// its page.
+// Where tokens r0 .. r0 + n - 1 are, one per thread of the first warps: element of their first code (-1 where the row
+// is in no run, -2 where its position or page is outside, which is flagged) and of kv head 0's factor.
 struct Places {
-    long long row[kMaxTT];
-    int slot[kMaxTT];
+    long long code[kMaxTT], factor[kMaxTT];
 };
 __device__ __forceinline__ void find_places(const RunArgs &p, int r0, int n, Places &place) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -66,24 +66,27 @@ __device__ __forceinline__ void find_places(const RunArgs &p, int r0, int n, Pla
         else hi = mid - 1;
     }
     const long long b0 = __ldg(p.indptr + lo), b1 = __ldg(p.indptr + lo + 1), start = __ldg(p.positions + lo);
-    long long row = -1;
-    int slot = 0;
+    long long code = -1, factor = 0;
     if (r >= b0 && r < b1) {
         const long long pos = start + (r - b0);
-        row = -2;
+        code = -2;
         if (pos >= 0 && pos < (long long)p.max_pages * p.page_size) {
             // (a position below 2^32, as a run starts at an int32 and has fewer than 2^31 rows)
             const int pg = (int)((uint32_t)pos / (uint32_t)p.page_size);
-            slot = (int)((uint32_t)pos - (uint32_t)pg * (uint32_t)p.page_size);
+            const int slot = (int)((uint32_t)pos - (uint32_t)pg * (uint32_t)p.page_size);
             const int page = __ldg(p.block_table + (long long)lo * p.max_pages + pg);
-            if (page >= 0 && page < p.num_pages) row = (long long)page * p.page_size + slot;
-            else flag_error(DAP_DEVERR_PAGE);
+            if (page >= 0 && page < p.num_pages) {
+                code = ((long long)page * p.page_size + slot) * (p.Hkv * p.D);
+                factor = (long long)page * p.Hkv * p.page_size + slot;
+            } else {
+                flag_error(DAP_DEVERR_PAGE);
+            }
         } else {
             flag_error(DAP_DEVERR_SEQLEN);
         }
     }
-    place.row[first + lane] = row;
-    place.slot[first + lane] = slot;
+    place.code[first + lane] = code;
+    place.factor[first + lane] = factor;
 }
 
 // Token and head of the rows that a lane takes, RPP apart: one division, then steps of (RPP / Hkv, RPP % Hkv).
@@ -143,22 +146,23 @@ __device__ __noinline__ uint2 slow_codes(uint4 w, float s) {
 // from where its rounding changes.  Rows with a maximum outside [2^-90, 2^90], where the steps could leave the
 // normal range, are divided by the hardware's rules.
 template <int D>
-__global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, const int TT) {
-    constexpr int LPR = D / 16, RPP = 256 / LPR;
+__global__ void __launch_bounds__(kThreads, 7) append_runs_kernel(const RunArgs p, const int TT) {
+    constexpr int LPR = D / 16, RPP = kThreads / LPR;
     __shared__ Places place;
     extern __shared__ __nv_bfloat16 factor[];  // [2][Hkv][TT]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int r0 = blockIdx.x * TT, n = min(TT, p.T - r0);
     const int c = threadIdx.x % LPR;
-    const __nv_bfloat16 *ks = p.rows[0] + c * 8 + (long long)r0 * p.st[0];
-    const __nv_bfloat16 *vs = p.rows[1] + c * 8 + (long long)r0 * p.st[1];
     RowStep at(threadIdx.x / LPR, RPP, p.Hkv);
+    const __nv_bfloat16 *k = p.rows[0] + c * 8 + (r0 + (long long)at.tok) * p.st[0] + at.head * p.sh[0];
+    const __nv_bfloat16 *v = p.rows[1] + c * 8 + (r0 + (long long)at.tok) * p.st[1] + at.head * p.sh[1];
+    // (their steps with `at`: within the heads, and over to the next token)
+    const long long ka = at.dq * p.st[0] + at.dr * p.sh[0], kb = ka + p.st[0] - p.Hkv * p.sh[0];
+    const long long va = at.dq * p.st[1] + at.dr * p.sh[1], vb = va + p.st[1] - p.Hkv * p.sh[1];
     uint4 next[4];
     auto load = [&] {  // the K row and the V row at (at.tok, at.head)
         if (at.tok < n) {
-            const __nv_bfloat16 *k = ks + at.tok * p.st[0] + at.head * p.sh[0];
-            const __nv_bfloat16 *v = vs + at.tok * p.st[1] + at.head * p.sh[1];
             next[0] = *reinterpret_cast<const uint4 *>(k);
             next[1] = *reinterpret_cast<const uint4 *>(k + D / 2);
             next[2] = *reinterpret_cast<const uint4 *>(v);
@@ -176,11 +180,13 @@ __global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, co
 #pragma unroll
         for (int u = 0; u < 4; ++u) x[u] = next[u];
         const int tok = at.tok, head = at.head;
+        const bool wrap = at.head + at.dr >= p.Hkv;
+        k += wrap ? kb : ka;
+        v += wrap ? vb : va;
         at.next();
         load();
         const bool live = tok < n;
-        const long long row = live ? place.row[tok] : -1;
-        const long long off = (row * p.Hkv + head) * D + c * 8;
+        const long long code0 = live ? place.code[tok] : -1, off = code0 + (head * D + c * 8);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             const uint32_t w[8] = {x[2 * kv].x,     x[2 * kv].y,     x[2 * kv].z,     x[2 * kv].w,
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, co
                 code[2] = b.x;
                 code[3] = b.y;
             }
-            if (row >= 0) {
+            if (code0 >= 0) {
                 uint8_t *dst = p.codes[kv] + off;
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
                 *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(code[2], code[3]);
@@ -226,12 +232,10 @@ __global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, co
     }
     __syncthreads();
     // the factors head by head: neighbouring threads write neighbouring slots
-    for (int i = threadIdx.x; i < n * p.Hkv; i += 256) {
+    for (int i = threadIdx.x; i < n * p.Hkv; i += kThreads) {
         const int h = i / n, t = i - h * n;
-        const long long row = place.row[t];
-        const int slot = place.slot[t];
-        if (row >= 0) {
-            const long long at_page = (row - slot) * p.Hkv + (long long)h * p.page_size + slot;
+        if (place.code[t] >= 0) {
+            const long long at_page = place.factor[t] + (long long)h * p.page_size;
             p.scale[0][at_page] = factor[h * TT + t];
             p.scale[1][at_page] = factor[(p.Hkv + h) * TT + t];
         }
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(256, 4) append_runs_kernel(const RunArgs p, co
 // Read: D / 16 lanes a row, two chunks of 8 codes (8 bytes read, 16 written) each, so that a warp's stores are
 // whole sectors; a lane takes the K row and the V row of one (token, head), U pairs in flight.
 template <int D>
-__global__ void __launch_bounds__(256, 6) read_runs_kernel(const RunArgs p, const int TT) {
-    constexpr int LPR = D / 16, RPP = 256 / LPR, U = 2;
+__global__ void __launch_bounds__(kThreads, 10) read_runs_kernel(const RunArgs p, const int TT) {
+    constexpr int LPR = D / 16, RPP = kThreads / LPR, U = 2;
     __shared__ Places place;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -261,17 +265,16 @@ __global__ void __launch_bounds__(256, 6) read_runs_kernel(const RunArgs p, cons
             tok[u] = at.tok;
             head[u] = at.head;
             at.next();
-            const long long row = tok[u] < n ? place.row[tok[u]] : -1;
-            run[u] = row != -1;
+            const long long code0 = tok[u] < n ? place.code[tok[u]] : -1;
+            run[u] = code0 != -1;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 x[u][kv][0] = x[u][kv][1] = make_uint2(0u, 0u);
                 s[u][kv] = 0.f;
             }
-            if (row >= 0) {
-                const int slot = place.slot[tok[u]];
-                const long long off = (row * p.Hkv + head[u]) * D + c * 8;
-                const long long f = (row - slot) * p.Hkv + (long long)head[u] * p.page_size + slot;
+            if (code0 >= 0) {
+                const long long off = code0 + (head[u] * D + c * 8);
+                const long long f = place.factor[tok[u]] + (long long)head[u] * p.page_size;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     x[u][kv][0] = *reinterpret_cast<const uint2 *>(p.codes[kv] + off);
@@ -309,17 +312,17 @@ __global__ void __launch_bounds__(256, 6) read_runs_kernel(const RunArgs p, cons
 template <int D>
 dap_status launch_d(const RunArgs &a, bool write, cudaStream_t stream) {
     // Tokens of a CTA: a read, two passes of its lanes over the rows (all in flight at once); a write, whose loads
-    // run one pass ahead, one pass or up to eight while the grid stays above one wave of four CTAs per SM
-    constexpr int RPP = 256 * 16 / D;
-    const long long rows = (long long)a.T * a.Hkv, waves = (rows + RPP * 608LL - 1) / (RPP * 608LL);
+    // run one pass ahead, one pass or up to eight while the grid stays above one wave of seven CTAs per SM
+    constexpr int RPP = kThreads * 16 / D;
+    const long long rows = (long long)a.T * a.Hkv, waves = (rows + RPP * 7 * 152LL - 1) / (RPP * 7 * 152LL);
     const int passes = write ? (int)std::min<long long>(8, std::max<long long>(1, waves)) : 2;
     const int TT = std::min(kMaxTT, std::max(1, passes * RPP / a.Hkv));
     const dim3 grid((unsigned)((a.T + (long long)TT - 1) / TT));
     const size_t smem = write ? (size_t)2 * a.Hkv * TT * sizeof(__nv_bfloat16) : 0;
     if (smem > 40 * 1024) return DAP_ERR_UNSUPPORTED;  // (over 10,000 kv heads)
     const cudaError_t e =
-        write ? launch_dependent_smem(append_runs_kernel<D>, grid, dim3(256), (int)smem, stream, a, TT)
-              : launch_dependent_smem(read_runs_kernel<D>, grid, dim3(256), (int)smem, stream, a, TT);
+        write ? launch_dependent_smem(append_runs_kernel<D>, grid, dim3(kThreads), (int)smem, stream, a, TT)
+              : launch_dependent_smem(read_runs_kernel<D>, grid, dim3(kThreads), (int)smem, stream, a, TT);
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
