@@ -393,7 +393,7 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
  * dap_shared_seqs_per_tile: 256 / G (128 / G at D = 256), 0 for unsupported heads.
  * dap_shared_plan: the split counts that a call runs.  A count that is 0 on entry is chosen so that the prefix's
  * CTAs (one SM each, one per tile, kv head and split) and the suffix's (one per sequence, kv head and split, four
- * to an SM) end together; one that is not is lowered as dap_resolve_splits does; the count of a part whose bound
+ * to an SM, two at D = 256) end together; one that is not is lowered as dap_resolve_splits does; the count of a part whose bound
  * is 0 becomes 0.  total_suffix: the summed lengths behind the prefixes (0: unknown, B * max_suffix_len).
  * Returns 0, or -1 for invalid arguments.  Pure host functions; no CUDA call.
  */
@@ -423,8 +423,8 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
  *                 planner's, >= 1: explicit).
  *   workspace     device, >= dap_workspace_bytes_shared(B, Hq, D, the two counts run), 16-byte aligned.
  *   Supported: D in {64, 128, 256}; G in {1, 2, 4, 8}; any page_size >= 1.  seqs_per_tile as
- *   dap_shared_seqs_per_tile.  The summation order depends only on logical positions, the group sizes and the
- *   split counts, so a result is the same for any placement of the pages.
+ *   dap_shared_seqs_per_tile.  The summation order depends only on logical positions, the page size, the group
+ *   sizes, the split counts and the device's SMs, so a result is the same for any placement of the pages.
  */
 dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long long q_stride_h,
                                     const void *k_cache, const void *v_cache, int num_pages,

@@ -9,14 +9,15 @@
 //     group's P_g keys, so every key is read once for up to 256 rows;
 //   * suffix: positions P_g .. L_b of each sequence, the split schedule of the single-token decode.
 // Each part is cut into splits that leave (acc, m, l) partials in the workspace, [B][prefix splits +
-// suffix splits][Hq][D] then [..][2], and a combine kernel merges a row's partials in that order.
+// suffix splits][Hq][D] then [..][2], and a combine kernel merges a row's partials in that order; with one suffix
+// split and few prefix partials the suffix kernel does that itself (launch_suffix has the rule).
 // The suffix kernel does not wait for the prefix kernel: it starts beside it, on the SMs that the prefix
 // leaves free, as soon as every prefix CTA runs (programmatic dependent launch), and one of its CTAs waits
 // for the prefix kernel's end before it exits, so that the combine, which waits for the suffix kernel, finds
 // both.  The prefix is bound by its products, the suffix by memory: run side by side they use both.  How many
 // SMs each gets is a matter of the prefix's split count, which dap_shared_plan chooses for both to end
 // together: 64 sequences behind 32768 shared keys, 64 .. 2048 of their own (64 query heads, 8 kv heads, D = 128),
-// 96 SMs and 56: 85 us; the prefix on all SMs, then the suffix: 110 us.
+// 96 SMs and 56: 88 us; the prefix on all SMs, then the suffix: 110 us.
 #pragma once
 
 #include <algorithm>
