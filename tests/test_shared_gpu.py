@@ -143,6 +143,24 @@ def test_against_plain_attention(sizes, prefixes, suffix, Hq, Hkv, D, ps):
     assert binding.get_device_errors() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_merging_of_many_partials(G, D):
+    """One suffix split, which may merge its rows itself, and any number of prefix partials: none, fewer than the warps, one
+    trip and two of them, more than a CTA takes itself."""
+    c = Case([5], [64 * 50 - 7], [0, -1, 1, 40, 90], 2 * G, 2, D, 16, seed=40 + G)
+    ref = c.plain()
+    for n in (1, 2, 3, 4, 7, 12, 13, 24, 25, 48, 50):
+        c.check(c.run(prefix_splits=n, suffix_splits=1), ref, f"{n} prefix partials")
+    c.prefix.zero_()
+    c.max_prefix = 0
+    c.lens = torch.tensor([0, 1, 64, 65, 90], dtype=torch.int32, device="cuda")
+    c.table[:] = c.table[0]
+    c.max_suffix = 90
+    c.check(c.run(suffix_splits=1), c.plain(), "no prefix")
+    assert binding.get_device_errors() == 0
+
+
 def test_equals_ordinary_decode():
     """The same batch through decode_attn_paged (page-aligned prefix: the block tables are complete)."""
     c = Case([24], [512], [i * 9 for i in range(24)], 32, 8, 128, 16)
