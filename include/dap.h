@@ -380,9 +380,10 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
  * Decode of a batch whose sequences share long prefixes (a system prompt, a document asked by
  * many): decode_attn_paged where the sequences come in groups, and the first prefix_lens[g] positions
  * of every sequence of group g hold the same K and V.  The prefix is read through the block table of
- * the group's first sequence, once for up to 256 query rows (sequences x the G heads of a kv head; 128
- * at D = 256), as a matrix product on the tensor cores; the rest of each sequence is read through its
- * own block table.  The result is decode_attn_paged's up to rounding.
+ * the group's first sequence (whatever that one's own length is), once for up to 256 query rows
+ * (sequences x the G heads of a kv head; 128 at D = 256), as a matrix product on the tensor cores; the
+ * rest of each sequence is read through its own block table.  The result is decode_attn_paged's up to
+ * rounding.
  *
  * Groups are runs of consecutive sequences.  dap_shared_map builds the work map on the host:
  *   group_sizes   host int32 [num_groups], each >= 0 (a sequence that shares nothing: a group of 1).

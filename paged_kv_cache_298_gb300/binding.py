@@ -644,7 +644,7 @@ class SharedPlan:
         self.map = host.to(device)   # the tiles, then the sequences' groups
         self.tiles, self.seq_group = self.map[:4 * cap].view(cap, 4), self.map[4 * cap:]
         self.sizes = (self.B, self.Hq, self.Hkv, self.D, self.num_groups, self.num_tiles, self.seqs_per_tile)
-        self._last = (None, None)
+        self._last = (None, None, None)
 
     def splits(self, max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0, prefix_splits: int = 0,
                suffix_splits: int = 0, device: int | None = None):
@@ -652,27 +652,29 @@ class SharedPlan:
         default: the current one)."""
         if device is None or device < 0:
             device = _current_device() if torch.cuda.is_available() else -1
+        asked = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
+        last, key, found = self._last
+        if last == asked:   # (steps of one batch often share their bounds)
+            return found
         # lengths that grow by a token a step keep their plan: rounded up to 64, or to an eighth of themselves
         max_suffix_len, total_suffix = (n + -n % max(64, 1 << max(0, n.bit_length() - 4)) for n in
                                         (max_suffix_len, total_suffix))
         max_suffix_len = min(max_suffix_len, 0x7FFFFFFF)
-        key = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
-        last, found = self._last
-        if last == key:
-            return found
-        lib = load()
-        if device >= 0:
-            with _on(device):
-                sms = lib.dap_device_sm_count()
-        else:
-            sms = 0
-        pre, suf = ctypes.c_int(prefix_splits), ctypes.c_int(suffix_splits)
-        _need(lib.dap_shared_plan(sms, self.num_tiles, self.B, self.Hq, self.Hkv, self.D, max_prefix_len, max_suffix_len,
-                                  total_suffix, ctypes.byref(pre), ctypes.byref(suf)) == 0,
-              "bounds and split counts must be >= 0")
-        ps, ss = pre.value, suf.value
-        self._last = (key, (ps, ss))   # (steps of one batch often share their bounds)
-        return ps, ss
+        rounded = (device, max_prefix_len, max_suffix_len, total_suffix, prefix_splits, suffix_splits)
+        if key != rounded:
+            lib = load()
+            if device >= 0:
+                with _on(device):
+                    sms = lib.dap_device_sm_count()
+            else:
+                sms = 0
+            pre, suf = ctypes.c_int(prefix_splits), ctypes.c_int(suffix_splits)
+            _need(lib.dap_shared_plan(sms, self.num_tiles, self.B, self.Hq, self.Hkv, self.D, max_prefix_len,
+                                      max_suffix_len, total_suffix, ctypes.byref(pre), ctypes.byref(suf)) == 0,
+                  "bounds and split counts must be >= 0")
+            found = pre.value, suf.value
+        self._last = asked, rounded, found
+        return found
 
 
 def workspace_bytes_shared(plan: SharedPlan, *, max_prefix_len: int, max_suffix_len: int, total_suffix: int = 0,

@@ -73,7 +73,7 @@ def _ext_flags() -> tuple[list[str], list[str]]:
     for d in inc:
         comp += ["-isystem" if d != INCLUDE else "-I", d]
     lib = os.path.join(root, "lib")
-    link = [f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{PKG}", "-l:libdap.so",
+    link = [f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-L{PKG}", "-l:libdap.so",
             f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
     return comp, link
 
