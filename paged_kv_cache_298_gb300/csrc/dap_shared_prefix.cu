@@ -67,6 +67,33 @@ struct PrefixCfg {
     static_assert(NSTREAM * 128 * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
+// `n` rows of sums (NC of their floats) that a warp has in shared memory, ROW_F apart, to their places (element `to` of
+// `out` for the lane's row): whole rows a store, eight stores' loads ahead of the first.
+template <class C, int NC>
+__device__ __forceinline__ void store_rows(const float *rows, float *out, long long to, int n, int lane) {
+    constexpr int W = NC < 128 ? NC : 128, LPR = W / 4, RPI = 32 / LPR, U = 8;
+    static_assert(NC % W == 0 && 32 % (RPI * U) == 0, "whole batches");
+    __syncwarp();
+#pragma unroll
+    for (int c0 = 0; c0 < NC; c0 += W) {
+        const int c = c0 + lane % LPR * 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += RPI * U) {
+            float4 v[U];
+            long long at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * RPI + lane / LPR;
+                at[u] = __shfl_sync(0xFFFFFFFFu, to, i);
+                v[u] = *reinterpret_cast<const float4 *>(rows + i * C::ROW_F + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * RPI + lane / LPR < n) *reinterpret_cast<float4 *>(out + at[u] + c) = v[u];
+        }
+    }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -451,14 +478,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                                          (C::NSTREAM == 1 || mbar_wait(&fin[2], 0)));
         tc_fence_after();
         const bool good = done && misc[2] == 0;
-        // q and the ring are idle now: the sums leave through them, a row a thread, as one bulk copy each (rows written
-        // to global memory by their threads, 32 lines a store: 11,000 cycles; by warps, row after row: 5500)
+        // q and the ring are idle now: the sums leave through them, written by warps, whole rows a store (rows written
+        // to global memory by their threads, 32 lines a store: 11,000 cycles for 256 rows; as a bulk copy a row: 6000)
         float *mine = reinterpret_cast<float *>(smem) + (x * 128 + r) * C::ROW_F;
-        const bool merge = C::NSTREAM == 2 && !both;  // both streams hold the same rows: stream 0 adds stream 1's
-        if (merge) {
-            if (x == 1 && active && good) {
+        const long long prow = ((long long)seq * pp.total_splits + s) * p.Hq + hq;
+        if (C::NSTREAM == 2 && !both) {
+            // Both streams hold the same rows: each adds the other's sums to its own for half of the dims (stream 0 for
+            // the first), which it gets through shared memory.
+            constexpr int H = D / 2;
+            const float *other = reinterpret_cast<float *>(smem) + ((1 - x) * 128 + r) * C::ROW_F;
+            if (active && good) {
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = (1 - x) * H, i = 0; i < H / 32; ++i, c += 32) {
                     float o[32];
                     if (N > 0) tmem_ld32(tO + c, o);
 #pragma unroll
@@ -469,43 +500,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 *reinterpret_cast<float2 *>(mine + D) = make_float2(m_ref, l);
             }
             named_sync(1, C::NWS * 32);
-        }
-        if ((x == 0 || !merge) && active && good) {
-            const float *other = mine + 128 * C::ROW_F;
-            float f0 = 1.f, f1 = 0.f;
-            if (merge) {
+            if (active && good) {
                 const float2 ml = *reinterpret_cast<const float2 *>(other + D);
                 const float m = fmaxf(m_ref, ml.x), mu = m == -INFINITY ? 0.f : m;
-                f0 = ex2(m_ref - mu);
-                f1 = ex2(ml.x - mu);
-                m_ref = m;
-                l = l * f0 + ml.y * f1;
+                const float f0 = ex2(m_ref - mu), f1 = ex2(ml.x - mu);
+#pragma unroll 1
+                for (int c = x * H, i = 0; i < H / 32; ++i, c += 32) {
+                    float o[32];
+                    if (N > 0) tmem_ld32(tO + c, o);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(other + c + k);
+                        *reinterpret_cast<float4 *>(mine + c + k) =
+                            N > 0 ? make_float4(o[k] * f0 + v.x * f1, o[k + 1] * f0 + v.y * f1,
+                                                o[k + 2] * f0 + v.z * f1, o[k + 3] * f0 + v.w * f1)
+                                  : make_float4(v.x * f1, v.y * f1, v.z * f1, v.w * f1);
+                    }
+                }
+                if (rvalid && x == 0)
+                    *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m, l * f0 + ml.y * f1);
+                store_rows<C, H>(mine - lane * C::ROW_F + x * H, pp.o_part + x * H, prow * D, min(32, nx - (r - lane)),
+                                 lane);
             }
-            const long long prow = ((long long)seq * pp.total_splits + s) * p.Hq + hq;
+        } else if (active && good) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(tO + c, o);
-                if (merge) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(other + c + k);
-                        o[k] = o[k] * f0 + v.x * f1;
-                        o[k + 1] = o[k + 1] * f0 + v.y * f1;
-                        o[k + 2] = o[k + 2] * f0 + v.z * f1;
-                        o[k + 3] = o[k + 3] * f0 + v.w * f1;
-                    }
-                }
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
                     *reinterpret_cast<float4 *>(mine + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
-            if (rvalid) {
-                *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
-                fence_async_smem();
-                bulk_store(pp.o_part + prow * D, mine, D * 4);
-                bulk_store_wait();
-            }
+            if (rvalid) *reinterpret_cast<float2 *>(pp.ml_part + prow * 2) = make_float2(m_ref, l);
+            store_rows<C, D>(mine - lane * C::ROW_F, pp.o_part, prow * D, min(32, nx - (r - lane)), lane);
         }
         if (threadIdx.x == 0 && misc[2]) {
             // a wait gave up: the copies still in flight land (bounded) before the shared memory goes
