@@ -550,7 +550,7 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
         const long long rows = num_tiles > 0 ? ((long long)B * G + num_tiles - 1) / num_tiles : 1;
         const double tile = D == 256 ? 0.95 : rows <= 128 ? 0.45 : 0.85, keys32 = D == 256 ? 0.6 : 0.4;
         const long long tiles = ceil_div_ll(max_prefix_len, kTileTokens);
-        const long long units = (num_tiles > 1 ? (num_tiles + 1LL) / 2 * 2 : 1) * Hkv;  // (pairs of tiles)
+        const long long units = std::max<long long>(1, num_tiles) * Hkv;
         const double suffix_mb = (double)total_suffix * Hkv * D * 4 * mb, merge = (double)B * Hq * D * 8 * mb / 8.;
         double best = 1e300;
         int best_prefix = 1, best_suffix = suffix ? 1 : 0;

@@ -96,17 +96,6 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// The same to this place in every CTA of `mask` (cluster ranks), completing `bytes` on the barrier at `bar`'s
-// place in each.
-__device__ __forceinline__ void tma_load_5d_multicast(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                                      int c3, int c4, uint64_t *bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar)), "h"(mask)
-        : "memory");
-}
-
 // 3-D tiled TMA load global -> shared, completing `bytes` on `bar`.
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
                                             uint64_t *bar) {

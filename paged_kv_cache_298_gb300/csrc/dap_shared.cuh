@@ -443,12 +443,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
 // ---- host side -------------------------------------------------------------------------------------
 
-// CTAs of a cluster of the prefix kernel, and of its grid.
-inline int prefix_cluster(const SharedArgs &a) { return a.page_size % 8 == 0 && a.num_tiles > 1 ? 2 : 1; }
-inline long long prefix_ctas(const SharedArgs &a) {
-    const int cl = prefix_cluster(a);
-    return (long long)((a.num_tiles + cl - 1) / cl * cl) * a.Hkv * a.prefix_splits;
-}
+// CTAs of the prefix kernel's grid.
+inline long long prefix_ctas(const SharedArgs &a) { return (long long)a.num_tiles * a.Hkv * a.prefix_splits; }
 
 namespace {
 

@@ -15,8 +15,6 @@
 //   tensor memory (lane = row): S  columns [128 x + 64 e, + 64)  fp32 scores of tile n in buffer e = n & 1;
 //                                  P (bf16 pairs) overwrites the first 32 once they are read;
 //                               O  columns [256 + x D, + D)  fp32 accumulator.
-// Two CTAs whose tiles are of the same group form a cluster: one copies every K tile, the other every V tile, to
-// both (TMA multicast), so that each tile is read from L2 once for both.
 // Warps: four softmax warps a stream (thread = row), a producer each for K and V, one a stream that issues its
 // scores and one that issues all products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores
 // are there when the softmax gets to them.
@@ -97,7 +95,7 @@ __device__ __forceinline__ void store_rows(const float *rows, float *out, long l
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                         const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G, const int cl) {
+                         const __grid_constant__ CUtensorMap mapV, const SharedParams pp, const int G) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = aligned_smem<C>(smem_raw);
     constexpr int BT = C::BT, NS = C::NS, D = C::D;
@@ -112,15 +110,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
     uint8_t *ring = smem + C::RING_OFF;
 
-    // clusters of cl (1 or 2) CTAs: tiles cl i .. of one kv head and split
-    const int rank = cl == 2 ? (int)(blockIdx.x & 1) : 0;
-    const int units = (pp.num_tiles + cl - 1) / cl * p.Hkv;
-    const int cid = (int)(blockIdx.x / cl);
-    const int s = cid / units;
-    const int rem = cid - s * units;
-    const int wc = rem / p.Hkv;
-    const int kvh = rem - wc * p.Hkv;
-    const int w = wc * cl + rank;
+    const int units = pp.num_tiles * p.Hkv;
+    const int s = (int)(blockIdx.x / units);
+    const int rem = (int)(blockIdx.x - s * units);
+    const int w = rem / p.Hkv;
+    const int kvh = rem - w * p.Hkv;
 
     // Tensor memory touches nothing the previous kernel writes: it is allocated before the wait.
     if (warp == 0) {
@@ -141,19 +135,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // (group, first sequence of the group, first sequence of the tile, sequences)
-    auto tile_of = [&](int i) -> int4 {
-        int4 t = i < pp.num_tiles ? __ldg(reinterpret_cast<const int4 *>(pp.tiles) + i) : make_int4(0, 0, 0, 0);
-        if (t.x < 0 || t.x >= pp.num_groups || t.y < 0 || t.y >= p.B || t.z < 0 || t.w < 1 || t.w > pp.seqs_per_tile ||
-            t.w > p.B - t.z)
-            t.w = 0;
-        return t;
-    };
-    const int4 tl = tile_of(w), buddy = cl == 2 ? tile_of(w ^ 1) : make_int4(0, 0, 0, 0);
-    const int q0 = tl.y, first = tl.z, nseq = tl.w;
-    const int P = nseq > 0 ? group_prefix(pp, tl.x) : 0;
-    // the cluster's CTAs share their K/V tiles
-    const bool paired = nseq > 0 && buddy.w > 0 && buddy.x == tl.x && buddy.y == q0;
-    if (nseq == 0 && w < pp.num_tiles && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
+    const int4 tl = __ldg(reinterpret_cast<const int4 *>(pp.tiles) + w);
+    const bool valid = tl.x >= 0 && tl.x < pp.num_groups && tl.y >= 0 && tl.y < p.B && tl.z >= 0 && tl.w >= 1 &&
+                       tl.w <= pp.seqs_per_tile && tl.w <= p.B - tl.z;
+    const int q0 = tl.y, first = tl.z, nseq = valid ? tl.w : 0;
+    const int P = valid ? group_prefix(pp, tl.x) : 0;
+    if (!valid && threadIdx.x == 0 && s == 0 && kvh == 0) flag_error(DAP_DEVERR_QMAP);
     const int nrows = nseq * G;
     const int tok0 = min(P, s * pp.prefix_chunk), tok1 = min(P, tok0 + pp.prefix_chunk);
     const int J = (tok1 - tok0 + BT - 1) / BT;  // K/V tiles of this CTA
@@ -168,9 +155,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(&k_full[i], full_arrivals<C>());
             mbar_init(&v_full[i], full_arrivals<C>());
             // a commit of every stream that takes the K tile, one after the last product that reads the V tile
-            const int kb = C::NSTREAM == 2 && buddy.w * G > 128 ? 2 : 1;
-            mbar_init(&k_empty[i], (both ? 2 : 1) + (paired ? kb : 0));
-            mbar_init(&v_empty[i], paired ? 2 : 1);
+            mbar_init(&k_empty[i], both ? 2 : 1);
+            mbar_init(&v_empty[i], 1);
         }
         for (int e = 0; e < 4; ++e) {
             mbar_init(&s_done[e], 1);
@@ -185,7 +171,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();  // barriers and the tensor-memory address are visible
-    if (cl == 2) cluster_sync_all();  // (to the other CTA too)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t CS = BT * 128;  // bytes between column blocks of a tile
@@ -237,8 +222,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int dq = BT / p.page_size, dr = BT - dq * p.page_size;
             int e = e0, row = row0 + (j * R < BT ? j * R : 0);  // (lanes without a box follow the tile's first)
             for (; row >= p.page_size; ++e) row -= p.page_size;
-            // (each CTA awaits its own K and V; in a pair rank 0 copies K, rank 1 V)
-            const bool copies = !paired || rank == tensor;
             for (; done < J; ++done) {
                 const int st = done % NS;
                 const int nbox = (min(BT, tok1 - (tok0 + done * BT)) + R - 1) / R;
@@ -246,14 +229,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB));
                 __syncwarp();
-                if (j < nbox && copies) {
+                if (j < nbox) {
                     if (pg < 0 || pg >= p.num_pages) {
                         flag_error(DAP_DEVERR_PAGE);
                         pg = 0;
                     }
-                    uint8_t *dst = place + st * 2 * C::TILE_BYTES + to;
-                    if (paired) tma_load_5d_multicast(dst, map, 0, row, cb, kvh, pg, &full[st], 3);
-                    else tma_load_5d(dst, map, 0, row, cb, kvh, pg, &full[st]);
+                    tma_load_5d(place + st * 2 * C::TILE_BYTES + to, map, 0, row, cb, kvh, pg, &full[st]);
                 }
                 e += dq;
                 if ((row += dr) >= p.page_size) {
@@ -287,7 +268,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 misc[2] = 1;
             }
         }
-        // every commit on this CTA's barriers, the other CTA's too, has arrived before the CTA ends
+        // every commit on these barriers has arrived before the CTA ends
         for (int i = max(0, J - NS); i < J && done == J; ++i)
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[i % NS], (i / NS) & 1))) {
                 misc[2] = 1;
@@ -300,7 +281,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         const int role = same(warp - C::ISSUER);  // a stream's scores; NSTREAM: all products with V
         const int Ju = same(J), last = same(nlast);
-        const bool two = same(both) != 0, tailed = same(ragged) != 0, shared = same(paired) != 0;
+        const bool two = same(both) != 0, tailed = same(ragged) != 0;
         const uint32_t tm = same(tmem);
         const int step = two || C::NSTREAM == 1 ? 1 : 2;  // tile n of stream x is step * n + (step == 2 ? x : 0)
         const uint32_t sQ = smem_addr(smem), sR = smem_addr(ring);
@@ -330,8 +311,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     umma_bf16(tS, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
                               dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
                 umma_commit(&s_done[e]);
-                if (shared) umma_commit_multicast(&k_empty[st], 3);
-                else umma_commit(&k_empty[st]);
+                umma_commit(&k_empty[st]);
             }
             __syncwarp();
             return true;
@@ -351,10 +331,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         umma_bf16_tmem_a(tOx, tP + i * 8, dV + (i == 0 ? 0u : i == 1 ? v1 : i == 2 ? v2 : v3), idO,
                                          n > 0 || i > 0);
                 umma_commit(&pv_done[e]);
-                if (!two || x == 1) {  // (a commit covers all products before it)
-                    if (shared) umma_commit_multicast(&v_empty[st], 3);
-                    else umma_commit(&v_empty[st]);
-                }
+                if (!two || x == 1) umma_commit(&v_empty[st]);  // (a commit covers all products before it)
             }
             __syncwarp();
             return true;
@@ -544,8 +521,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    // (neither CTA of a cluster leaves while the other's copies and commits may still reach it)
-    if (cl == 2) cluster_sync_all();
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
@@ -678,15 +653,11 @@ dap_status launch_prefix(const SharedArgs &a, cudaStream_t stream) {
     auto kern = shared_prefix_kernel<C>;
     static PerDeviceOcc occ = {};
     if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
-    const int cl = prefix_cluster(a);
     const long long grid = prefix_ctas(a);
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const SharedParams p = shared_params(a, R);
-    const cudaError_t e =
-        cl == 2 ? launch_cluster_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, 2, stream, mq,
-                                                mk, mv, p, a.Hq / a.Hkv, cl)
-                : launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p,
-                                        a.Hq / a.Hkv, cl);
+    const cudaError_t e = launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk,
+                                                mv, p, a.Hq / a.Hkv);
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
