@@ -181,9 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Launched as a programmatic dependent of the previous kernel on the stream: nothing
     // global is read before the wait (that kernel may still write q, the cache or the
-    // slot table); the next launch may start at once (it waits the same way).
+    // slot table); the next launch may start (it waits the same way) once every CTA holds its
+    // tensor memory, which the next kernel, too, takes before its wait.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- 1a. q's first four 64-wide blocks, right away: they travel during the compaction
     if (tid == 0) {
         for (int kb = 0; kb < kQStages; ++kb) {

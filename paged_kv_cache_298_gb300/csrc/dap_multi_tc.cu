@@ -97,9 +97,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // Programmatic dependent launch: nothing global is read before the wait.
+    // Programmatic dependent launch: nothing global is read before the wait.  The next kernels may start once every
+    // CTA holds its tensor memory (they may take some before they wait for this one).
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int wb = p.tile_batch[w], wi = p.tile_index[w];
     const int bb = (wb >= 0 && wb < p.B) ? wb : 0;

@@ -130,9 +130,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             prefetch_tensormap(&mapV);
         }
     }
-    // Nothing global is read before the wait; the suffix kernel may start after it.
+    // Nothing global is read before the wait; the suffix kernel may start after it, and once every CTA holds its tensor
+    // memory: a kernel further down the stream may take some before its own wait, and a CTA that still waited for columns
+    // held by a kernel that waits for this one would never get them.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // (group, first sequence of the group, first sequence of the tile, sequences)
     const int4 tl = __ldg(reinterpret_cast<const int4 *>(pp.tiles) + w);

@@ -20,3 +20,22 @@ def test_no_load_to_several_ctas(path):
     """The library is what every replica of a run on several GPUs loads, and the addresses that its kernels copy from are the
     caller's: no copy is sent to more than one CTA."""
     assert "multicast" not in code_of(path)
+
+
+@pytest.mark.parametrize("path", [p for p in SOURCES if "tcgen05.alloc" in code_of(p)], ids=os.path.basename)
+def test_dependents_launch_after_tensor_memory_is_held(path):
+    """A kernel's next one may become resident once every CTA has let it, and may take tensor memory before it waits for the
+    kernel's end.  So a CTA lets it from the warp that allocates, after the allocation (which waits until it succeeds): else a
+    CTA that still waits for its columns and the one that took them would wait for each other."""
+    code = code_of(path)
+    allocs = [m.start() for m in re.finditer(r"tcgen05\.alloc\.", code)]
+    assert allocs
+    for at in allocs:
+        guard = code.rfind("if (", 0, at)
+        assert re.match(r"if \(warp == 0\) \{\s*asm", code[guard:]), "one warp allocates"
+        trigger = code.find("griddepcontrol.launch_dependents", at)
+        assert trigger > 0
+        line = code[code.rfind("\n", 0, trigger):trigger]
+        assert line.strip() == 'if (warp == 0) asm volatile("', "the allocating warp lets the dependents launch"
+        assert code.find("griddepcontrol.launch_dependents", 0, at) < 0 or "__global__" in code[
+            code.find("griddepcontrol.launch_dependents"):at], "not before the allocation"
