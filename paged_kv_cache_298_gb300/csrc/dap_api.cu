@@ -581,12 +581,12 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
             best_prefix = *prefix_splits;
         } else {
             const long long most = std::min<long long>(tiles, std::max<long long>(1, sms / std::max(1LL, units)));
+            // (by count, not by tiles a split: at most as many as the device has SMs, however long the prefix)
             long long last = 0;
-            for (long long per = ceil_div_ll(tiles, most); per <= tiles; ++per) {
-                const long long n = ceil_div_ll(tiles, per);
+            for (long long count = most; count >= 1; --count) {
+                const long long per = ceil_div_ll(tiles, count), n = ceil_div_ll(tiles, per);
                 if (n != last) consider(per);
                 last = n;
-                if (n == 1) break;
             }
         }
         *prefix_splits = best_prefix;
