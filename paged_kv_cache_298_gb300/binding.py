@@ -62,8 +62,8 @@ def library_path() -> str:
 
 
 def load(build_if_missing: bool = True):
-    """Load libdap.so and the extension beside it (building them when absent or stale, if allowed)."""
-    global _lib, _ext
+    """Load libdap.so (building it with nvcc when absent or stale, if allowed)."""
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -74,11 +74,10 @@ def load(build_if_missing: bool = True):
             try:
                 _build.build()
             except Exception as e:  # no nvcc or a compile error: fail loudly
-                if not (os.path.exists(_LIB_PATH) and os.path.exists(_EXT_PATH)):
+                if not os.path.exists(_LIB_PATH):
                     raise RuntimeError(f"libdap.so is missing and could not be built: {e}") from e
-        for path in (_LIB_PATH, _EXT_PATH):
-            if not os.path.exists(path):
-                raise RuntimeError(f"{os.path.basename(path)} not found at {path}; run __graft_entry__.build()")
+        if not os.path.exists(_LIB_PATH):
+            raise RuntimeError(f"libdap.so not found at {_LIB_PATH}; run __graft_entry__.build()")
         lib = ctypes.CDLL(_LIB_PATH)
         P, I, LL, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
         lib.dap_status_string.argtypes = [I]
@@ -148,6 +147,29 @@ def load(build_if_missing: bool = True):
         lib.dap_get_device_errors.restype = I
         lib.dap_selftest_wait_timeout.argtypes = [ctypes.c_void_p]
         lib.dap_selftest_wait_timeout.restype = I
+        _lib = lib
+        return lib
+
+
+def load_native(build_if_missing: bool = True):
+    """Load the extension _dap_torch.so (building it when absent, stale or made for another torch or Python, if
+    allowed), which the calls marshalled by it need beside libdap.so."""
+    global _ext
+    if _ext is not None:
+        return _ext
+    load(build_if_missing)
+    with _lock:
+        if _ext is not None:
+            return _ext
+        if build_if_missing:
+            from . import build as _build
+            try:
+                _build.build_ext()
+            except Exception as e:  # no compiler or a compile error: fail loudly
+                if not os.path.exists(_EXT_PATH):
+                    raise RuntimeError(f"_dap_torch.so is missing and could not be built: {e}") from e
+        if not os.path.exists(_EXT_PATH):
+            raise RuntimeError(f"_dap_torch.so not found at {_EXT_PATH}; run __graft_entry__.build()")
         try:
             spec = importlib.util.spec_from_file_location("_dap_torch", _EXT_PATH)
             ext = importlib.util.module_from_spec(spec)
@@ -156,14 +178,7 @@ def load(build_if_missing: bool = True):
             raise RuntimeError(f"{_EXT_PATH} cannot be loaded; run __graft_entry__.build(): {e}") from e
         ext.set_error(DapError)
         _ext = ext
-        _lib = lib
-        return lib
-
-
-def _native():
-    if _ext is None:
-        load()
-    return _ext
+        return ext
 
 
 def status_string(status: int) -> str:
@@ -699,7 +714,7 @@ def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_
     dev = q.get_device()
     S = plan.splits(int(max_prefix_len), int(max_suffix_len), int(total_suffix), int(prefix_splits),
                     int(suffix_splits), dev)
-    return _native().decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan.map, plan.sizes,
+    return (_ext or load_native()).decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan.map, plan.sizes,
                                    int(max_prefix_len), int(max_suffix_len), S, scale, workspace, out,
                                    None if stream is None else _stream(stream, dev))
 
@@ -782,7 +797,7 @@ def kv_append_paged_fp8_multi(k_new, v_new, k_codes, v_codes, k_scale, v_scale, 
     sequences back to back (views of a fused projection will do), ``indptr`` [B + 1] the runs'
     boundaries and ``positions`` [B] the position of each run's first row.  Returns the four
     cache arrays, updated in place."""
-    _native().append_runs(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions,
+    (_ext or load_native()).append_runs(k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions,
                           None if stream is None else _stream(stream, k_new.get_device()))
     return k_codes, v_codes, k_scale, v_scale
 
@@ -793,5 +808,5 @@ def kv_read_paged_fp8(k_codes, v_codes, k_scale, v_scale, block_table, indptr, p
     Runs as kv_append_paged_fp8_multi; ``total_tokens`` (the host's copy of indptr[B]) sizes the
     outputs when they are not given.  Returns (k_out, v_out) [total_tokens, Hkv, D]; rows outside
     every run are not written."""
-    return _native().read_runs(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, total_tokens, k_out,
+    return (_ext or load_native()).read_runs(k_codes, v_codes, k_scale, v_scale, block_table, indptr, positions, total_tokens, k_out,
                                v_out, None if stream is None else _stream(stream, k_codes.get_device()))

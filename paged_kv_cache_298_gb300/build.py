@@ -2,8 +2,9 @@
 extension ``_dap_torch.so`` (argument marshalling, csrc/dap_torch.cpp) with the host compiler.
 
 Each translation unit is compiled in parallel, then linked.  The results land next to this
-file; objects go to ``_build/``.  Rebuilds only when a source or header is newer than a
-library, or when torch or Python are not those the extension was built for.
+file; objects go to ``_build/``.  Rebuilds only when a source or header is newer than the
+library, and the extension also when torch or Python are not those it was built for.  The
+library needs nvcc only; the extension needs torch's headers and a built library.
 """
 from __future__ import annotations
 
@@ -42,7 +43,16 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [EXT_SRC, os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+
+
+def _newer_than(path: str, inputs: list[str]) -> bool:
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t for f in inputs)
+
+
+def up_to_date() -> bool:
+    return os.path.exists(LIB) and _newer_than(LIB, _inputs())
 
 
 def _ext_for() -> str:
@@ -51,14 +61,16 @@ def _ext_for() -> str:
     return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, Python {sys.version}"
 
 
-def up_to_date() -> bool:
-    if not all(os.path.exists(f) for f in (LIB, EXT, EXT_FOR)):
+def ext_fits() -> bool:
+    """Whether the extension that is there was built for the torch and Python that run."""
+    if not (os.path.exists(EXT) and os.path.exists(EXT_FOR)):
         return False
     with open(EXT_FOR) as f:
-        if f.read() != _ext_for():
-            return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+        return f.read() == _ext_for()
+
+
+def ext_up_to_date() -> bool:
+    return ext_fits() and _newer_than(EXT, [EXT_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _ext_flags() -> tuple[list[str], list[str]]:
@@ -78,44 +90,67 @@ def _ext_flags() -> tuple[list[str], list[str]]:
     return comp, link
 
 
+def _run(cmd: list[str], what: str, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    if verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
+    """The library."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     flags = NVCC_FLAGS + (extra_flags or [])
 
-    cxx = os.environ.get("CXX", "g++")
-    ext_comp, ext_link = _ext_flags()
-
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [cxx, *ext_comp, "-c", src, "-o", obj] if src == EXT_SRC else [nvcc, *flags, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose:
-            sys.stderr.write(r.stdout + r.stderr)
+        _run([nvcc, *flags, "-c", src, "-o", obj], f"nvcc failed for {src}", verbose)
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        *objs, ext_obj = ex.map(compile_one, sources() + [EXT_SRC])
+        objs = list(ex.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64",
-           *objs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64",
+          *objs, "-o", tmp], "link failed")
     os.replace(tmp, LIB)
-    tmp = EXT + f".tmp{os.getpid()}"
-    r = subprocess.run([cxx, "-shared", ext_obj, "-o", tmp, *ext_link], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, EXT)
-    with open(EXT_FOR, "w") as f:
-        f.write(_ext_for())
     return LIB
 
 
+def _compile_ext(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    obj = os.path.join(BUILD, os.path.basename(EXT_SRC) + ".o")
+    cxx = os.environ.get("CXX", "g++")
+    _run([cxx, *_ext_flags()[0], "-c", EXT_SRC, "-o", obj], f"{cxx} failed for {EXT_SRC}", verbose)
+    return obj
+
+
+def _link_ext(obj: str) -> str:
+    tmp = EXT + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, *_ext_flags()[1]], "link failed")
+    os.replace(tmp, EXT)
+    with open(EXT_FOR, "w") as f:
+        f.write(_ext_for())
+    return EXT
+
+
+def build_ext(force: bool = False, verbose: bool = False) -> str:
+    """The extension, against the library that is there."""
+    return EXT if not force and ext_up_to_date() else _link_ext(_compile_ext(verbose))
+
+
+def build_all(force: bool = False, verbose: bool = False) -> None:
+    """Both, compiled side by side."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        obj = None if not force and ext_up_to_date() else ex.submit(_compile_ext, verbose)
+        build(force, verbose)
+        if obj is not None:
+            _link_ext(obj.result())
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    build_all(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    print(LIB)
