@@ -161,20 +161,23 @@ def load_native(build_if_missing: bool = True):
     with _lock:
         if _ext is not None:
             return _ext
+        from . import build as _build
+        failed = None
         if build_if_missing:
-            from . import build as _build
             try:
                 _build.build_ext()
-            except Exception as e:  # no compiler or a compile error: fail loudly
-                if not os.path.exists(_EXT_PATH):
-                    raise RuntimeError(f"_dap_torch.so is missing and could not be built: {e}") from e
+            except Exception as e:  # no compiler or a compile error
+                failed = e
         if not os.path.exists(_EXT_PATH):
-            raise RuntimeError(f"_dap_torch.so not found at {_EXT_PATH}; run __graft_entry__.build()")
+            raise RuntimeError(f"_dap_torch.so not found at {_EXT_PATH}; run __graft_entry__.build()") from failed
+        # (it reads tensors by torch's own layout, so one that happens to load proves nothing)
+        if not _build.ext_fits():
+            raise RuntimeError(f"{_EXT_PATH} was built for another torch or Python; run __graft_entry__.build()") from failed
         try:
             spec = importlib.util.spec_from_file_location("_dap_torch", _EXT_PATH)
             ext = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(ext)
-        except ImportError as e:  # built for another torch or Python
+        except ImportError as e:
             raise RuntimeError(f"{_EXT_PATH} cannot be loaded; run __graft_entry__.build(): {e}") from e
         ext.set_error(DapError)
         _ext = ext

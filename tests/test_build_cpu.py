@@ -52,3 +52,23 @@ spec.loader.exec_module(b)
 assert b.up_to_date()
 assert b.build() == b.LIB
 ''', CXX="/bin/false")
+
+
+def test_an_extension_for_another_torch_is_refused(tmp_path):
+    """The extension reads torch's tensors by their layout in memory.  One made for another torch or Python, that cannot be made
+    anew, is not loaded, even where its symbols would resolve."""
+    record = tmp_path / "for"
+    record.write_text("torch 0.0 at /nowhere, Python 0")
+    python(f'''
+from paged_kv_cache_298_gb300 import binding, build
+build.EXT_FOR = {str(record)!r}
+for allowed in (True, False):
+    try:
+        binding.load_native(build_if_missing=allowed)
+    except RuntimeError as e:
+        assert "another torch or Python" in str(e), e
+    else:
+        raise AssertionError("loaded")
+assert binding._ext is None
+''', CXX="/bin/false")
+    assert record.read_text().startswith("torch 0.0")
