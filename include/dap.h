@@ -419,7 +419,8 @@ size_t dap_workspace_bytes_shared(int B, int Hq, int D, int prefix_splits, int s
  *   seq_group, tiles  device copies of dap_shared_map's output (tiles 16-byte aligned; seq_group is not read
  *                 when num_groups is 1).  A sequence whose group is out of range gives a zero row, a tile out of
  *                 range leaves its sequences' results undefined; both set DAP_DEVERR_QMAP.
- *   max_prefix_len, max_suffix_len  host: upper bounds of prefix_lens[g] and seq_lens[b] - prefix_lens[g].
+ *   max_prefix_len, max_suffix_len  host: upper bounds of prefix_lens[g] and seq_lens[b] - prefix_lens[g], each at
+ *                 most 2^30 - 64.
  *   prefix_splits, suffix_splits    as dap_shared_plan on the device's SMs with total_suffix = 0 (0: the
  *                 planner's, >= 1: explicit).
  *   workspace     device, >= dap_workspace_bytes_shared(B, Hq, D, the two counts run), 16-byte aligned.

@@ -611,8 +611,10 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
                                     int D, float scale, int prefix_splits, int suffix_splits,
                                     void *workspace, size_t workspace_bytes, void *out, long long out_stride_b,
                                     long long out_stride_h, void *stream) {
+    // (a suffix, up to 31 positions in front of it and a chunk together stay inside 32 bits)
+    constexpr int kMostKeys = (1 << 30) - 64;
     if (prefix_splits < 0 || prefix_splits > 65536 || suffix_splits < 0 || num_groups < 0 || num_tiles < 0 ||
-        max_suffix_len < 0)
+        max_suffix_len < 0 || max_prefix_len > kMostKeys || max_suffix_len > kMostKeys)
         return DAP_ERR_SHAPE;
     dap_status st = check_common(q, q_stride_b, q_stride_h, seq_lens, max_prefix_len, B, Hq, Hkv, D, scale,
                                  suffix_splits, out, out_stride_b, out_stride_h);
