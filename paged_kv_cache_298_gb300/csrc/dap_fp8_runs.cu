@@ -314,12 +314,17 @@ dap_status launch_d(const RunArgs &a, bool write, cudaStream_t stream) {
     // Tokens of a CTA: a read, two passes of its lanes over the rows (all in flight at once); a write, whose loads
     // run one pass ahead, one pass or up to eight while the grid stays above one wave of seven CTAs per SM
     constexpr int RPP = kThreads * 16 / D;
-    const long long rows = (long long)a.T * a.Hkv, waves = (rows + RPP * 7 * 152LL - 1) / (RPP * 7 * 152LL);
-    const int passes = write ? (int)std::min<long long>(8, std::max<long long>(1, waves)) : 2;
+    if (write && a.Hkv > 10240) return DAP_ERR_UNSUPPORTED;  // (the factors of one token take over 40 KB)
+    int passes = 2;
+    if (write) {
+        const int sms = dap_device_sm_count();
+        if (sms <= 0) return DAP_ERR_CUDA;
+        const long long rows = (long long)a.T * a.Hkv, wave = (long long)RPP * 7 * sms;
+        passes = (int)std::min<long long>(8, std::max<long long>(1, (rows + wave - 1) / wave));
+    }
     const int TT = std::min(kMaxTT, std::max(1, passes * RPP / a.Hkv));
     const dim3 grid((unsigned)((a.T + (long long)TT - 1) / TT));
     const size_t smem = write ? (size_t)2 * a.Hkv * TT * sizeof(__nv_bfloat16) : 0;
-    if (smem > 40 * 1024) return DAP_ERR_UNSUPPORTED;  // (over 10,000 kv heads)
     const cudaError_t e =
         write ? launch_dependent_smem(append_runs_kernel<D>, grid, dim3(kThreads), (int)smem, stream, a, TT)
               : launch_dependent_smem(read_runs_kernel<D>, grid, dim3(kThreads), (int)smem, stream, a, TT);

@@ -39,3 +39,8 @@ def test_dependents_launch_after_tensor_memory_is_held(path):
         assert line.strip() == 'if (warp == 0) asm volatile("', "the allocating warp lets the dependents launch"
         assert code.find("griddepcontrol.launch_dependents", 0, at) < 0 or "__global__" in code[
             code.find("griddepcontrol.launch_dependents"):at], "not before the allocation"
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_the_device_says_how_many_sms_it_has(path):
+    assert not re.search(r"\b1(48|52)(LL|L|u)?\b", code_of(path))
