@@ -383,7 +383,10 @@ dap_status decode_attn_paged_masked(const void *q, long long q_stride_b, long lo
  * the group's first sequence (whatever that one's own length is), once for up to 256 query rows
  * (sequences x the G heads of a kv head; 128 at D = 256), as a matrix product on the tensor cores; the
  * rest of each sequence is read through its own block table.  The result is decode_attn_paged's up to
- * rounding.
+ * rounding.  It is the faster of the two from about 30 MB of keys and values that sharing saves, which is
+ * (sequences - groups) * prefix * Hkv * D * 4 bytes, with four sequences a group or more: at 32 query heads, 8 kv heads
+ * of 128, at 64 sequences behind 64 keys, 16 behind 1024, 4 behind 4096 (the two are even at 32 behind 256); below that
+ * decode_attn_paged's single kernel wins (4.7 us against 7.8 for two sequences behind 64 keys).
  *
  * Groups are runs of consecutive sequences.  dap_shared_map builds the work map on the host:
  *   group_sizes   host int32 [num_groups], each >= 0 (a sequence that shares nothing: a group of 1).

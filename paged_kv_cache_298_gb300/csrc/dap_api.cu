@@ -541,7 +541,7 @@ int dap_shared_plan(int sm_count, int num_tiles, int B, int Hq, int Hkv, int D, 
     if (prefix && (*prefix_splits == 0 || (suffix && *suffix_splits == 0))) {
         // A prefix CTA takes a whole SM; the suffix's CTAs, four to an SM (two at D = 256), run on the others meanwhile,
         // and on all of them afterwards.  The pair of counts with the least time by this model, in microseconds, fitted
-        // to sweeps of both counts over 45 batches (1.8% above the best pair in the mean, 13% at most): 6 to start and
+        // to sweeps of both counts over 45 batches (3% above the best pair in the mean, 22% at most): 6 to start and
         // end a prefix CTA, 0.85 a 64-key tile (0.45 with at most 128 rows, 0.95 at D = 256); 3 to start and end a
         // suffix CTA and 0.4 for 32 keys (0.6 at D = 256); suffix K/V at 0.05 MB/us an SM, 6.6 MB/us in all; partial
         // rows through the workspace at 8 MB/us, 0.5 for a combine of its own.

@@ -17,7 +17,13 @@
 // both.  The prefix is bound by its products, the suffix by memory: run side by side they use both.  How many
 // SMs each gets is a matter of the prefix's split count, which dap_shared_plan chooses for both to end
 // together: 64 sequences behind 32768 shared keys, 64 .. 2048 of their own (64 query heads, 8 kv heads, D = 128),
-// 96 SMs and 56: 88 us; the prefix on all SMs, then the suffix: 110 us.
+// 96 SMs and 56: 90 us; the prefix on all SMs, then the suffix: 114 us.
+// An assumption of that start: the programming model promises a grid sight of earlier grids' writes at its own
+// griddepcontrol.wait.  The suffix CTAs and the combine read lengths, tables and K/V without one (the combine: the lengths
+// only).  They start after every prefix CTA has passed its wait, so the writers' grids have ended and their writes are in
+// L2, and no SM holds older copies, as a grid's start invalidates its L1.  Tested where lengths and K/V are written by the
+// call before, again and again without waiting (tests/test_shared_gpu.py: lengths that grow in place, append then
+// decode).
 #pragma once
 
 #include <algorithm>
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         prefetch_tensormap(&mapV);
     }
     // With a prefix kernel before it, this grid starts once every CTA of that kernel has passed its
-    // own wait, so what came before is done; without one it waits itself.
+    // own wait, so what came before is done (and seen: the assumption above); without one it waits itself.
     if (pp.prefix_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool last = pp.prefix_splits > 0 && blockIdx.x == gridDim.x - 1;

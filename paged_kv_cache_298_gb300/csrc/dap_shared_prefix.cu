@@ -18,10 +18,11 @@
 // Warps: four softmax warps a stream (thread = row), a producer each for K and V, one a stream that issues its
 // scores and one that issues all products with V.  S(n + 2) needs only PV(n), whose P it replaces, so the scores
 // are there when the softmax gets to them.
-// Bound: the products.  At D = 128 those of a 64-key tile of 256 rows take 1344 cycles (a microbenchmark: 50 an S
-// product, N = 64, whose operands both come from shared memory, 66 a PV product, N = 128); a tile takes 1450
-// (0.77 us, 11 TFLOP/s an SM), with at most 128 rows 0.44 us at page sizes that are multiples of 64 and 0.65 at 16,
-// where the producers' copies bound it; 0.87 us at D = 256 (128 rows).
+// Bound: the products, in this shape.  At D = 128 those of a 64-key tile of 256 rows take 1344 cycles (a microbenchmark:
+// 50 an S product, N = 64, whose operands both come from shared memory, 66 a PV product, N = 128); at the PV products'
+// rate the same work is 1024.  A tile takes 0.82 us (10 TFLOP/s an SM), with at most 128 rows 0.43 us at page sizes
+// that are multiples of 64 and 0.65 at 16, where the producers' copies bound it; 0.86 us at D = 256 (128 rows; 1.00 at
+// page size 16).
 // Why these warps (cycles of a tile at the time, D = 128): one score buffer a stream, every step of the chain S,
 // softmax, PV waiting for the last: 3130; two buffers, one issuing warp a stream: 2100, as PV(n) has to end before
 // the same warp can go on to S(n + 2); one warp for everything, PV_0(n), S_1(n + 1), PV_1(n), S_0(n + 2): 2770, as
@@ -31,7 +32,8 @@
 // producers' time, and the ring already covers the latency.
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only
 // when a tile's maximum passes the reference by more than 2^8), so the weights stay <= 256.  The
-// weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32.
+// weights are rounded to bf16 for the product with V, whose type is bf16; l sums them in fp32, before that
+// rounding (the suffix kernel's l, whose weights are at hand as bf16 fragments, after it: either is within 2^-8 of the other).
 #include "dap_shared.cuh"
 #include "dap_tc.cuh"
 
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(256) shared_combine_kernel(const SharedParams 
     const int b = live ? (int)(gw / p.Hq) : 0, hq = live ? (int)(gw - (long long)b * p.Hq) : 0;
     unsigned int flags = 0;
     // The lengths were there before the prefix or suffix kernel read them, and this grid starts after those
-    // have: only without them it has to wait first.
+    // have: only without them it has to wait first.  (That they can be seen without a wait of this grid's own is the
+    // assumption that dap_shared.cuh states.)
     if (pp.total_splits == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     const Span span = seq_span(pp, b, &flags);
     const int np = span.L > 0 && span.P > 0 ? (span.P + pp.prefix_chunk - 1) / pp.prefix_chunk : 0;
