@@ -1,5 +1,7 @@
 """Shared-prefix decode: captured calls replayed with other lengths and prefixes, against plain attention on those; and the same
 bits from call to call.  Case and its tolerance are test_shared_gpu's."""
+import threading
+
 import pytest
 import torch
 
@@ -90,4 +92,35 @@ def test_the_same_bits_every_time(sizes, prefixes, suffix, Hq, Hkv, D, ps):
         if i % 3 == 2:
             torch.cuda.synchronize()
         assert torch.equal(out, first), f"call {i}"
+    assert binding.get_device_errors() == 0
+
+
+def test_two_threads_at_once():
+    """Two host threads with a stream each, the lock of the interpreter being released inside a call: one plan for both, whose
+    bounds (and so its kept split counts) differ from call to call."""
+    c = Case([20], [300], [7 * j for j in range(20)], 8, 2, 128, 16, seed=9)
+    bounds = [dict(max_prefix_len=300 + 4 * i, max_suffix_len=133 + 70 * i) for i in range(2)]
+    c.table = torch.cat([c.table, torch.full((20, 8), -1, dtype=torch.int32, device="cuda")], dim=1).contiguous()
+    want = [c.run(**b) for b in bounds]
+    torch.cuda.synchronize()
+    results, errors = [[], []], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for n in range(100):
+                results[i].append((n % 2, c.run(stream=stream, **bounds[n % 2])))
+            stream.synchronize()
+        except Exception as e:   # noqa: BLE001 (shown by the assert below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for r in results:
+        assert len(r) == 100 and all(torch.equal(o, want[k]) for k, o in r)
     assert binding.get_device_errors() == 0
