@@ -3,8 +3,8 @@
  *
  * Single-token GQA decode attention over a paged KV cache (bf16 or fp8 e4m3), its
  * contiguous-cache form, multi-token causal decode, masked decode (bool masks, with the
- * causal rule), the fp8 sliding-window latent (K = V) variant, and the cache appends that
- * feed them.  Plain pointers and sizes only.
+ * causal rule), sliding windows with sinks and trees of drafted tokens, the fp8 sliding-window
+ * latent (K = V) variant, the cache appends that feed them, and the page tables beneath.  Plain pointers and sizes only.
  *
  * Conventions shared by every entry point:
  *   - The caller owns every buffer.  The library allocates no device memory and never
@@ -67,6 +67,8 @@ typedef enum {
 #define DAP_DEVERR_PAGE 0x4u     /* block_table entry outside [0, num_pages); page 0 read instead */
 #define DAP_DEVERR_SLOT 0x8u     /* fp8 slot index >= num_blocks*block_size; row skipped */
 #define DAP_DEVERR_QMAP 0x10u    /* multi-token work map names no token of a sequence; tile skipped */
+#define DAP_DEVERR_POOL 0x20u    /* a resize's pages do not fit the pool (too few free, or too many returned); nothing changed */
+#define DAP_DEVERR_TREE 0x40u    /* a node's parent is no earlier node of its tree; taken for a child of the context */
 
 /* Human-readable name of a status code.  Never NULL. */
 const char *dap_status_string(int status);
@@ -441,6 +443,120 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
                                     int prefix_splits, int suffix_splits, void *workspace,
                                     size_t workspace_bytes, void *out, long long out_stride_b,
                                     long long out_stride_h, void *stream);
+
+/*
+ * Attention of new tokens over spans of the paged cache: a sliding window with a few first tokens that stay visible
+ * (sinks), and trees of drafted tokens.  The new tokens of all sequences are packed back to back as in
+ * decode_attn_paged_multi (qo_indptr), and their K and V are in the cache: sequence b has seq_lens[b] >= q_len[b] places
+ * in it, of which ctx = seq_lens[b] - q_len[b] lie in front of its new tokens, and new token i is in place ctx + i.
+ *
+ * dap_span_tokens_per_tile: new tokens of a work tile of these calls (dap_q_tile_map builds the map with it): 8 / G or
+ * 16 / G while they hold the longest run of new tokens, longer runs of head dims 64, 128 and 256 in 128 or 256 rows of
+ * tensor-memory products; 0 for unsupported heads.
+ * dap_span_splits: the split count that a call runs for the num_splits it is given (0: the planner's).  The keys of a
+ * tile are at most the window, the sinks and what rounding to 64 keys adds, so they, not the lengths, are cut.
+ *   tree      whether the call has parents.  total_kv: sum of seq_lens (host), 0: unknown.
+ * Returns 0 for invalid arguments.  Size the workspace with dap_workspace_bytes_multi(total_q, Hq, D, <the value>).
+ * Pure host functions; no CUDA call.
+ */
+int dap_span_tokens_per_tile(int Hq, int Hkv, int D, int max_q_len);
+int dap_span_splits(int sm_count, int num_tiles, int Hq, int Hkv, int D, int tokens_per_tile, int max_kv_len, int window,
+                    int sinks, int tree, long long total_kv, int num_splits);
+
+/*
+ * Sliding-window paged GQA attention with sinks, for one or many new tokens a sequence: token i, in place and position
+ * p = ctx + i, sees the places t <= p with t > p - window or t < sinks:
+ *   out[qo_indptr[b] + i, h, :] = sum_t softmax_t(scale * q[.., h, :] . K[b,t,h/G,:]) V[b,t,h/G,:].
+ * A token with p < 0 (q_len[b] > seq_lens[b], flagged DAP_DEVERR_SEQLEN) gives a zero row.
+ *   q, k_cache, v_cache, block_table, seq_lens, max_kv_len, out, scale, strides, alignment: as decode_attn_paged_multi,
+ *                max_kv_len at most 2^30 - 64.  A work-map entry that names no token of its sequence is skipped and
+ *                flagged (DAP_DEVERR_QMAP); tokens that no entry names have undefined results.
+ *   qo_indptr, tile_batch, tile_index   the work map, made with tokens_per_tile; or all three NULL: one new token a
+ *                sequence (total_q = num_tiles = B, tokens_per_tile 8 / G).
+ *   tokens_per_tile  8 / G, 16 / G or, at D 64, 128 and 256, dap_span_tokens_per_tile's for long runs.
+ *   window       >= 1 (one that reaches max_kv_len is none).  sinks >= 0.
+ *   num_splits   as dap_span_splits on the device's SMs with total_kv = 0.
+ *   workspace    >= dap_workspace_bytes_multi(total_q, Hq, D, S) bytes for the S used, 16-byte aligned.  Calls that may
+ *                run at the same time need workspaces of their own.
+ *   Only pages with a place that some token of the tile sees are looked at: entries of pages that lie wholly between the
+ *   sinks and the window of the sequence's first new token may be stale.  K and V of places that no token of the sequence
+ *   sees may hold anything; those of the others must be finite (a weight of zero does not hide an infinity).
+ *   Supported: D in {32, 64, 128, 256}; G in {1, 2, 4, 8}; any page_size >= 1.  The summation order depends only on
+ *   logical positions, sizes and the split count.
+ */
+dap_status decode_attn_paged_window(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                                    const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                                    int max_pages, const int32_t *seq_lens, const int32_t *qo_indptr,
+                                    const int32_t *tile_batch, const int32_t *tile_index, int num_tiles,
+                                    int tokens_per_tile, int total_q, int window, int sinks, int max_kv_len, int B,
+                                    int Hq, int Hkv, int D, float scale, int num_splits, void *workspace,
+                                    size_t workspace_bytes, void *out, long long out_stride_t, long long out_stride_h,
+                                    void *stream);
+
+/*
+ * Attention of drafted token trees (speculative verification): the new tokens of a sequence are the nodes of a tree, in
+ * an order in which parents come first.  Node i sees the ctx places in front of the tree, its ancestors and itself:
+ *   out[qo_indptr[b] + i, h, :] = sum_t softmax_t(scale * q[.., h, :] . K[b,t,h/G,:]) V[b,t,h/G,:] over those t.
+ *   parents      device int32 [total_q]: the parent's index within the tree, -1 for a child of the context.  One that is
+ *                neither -1 nor an earlier node is taken for -1 and sets DAP_DEVERR_TREE.
+ *   window       0: none.  Else node i's position is ctx + its depth (0 for a child of the context), and of what it sees
+ *                only positions > its own - window or < sinks take part.
+ *   A tree has at most 256 nodes (more: its rows are not written, DAP_DEVERR_QMAP).
+ *   Everything else as decode_attn_paged_window.
+ */
+dap_status decode_attn_paged_tree(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                                  const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                                  int max_pages, const int32_t *seq_lens, const int32_t *parents,
+                                  const int32_t *qo_indptr, const int32_t *tile_batch, const int32_t *tile_index,
+                                  int num_tiles, int tokens_per_tile, int total_q, int window, int sinks,
+                                  int max_kv_len, int B, int Hq, int Hkv, int D, float scale, int num_splits,
+                                  void *workspace, size_t workspace_bytes, void *out, long long out_stride_t,
+                                  long long out_stride_h, void *stream);
+
+/*
+ * Accepted drafts into place: for every sequence b and j < accepted[b], the K and V rows (all kv heads) of place
+ * positions[b] + path[b][j] go to place positions[b] + j, as if all were read before the first is written.
+ *   positions    device int32 [B]: the places in front of the tree (ctx).
+ *   path         device int32 [B, max_path], row-major: the accepted nodes, strictly ascending from 0 or more (any line of
+ *                a tree whose parents come first).  max_path <= 256.
+ *   accepted     device int32 [B], in [0, max_path].
+ *   A path that does not ascend, or a count out of range, leaves its sequence as it is and sets DAP_DEVERR_QMAP; so does a
+ *   place outside [0, max_pages * page_size) with DAP_DEVERR_SEQLEN.  A row whose page, from or to, is outside the pool is
+ *   not moved (DAP_DEVERR_PAGE).  No two sequences may write to the same place, nor one where another reads.
+ *   Supported: D a multiple of 8; pointers 16-byte aligned.
+ */
+dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                           int max_pages, const int32_t *positions, const int32_t *path, const int32_t *accepted,
+                           int max_path, int B, int Hkv, int D, void *stream);
+
+/*
+ * The lengths of a batch change: pages are returned and taken, and the block table, the boundaries of the new rows and
+ * their slots follow, all on the device.  With pages(n) = ceil(n / page_size):
+ *   1. for b ascending, entries pages(new_lens[b]) .. pages(old_lens[b]) - 1 of a sequence that shrinks go on top of the
+ *      stack of free pages, in order (the entries themselves stay in the table);
+ *   2. the top A pages of the stack, A = the sum of pages(new) - pages(old) over the sequences that grow, become, in the
+ *      stack's order, the entries pages(old) .. pages(new) - 1 of those, b ascending.  (The same step backwards restores
+ *      the stack.)
+ *   old_lens, new_lens  device int32 [B], each in [0, max_pages * page_size]; a sequence with one outside keeps its pages
+ *                       and gets no rows (DAP_DEVERR_SEQLEN).
+ *   block_table         device int32 [B, max_pages] row-major, updated.
+ *   free_pages          device int32 [num_pages], num_free device int32 [1]: the stack (entries [0, num_free) are free),
+ *                       updated.
+ *   indptr              device int32 [B + 1] (written): boundaries of the new rows, max(0, new - old) a sequence (as the
+ *                       appends of runs take it, with old_lens as positions).
+ *   slots               device int64 or int32 (slot_bytes 8 or 4) [total_rows] (written; NULL when total_rows is 0): row r
+ *                       of sequence b, at position t = old_lens[b] + r - indptr[b], has slot
+ *                       block_table[b][t / page_size] * page_size + t % page_size; rows behind the last have -1, and so has
+ *                       a row whose page is outside the pool (DAP_DEVERR_PAGE).  (int64: what kv_append_fp8 takes.  int32:
+ *                       a block table of one-slot pages, through which kv_append_paged writes the rows of a whole run.)
+ *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT; the rows that there is room for are written.
+ *   Where the pool has too few free pages, or would get more than num_pages, nothing is changed: boundaries are all 0,
+ *   slots -1, and DAP_DEVERR_POOL is set (new rows past 2^31 - 1 likewise, with DAP_DEVERR_SEQLEN).
+ *   Supported: B <= 16384, B * max_pages <= 2^30, int32 slots with num_pages * page_size <= 2^31 - 1.
+ */
+dap_status kv_resize_paged(const int32_t *old_lens, const int32_t *new_lens, int32_t *block_table, int max_pages,
+                           int page_size, int32_t *free_pages, int num_pages, int32_t *num_free, int32_t *indptr,
+                           void *slots, int slot_bytes, int total_rows, int B, void *stream);
 
 /*
  * fp8 sliding-window latent decode, K = V [C].

@@ -27,7 +27,10 @@ DAP_OK = 0
 STATUS_NAMES = {0: "DAP_OK", 1: "DAP_ERR_NULL", 2: "DAP_ERR_SHAPE", 3: "DAP_ERR_UNSUPPORTED",
                 4: "DAP_ERR_WORKSPACE", 5: "DAP_ERR_ALIGN", 6: "DAP_ERR_CUDA", 7: "DAP_ERR_SCRATCH_LIMIT"}
 NOALLOC_SCRATCH_BYTES = 16 << 20
+TREE_NODES_MOST = 256
+_SLOT_BYTES = {torch.int64: 8, torch.int32: 4}
 DEVERR_TIMEOUT, DEVERR_SEQLEN, DEVERR_PAGE, DEVERR_SLOT, DEVERR_QMAP = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_POOL, DEVERR_TREE = 0x20, 0x40
 
 # every symbol include/dap.h declares
 EXPORTS = ("dap_status_string", "dap_version", "dap_device_sm_count", "dap_plan_splits",
@@ -38,7 +41,8 @@ EXPORTS = ("dap_status_string", "dap_version", "dap_device_sm_count", "dap_plan_
            "decode_attn_paged_fp8kv", "kv_append_paged_fp8", "decode_attn_paged_masked",
            "dap_selftest_wait_timeout", "kv_append_paged_fp8_multi", "kv_read_paged_fp8",
            "decode_attn_paged_shared", "dap_shared_seqs_per_tile", "dap_shared_map", "dap_shared_plan",
-           "dap_workspace_bytes_shared")
+           "dap_workspace_bytes_shared", "dap_span_tokens_per_tile", "dap_span_splits", "decode_attn_paged_window",
+           "decode_attn_paged_tree", "kv_commit_paged", "kv_resize_paged")
 
 
 SPLITS_BALANCED = -1   # include/dap.h: DAP_SPLITS_BALANCED
@@ -141,6 +145,20 @@ def load(build_if_missing: bool = True):
         lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I,
                                                  F, I, I, P, SZ, P, LL, LL, P]
         lib.decode_attn_paged_shared.restype = I
+        lib.dap_span_tokens_per_tile.argtypes = [I, I, I, I]
+        lib.dap_span_tokens_per_tile.restype = I
+        lib.dap_span_splits.argtypes = [I, I, I, I, I, I, I, I, I, I, LL, I]
+        lib.dap_span_splits.restype = I
+        lib.decode_attn_paged_window.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
+                                                 F, I, P, SZ, P, LL, LL, P]
+        lib.decode_attn_paged_window.restype = I
+        lib.decode_attn_paged_tree.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
+                                               F, I, P, SZ, P, LL, LL, P]
+        lib.decode_attn_paged_tree.restype = I
+        lib.kv_commit_paged.argtypes = [P, P, I, I, P, I, P, P, P, I, I, I, I, P]
+        lib.kv_commit_paged.restype = I
+        lib.kv_resize_paged.argtypes = [P, P, P, I, I, P, I, P, P, P, I, I, I, P]
+        lib.kv_resize_paged.restype = I
         lib.dap_set_trace_events.argtypes = [P, P, P]
         lib.dap_set_trace_events.restype = None
         lib.dap_get_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), I]
@@ -720,6 +738,120 @@ def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_
     return (_ext or load_native()).decode_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan.map, plan.sizes,
                                    int(max_prefix_len), int(max_suffix_len), S, scale, workspace, out,
                                    None if stream is None else _stream(stream, dev))
+
+
+# ---- sliding windows and drafted trees ----------------------------------------------------
+
+class SpanPlan:
+    """The work map of one batch of new-token counts for decode_attn_paged_window and decode_attn_paged_tree, made once
+    for as long as the counts last (a decode step of B sequences: ``[1] * B``).  The lengths are not part of it."""
+
+    def __init__(self, q_lens, Hq: int, Hkv: int, D: int, device):
+        ql = [int(n) for n in (q_lens.tolist() if isinstance(q_lens, torch.Tensor) else q_lens)]
+        self.Hq, self.Hkv, self.D = int(Hq), int(Hkv), int(D)
+        self.max_q_len = max(ql, default=0)
+        self.tokens_per_tile = load().dap_span_tokens_per_tile(self.Hq, self.Hkv, self.D, max(0, self.max_q_len))
+        _need(self.tokens_per_tile > 0, "Hq / Hkv must be 1, 2, 4 or 8")
+        _need(min(ql, default=0) >= 0 and sum(ql) < 1 << 31, "q_lens must be counts >= 0")
+        self.B, self.total_q = len(ql), sum(ql)
+        if ql and min(ql) == self.max_q_len == 1:   # a token each: the library needs no map
+            self.num_tiles, self.map = self.B, None
+        else:
+            qi, tb, ti = q_tile_map(ql, self.tokens_per_tile)
+            self.num_tiles = tb.numel()
+            self.map = torch.cat([qi, tb, ti]).to(device)
+        self.sizes = (self.B, self.total_q, self.num_tiles, self.tokens_per_tile, self.Hq, self.Hkv, self.D)
+        self._last = (None, None, None)
+
+    def splits(self, max_kv_len: int, window: int = 0, sinks: int = 0, tree: bool = False, total_kv: int = 0,
+               num_splits: int = 0, device: int | None = None) -> int:
+        """The split count that a call with these bounds runs on a device (index; default: the current one)."""
+        if device is None or device < 0:
+            device = _current_device() if torch.cuda.is_available() else -1
+        asked = (device, max_kv_len, window, sinks, tree, total_kv, num_splits)
+        last, key, found = self._last
+        if last == asked:
+            return found
+        # lengths that grow by a token a step keep their plan: the sum is rounded up to an eighth of itself
+        total_kv += -total_kv % max(64, 1 << max(0, total_kv.bit_length() - 4))
+        rounded = (device, max_kv_len, window, sinks, tree, total_kv, num_splits)
+        if key != rounded:
+            lib, sms = load(), 0
+            if device >= 0:
+                with _on(device):
+                    sms = lib.dap_device_sm_count()
+            found = lib.dap_span_splits(sms, self.num_tiles, self.Hq, self.Hkv, self.D, self.tokens_per_tile, max_kv_len,
+                                        window, sinks, int(tree), total_kv, num_splits)
+            _need(found > 0, "bounds and num_splits must be >= 0")
+        self._last = asked, rounded, found
+        return found
+
+
+def workspace_bytes_span(plan: SpanPlan, *, max_kv_len: int, window: int = 0, sinks: int = 0, tree: bool = False,
+                         total_kv: int = 0, num_splits: int = 0) -> int:
+    """Workspace bytes of a decode_attn_paged_window or (``tree``) decode_attn_paged_tree call with these arguments on the
+    current device."""
+    S = plan.splits(int(max_kv_len), int(window), int(sinks), bool(tree), int(total_kv), int(num_splits))
+    return load().dap_workspace_bytes_multi(plan.total_q, plan.Hq, plan.D, S)
+
+
+def _span(q, k_cache, v_cache, block_table, seq_lens, parents, plan, max_kv_len, window, sinks, scale, num_splits,
+          total_kv, workspace, out, stream):
+    if scale is None:
+        scale = 1.0 / math.sqrt(plan.D)
+    dev = q.get_device()
+    max_kv_len, window, sinks = int(max_kv_len), int(window), int(sinks)
+    S = plan.splits(max_kv_len, window, sinks, parents is not None, int(total_kv), int(num_splits), dev)
+    return (_ext or load_native()).decode_span(q, k_cache, v_cache, block_table, seq_lens, parents, plan.map, plan.sizes,
+                                               window, sinks, max_kv_len, S, scale, workspace, out,
+                                               None if stream is None else _stream(stream, dev))
+
+
+def decode_attn_paged_window(q, k_cache, v_cache, block_table, seq_lens, plan: SpanPlan, *, window: int, sinks: int = 0,
+                             max_kv_len: int, scale: float | None = None, num_splits: int = 0, total_kv: int = 0,
+                             workspace=None, out=None, stream=None):
+    """Paged GQA attention with a sliding window and the first ``sinks`` positions (include/dap.h:
+    decode_attn_paged_window).  q [total_q, Hq, D] holds the new tokens of all sequences back to back (their K/V are in
+    the cache, ``seq_lens`` count them); ``plan`` is the SpanPlan of their counts.  num_splits 0 = the planner's choice
+    (made with the host-known sum of seq_lens ``total_kv`` when given).  Returns ``out`` [total_q, Hq, D]."""
+    _need(int(window) >= 1, "window must be at least 1")
+    return _span(q, k_cache, v_cache, block_table, seq_lens, None, plan, max_kv_len, window, sinks, scale, num_splits,
+                 total_kv, workspace, out, stream)
+
+
+def decode_attn_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, plan: SpanPlan, *, max_kv_len: int,
+                           window: int = 0, sinks: int = 0, scale: float | None = None, num_splits: int = 0,
+                           total_kv: int = 0, workspace=None, out=None, stream=None):
+    """Paged GQA attention of drafted token trees (include/dap.h: decode_attn_paged_tree): q [total_q, Hq, D] holds the
+    nodes of all trees back to back, ``parents`` [total_q] int32 each node's parent within its tree (-1: a child of the
+    context; parents come first), ``plan`` is the SpanPlan of the node counts (at most 256 a tree).  A ``window`` (0: none)
+    goes by the nodes' depths.  Returns ``out`` [total_q, Hq, D]."""
+    _need(plan.max_q_len <= TREE_NODES_MOST, f"a tree has at most {TREE_NODES_MOST} nodes")
+    _need(parents is not None, "parents is required")
+    return _span(q, k_cache, v_cache, block_table, seq_lens, parents, plan, max_kv_len, window, sinks, scale, num_splits,
+                 total_kv, workspace, out, stream)
+
+
+# ---- page tables ---------------------------------------------------------------------------
+
+def kv_resize_paged(old_lens, new_lens, block_table, free_pages, num_free, *, page_size: int, total_rows: int = 0,
+                    indptr=None, slots=None, slot_dtype=torch.int64, stream=None):
+    """Pages taken and returned on the GPU as the lengths of a batch change (include/dap.h: kv_resize_paged): updates
+    ``block_table`` [B, max_pages] and the stack of free pages (``free_pages`` [num_pages], ``num_free`` [1]) in place, and
+    returns (indptr [B + 1], slots [total_rows]): the boundaries of the new rows and each one's slot (int64 or int32), -1
+    behind the last.  Lengths, tables and stack are int32 on one device."""
+    return (_ext or load_native()).resize(old_lens, new_lens, block_table, free_pages, num_free, int(page_size),
+                                          int(total_rows), indptr, slots, _SLOT_BYTES.get(slot_dtype, 0),
+                                          None if stream is None else _stream(stream, block_table.get_device()))
+
+
+def kv_commit_paged(k_cache, v_cache, block_table, positions, path, accepted, *, stream=None):
+    """Accepted drafts into place (include/dap.h: kv_commit_paged): for j < accepted[b] the K/V rows of place
+    positions[b] + path[b, j] go to place positions[b] + j.  ``path`` [B, max_path] holds the accepted nodes of each tree in
+    ascending order.  Returns (k_cache, v_cache), updated in place."""
+    (_ext or load_native()).commit(k_cache, v_cache, block_table, positions, path, accepted,
+                                   None if stream is None else _stream(stream, k_cache.get_device()))
+    return k_cache, v_cache
 
 
 # ---- cache writes ------------------------------------------------------------------------

@@ -98,6 +98,14 @@ dap_status check_mask(const uint8_t *mask, long long mask_stride, int max_kv_len
     return DAP_OK;
 }
 
+// The most keys that a work tile of the span calls has, in tiles' order: the window of its first token, `tokens` new
+// ones, the sinks, and what rounding both spans to 64 adds.
+int span_keys(int max_kv_len, int window, int sinks, int tokens) {
+    if (window <= 0) return max_kv_len;
+    const long long keys = (long long)window + ceil_div_ll(sinks, kTileTokens) * kTileTokens + (kTileTokens - 2) + tokens;
+    return (int)std::min<long long>(max_kv_len, keys);
+}
+
 }  // namespace
 }  // namespace dap
 
@@ -681,6 +689,181 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
     return merged ? DAP_OK : launch_shared_combine(a, cs);
 }
 
+int dap_span_tokens_per_tile(int Hq, int Hkv, int D, int max_q_len) {
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !supported_group(Hq / Hkv) || max_q_len < 0) return 0;
+    return span_tokens_per_tile(Hq / Hkv, D, max_q_len);
+}
+
+int dap_span_splits(int sm_count, int num_tiles, int Hq, int Hkv, int D, int tokens_per_tile, int max_kv_len, int window,
+                    int sinks, int tree, long long total_kv, int num_splits) {
+    if (num_tiles < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || tokens_per_tile < 1 || max_kv_len < 0 ||
+        window < 0 || sinks < 0 || num_splits < 0 || total_kv < 0)
+        return 0;
+    const int most = span_keys(max_kv_len, window, sinks, tree ? kTreeMost : tokens_per_tile);
+    if (total_kv > 0) total_kv = std::min(total_kv, (long long)num_tiles * most);
+    return dap_resolve_splits(num_splits, sm_count, num_tiles, Hq, Hkv, D, 1, most, total_kv);
+}
+
+static dap_status span_call(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                            const void *v_cache, int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                            const int32_t *seq_lens, const int32_t *parents, bool tree, const int32_t *qo_indptr,
+                            const int32_t *tile_batch, const int32_t *tile_index, int num_tiles, int tokens_per_tile,
+                            int total_q, int window, int sinks, int max_kv_len, int B, int Hq, int Hkv, int D,
+                            float scale, int num_splits, void *workspace, size_t workspace_bytes, void *out,
+                            long long out_stride_t, long long out_stride_h, void *stream) {
+    constexpr int kMostKeys = (1 << 30) - 64;  // (places, rounded up and with a chunk added, stay inside 32 bits)
+    if (total_q < 0 || num_tiles < 0 || B < 0 || window < (tree ? 0 : 1) || sinks < 0 || max_kv_len > kMostKeys)
+        return DAP_ERR_SHAPE;
+    if (total_q == 0 && num_tiles == 0) return DAP_OK;
+    if (B == 0 || total_q == 0 || num_tiles == 0 || num_tiles > total_q) return DAP_ERR_SHAPE;
+    dap_status st = check_common(q, q_stride_t, q_stride_h, seq_lens, max_kv_len, total_q, Hq, Hkv, D, scale,
+                                 num_splits, out, out_stride_t, out_stride_h);
+    if (st != DAP_OK) return st;
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 || (long long)max_kv_len > (long long)max_pages * page_size)
+        return DAP_ERR_SHAPE;
+    if (!k_cache || !v_cache || !block_table || (tree && !parents)) return DAP_ERR_NULL;
+    const bool mapped = qo_indptr || tile_batch || tile_index;
+    if (mapped && !(qo_indptr && tile_batch && tile_index)) return DAP_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(qo_indptr) ||
+        !aligned4(tile_batch) || !aligned4(tile_index) || !aligned4(parents))
+        return DAP_ERR_ALIGN;
+    const int G = Hq / Hkv;
+    const bool known = tokens_per_tile == 8 / G || tokens_per_tile == 16 / G ||
+                       tokens_per_tile == span_tokens_per_tile(G, D, 0x7FFFFFFF);
+    if (!known || (!mapped && (total_q != B || num_tiles != B || tokens_per_tile != 8 / G))) return DAP_ERR_SHAPE;
+    if (window >= max_kv_len) window = 0;  // (no token is further from a key)
+    if (window == 0) sinks = 0;
+    sinks = std::min(sinks, max_kv_len);
+    int sms = 0;
+    if (num_splits == 0 && (sms = dap_device_sm_count()) <= 0) return DAP_ERR_CUDA;
+    const int S = dap_span_splits(sms, num_tiles, Hq, Hkv, D, tokens_per_tile, max_kv_len, window, sinks, tree, 0,
+                                  num_splits);
+    if (S == 0) return DAP_ERR_SHAPE;
+    if (S > 1 && (!workspace || workspace_bytes < dap_workspace_bytes_multi(total_q, Hq, D, S) || !aligned16(workspace)))
+        return DAP_ERR_WORKSPACE;
+    SpanArgs a = {};
+    a.d.paged = true;
+    a.d.q = q;
+    a.d.q_sb = q_stride_t;
+    a.d.q_sh = q_stride_h;
+    a.d.k = k_cache;
+    a.d.v = v_cache;
+    a.d.num_pages = num_pages;
+    a.d.page_size = page_size;
+    a.d.block_table = block_table;
+    a.d.max_pages = max_pages;
+    a.d.seq_lens = seq_lens;
+    a.d.max_kv_len = max_kv_len;
+    a.d.B = B;
+    a.d.Hq = Hq;
+    a.d.Hkv = Hkv;
+    a.d.D = D;
+    a.d.scale = scale;
+    a.d.num_splits = S;
+    a.d.chunk = dap_chunk_tokens(span_keys(max_kv_len, window, sinks, tree ? kTreeMost : tokens_per_tile), S);
+    a.d.workspace = workspace;
+    a.d.out = out;
+    a.d.o_sb = out_stride_t;
+    a.d.o_sh = out_stride_h;
+    a.d.qo_indptr = qo_indptr;
+    a.d.tile_batch = tile_batch;
+    a.d.tile_index = tile_index;
+    a.d.num_tiles = num_tiles;
+    a.d.tokens_per_tile = tokens_per_tile;
+    a.d.total_q = total_q;
+    a.parents = tree ? parents : nullptr;
+    a.window = window;
+    a.sinks = sinks;
+    return launch_span(a, static_cast<cudaStream_t>(stream));
+}
+
+dap_status decode_attn_paged_window(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                                    const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                                    int max_pages, const int32_t *seq_lens, const int32_t *qo_indptr,
+                                    const int32_t *tile_batch, const int32_t *tile_index, int num_tiles,
+                                    int tokens_per_tile, int total_q, int window, int sinks, int max_kv_len, int B,
+                                    int Hq, int Hkv, int D, float scale, int num_splits, void *workspace,
+                                    size_t workspace_bytes, void *out, long long out_stride_t, long long out_stride_h,
+                                    void *stream) {
+    return span_call(q, q_stride_t, q_stride_h, k_cache, v_cache, num_pages, page_size, block_table, max_pages, seq_lens,
+                     nullptr, false, qo_indptr, tile_batch, tile_index, num_tiles, tokens_per_tile, total_q, window, sinks,
+                     max_kv_len, B, Hq, Hkv, D, scale, num_splits, workspace, workspace_bytes, out, out_stride_t,
+                     out_stride_h, stream);
+}
+
+dap_status decode_attn_paged_tree(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                                  const void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                                  int max_pages, const int32_t *seq_lens, const int32_t *parents,
+                                  const int32_t *qo_indptr, const int32_t *tile_batch, const int32_t *tile_index,
+                                  int num_tiles, int tokens_per_tile, int total_q, int window, int sinks,
+                                  int max_kv_len, int B, int Hq, int Hkv, int D, float scale, int num_splits,
+                                  void *workspace, size_t workspace_bytes, void *out, long long out_stride_t,
+                                  long long out_stride_h, void *stream) {
+    return span_call(q, q_stride_t, q_stride_h, k_cache, v_cache, num_pages, page_size, block_table, max_pages, seq_lens,
+                     parents, true, qo_indptr, tile_batch, tile_index, num_tiles, tokens_per_tile, total_q, window, sinks,
+                     max_kv_len, B, Hq, Hkv, D, scale, num_splits, workspace, workspace_bytes, out, out_stride_t,
+                     out_stride_h, stream);
+}
+
+dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page_size, const int32_t *block_table,
+                           int max_pages, const int32_t *positions, const int32_t *path, const int32_t *accepted,
+                           int max_path, int B, int Hkv, int D, void *stream) {
+    if (B < 0 || Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1 || max_pages < 1 || max_path < 0 ||
+        max_path > kTreeMost)
+        return DAP_ERR_SHAPE;
+    if (B == 0 || max_path == 0) return DAP_OK;
+    if (!k_cache || !v_cache || !block_table || !positions || !path || !accepted) return DAP_ERR_NULL;
+    if (D % 8 != 0) return DAP_ERR_UNSUPPORTED;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(positions) || !aligned4(path) ||
+        !aligned4(accepted))
+        return DAP_ERR_ALIGN;
+    CommitArgs a = {};
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.positions = positions;
+    a.path = path;
+    a.accepted = accepted;
+    a.max_path = max_path;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.D = D;
+    return launch_commit(a, static_cast<cudaStream_t>(stream));
+}
+
+dap_status kv_resize_paged(const int32_t *old_lens, const int32_t *new_lens, int32_t *block_table, int max_pages,
+                           int page_size, int32_t *free_pages, int num_pages, int32_t *num_free, int32_t *indptr,
+                           void *slots, int slot_bytes, int total_rows, int B, void *stream) {
+    if (B < 0 || max_pages < 1 || page_size < 1 || num_pages < 1 || total_rows < 0 || (slot_bytes != 4 && slot_bytes != 8))
+        return DAP_ERR_SHAPE;
+    if (B > kResizeMost || (long long)B * max_pages > (1LL << 30) ||
+        (slot_bytes == 4 && (long long)num_pages * page_size > 0x7FFFFFFFLL))
+        return DAP_ERR_UNSUPPORTED;
+    if (!indptr || !free_pages || !num_free || (total_rows > 0 && !slots)) return DAP_ERR_NULL;
+    if (B > 0 && (!old_lens || !new_lens || !block_table)) return DAP_ERR_NULL;
+    if (!aligned4(old_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+        !aligned4(num_free) || !aligned4(indptr) || (reinterpret_cast<uintptr_t>(slots) & (unsigned)(slot_bytes - 1)))
+        return DAP_ERR_ALIGN;
+    ResizeArgs a = {};
+    a.old_lens = old_lens;
+    a.new_lens = new_lens;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.free_pages = free_pages;
+    a.num_pages = num_pages;
+    a.num_free = num_free;
+    a.indptr = indptr;
+    a.slots = slots;
+    a.slot_bytes = slot_bytes;
+    a.rows = total_rows;
+    a.B = B;
+    return launch_resize(a, static_cast<cudaStream_t>(stream));
+}
+
 static dap_status fp8_runs(bool write, const void *k_rows, const void *v_rows, long long k_stride_t,
                            long long k_stride_h, long long v_stride_t, long long v_stride_h, const uint8_t *k_codes,
                            const uint8_t *v_codes, const void *k_scale, const void *v_scale, int num_pages,
@@ -832,6 +1015,9 @@ dap_status dap_get_device_errors(unsigned int *flags, int clear) {
     if (!read_errors_shared_prefix(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_shared_suffix(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_shared_suffix_gather(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_span(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_span_gather(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_tables(flags, clear != 0)) return DAP_ERR_CUDA;
     return DAP_OK;
 }
 

@@ -158,6 +158,46 @@ struct RunArgs {
 dap_status launch_fp8_runs(const RunArgs &a, bool write, cudaStream_t stream);
 bool read_errors_fp8_runs(unsigned int *flags, bool clear);
 
+// Lengths of a batch changed on the GPU, already validated.
+constexpr int kResizeMost = 16384;  // sequences: three prefix sums of theirs fit a CTA's shared memory
+struct ResizeArgs {
+    const int32_t *old_lens, *new_lens;
+    int32_t *block_table;
+    int max_pages, page_size;
+    int32_t *free_pages;
+    int num_pages;
+    int32_t *num_free, *indptr;
+    void *slots;
+    int slot_bytes, rows, B;
+};
+dap_status launch_resize(const ResizeArgs &a, cudaStream_t stream);
+
+// Accepted drafts moved behind the context, already validated.
+struct CommitArgs {
+    void *k_cache, *v_cache;
+    int num_pages, page_size;
+    const int32_t *block_table;
+    int max_pages;
+    const int32_t *positions, *path, *accepted;
+    int max_path, B, Hkv, D;
+};
+dap_status launch_commit(const CommitArgs &a, cudaStream_t stream);
+bool read_errors_tables(unsigned int *flags, bool clear);
+
+// Attention of new tokens over spans of the cache (a window and first tokens, a tree of drafts), already validated:
+// DecodeArgs with its work map (none: one token a sequence), and
+struct SpanArgs {
+    DecodeArgs d;
+    const int32_t *parents;  // of the tree's nodes, or NULL: causal
+    int window, sinks;       // window 0: none
+};
+constexpr int kTreeMost = 256;  // nodes of one tree
+int span_tokens_per_tile(int G, int D, int max_q_len);
+dap_status launch_span(const SpanArgs &a, cudaStream_t stream);
+dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream);
+bool read_errors_span(unsigned int *flags, bool clear);
+bool read_errors_span_gather(unsigned int *flags, bool clear);
+
 bool read_errors_multi(unsigned int *flags, bool clear);
 bool read_errors_multi_gather(unsigned int *flags, bool clear);
 bool read_errors_multi_tc(unsigned int *flags, bool clear);

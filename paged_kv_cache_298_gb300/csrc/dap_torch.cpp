@@ -281,6 +281,143 @@ PyObject *decode_shared(PyObject *const *a) {
     return THPVariable_Wrap(out);
 }
 
+// The bf16 paged caches' shape.
+struct Caches {
+    int P, ps, Hkv, D;
+    Caches(const at::Tensor &k, const at::Tensor &v) {
+        if (k.scalar_type() != at::kBFloat16 || k.dim() != 4 || !k.is_contiguous() || v.scalar_type() != at::kBFloat16 ||
+            v.sizes() != k.sizes() || !v.is_contiguous())
+            value_error("k_cache/v_cache must be contiguous bf16 [P, ps, Hkv, D]");
+        P = fit(k.size(0), "too many pages");
+        ps = fit(k.size(1), "page size too large");
+        Hkv = fit(k.size(2), "too many heads");
+        D = fit(k.size(3), "head dim too large");
+    }
+};
+
+// decode_span(q, k_cache, v_cache, block_table, seq_lens, parents, the plan's map [qo_indptr, tile_batch, tile_index],
+// (B, total_q, tiles, tokens_per_tile, Hq, Hkv, D), window, sinks, max_kv_len, num_splits, scale, workspace, out, stream)
+// -> out
+PyObject *decode_span(PyObject *const *a) {
+    const bool tree = a[5] != Py_None;
+    const char *what = tree ? "decode_attn_paged_tree" : "decode_attn_paged_window";
+    Call c{what};
+    const at::Tensor &q = c.tensor(a[0], "q"), &k = c.tensor(a[1], "k_cache"), &v = c.tensor(a[2], "v_cache");
+    const at::Tensor &bt = c.tensor(a[3], "block_table"), &sl = c.tensor(a[4], "seq_lens");
+    const at::Tensor *pa = c.optional(a[5], "parents"), *map = c.optional(a[6], "plan");
+    const at::Tensor *wg = c.optional(a[13], "workspace"), *og = c.optional(a[14], "out");
+    int d[7];
+    for (int i = 0; i < 7; ++i) d[i] = integer32(PyTuple_GET_ITEM(a[7], i));
+    const int B = d[0], total = d[1], tiles = d[2], Hq = d[4], Hkv = d[5], D = d[6];
+    if (map && (!int32s(*map) || map->numel() != (int64_t)B + 1 + 2 * (int64_t)tiles))
+        value_error("the plan's map does not fit its sizes");
+    rows3(q, "q must be a bf16 [*, *, D] tensor with unit stride in D");
+    if (q.size(0) != total || q.size(1) != Hq || q.size(2) != D)
+        value_error("q differs from the plan's token count, heads or head dim");
+    const Caches kv(k, v);
+    if (kv.Hkv != Hkv || kv.D != D) value_error("the cache's kv heads or head dim differ from the plan's");
+    table_of(bt, B);
+    if (!int32s(sl) || sl.numel() != B) value_error("seq_lens must be contiguous int32 [B]");
+    if (pa && (!int32s(*pa) || pa->numel() != total)) value_error("parents must be contiguous int32 [total_q]");
+    const int max_pages = fit(bt.size(1), "block_table too wide");
+    const int window = integer32(a[8]), sinks = integer32(a[9]), max_len = integer32(a[10]), S = integer32(a[11]);
+    const double scale = PyFloat_AsDouble(a[12]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+    const On on(a[15], c.device);
+    at::Tensor out, ws;
+    if (og) {
+        rows3(*og, "out must be a bf16 [*, *, D] tensor with unit stride in D");
+        if (og->sizes() != q.sizes()) value_error("out must be [total_q, Hq, D]");
+        out = *og;
+    } else {
+        out = fresh({total, Hq, D}, at::kBFloat16, c.device);
+    }
+    ws = wg ? *wg : fresh({(int64_t)dap_workspace_bytes_multi(total, Hq, D, S)}, at::kByte, c.device);
+    if (!ws.is_contiguous()) value_error("workspace must be contiguous");
+    const int32_t *m = map ? static_cast<const int32_t *>(map->data_ptr()) : nullptr;
+    const int32_t *tb = m ? m + B + 1 : nullptr, *ti = m ? tb + tiles : nullptr;
+    const int32_t *table = static_cast<const int32_t *>(bt.data_ptr()), *lens = static_cast<const int32_t *>(sl.data_ptr());
+    const int32_t *parents = pa ? static_cast<const int32_t *>(pa->data_ptr()) : nullptr;
+    dap_status st;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
+    if (tree)
+        st = decode_attn_paged_tree(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), kv.P, kv.ps, table,
+                                    max_pages, lens, parents, m, tb, ti, tiles, d[3], total, window, sinks, max_len, B, Hq,
+                                    Hkv, D, (float)scale, S, ws.data_ptr(), ws.nbytes(), out.data_ptr(), out.stride(0),
+                                    out.stride(1), on.stream);
+    else
+        st = decode_attn_paged_window(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), kv.P, kv.ps,
+                                      table, max_pages, lens, m, tb, ti, tiles, d[3], total, window, sinks, max_len, B, Hq,
+                                      Hkv, D, (float)scale, S, ws.data_ptr(), ws.nbytes(), out.data_ptr(), out.stride(0),
+                                      out.stride(1), on.stream);
+    Py_END_ALLOW_THREADS;
+    check_status(st, what);
+    return THPVariable_Wrap(out);
+}
+
+int32_t *ints(const at::Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); }
+
+// resize(old_lens, new_lens, block_table, free_pages, num_free, page_size, total_rows, indptr, slots, bytes of a slot that
+// is made here, stream) -> (indptr, slots)
+PyObject *resize(PyObject *const *a) {
+    const char *what = "kv_resize_paged";
+    Call c{what};
+    const at::Tensor &ol = c.tensor(a[0], "old_lens"), &nl = c.tensor(a[1], "new_lens"), &bt = c.tensor(a[2], "block_table");
+    const at::Tensor &fp = c.tensor(a[3], "free_pages"), &nf = c.tensor(a[4], "num_free");
+    const at::Tensor *ig = c.optional(a[7], "indptr"), *sg = c.optional(a[8], "slots");
+    const int B = fit(ol.numel(), "too many sequences"), ps = integer32(a[5]), rows = integer32(a[6]);
+    if (!int32s(ol) || !int32s(nl) || nl.numel() != B) value_error("old_lens and new_lens must be contiguous int32 [B]");
+    table_of(bt, B);
+    if (!int32s(fp)) value_error("free_pages must be contiguous int32 [num_pages]");
+    if (!int32s(nf) || nf.numel() != 1) value_error("num_free must be int32 [1]");
+    if (ig && (!int32s(*ig) || ig->numel() != (int64_t)B + 1)) value_error("indptr must be contiguous int32 [B + 1]");
+    if (rows < 0) value_error("total_rows must not be negative");
+    int bytes = integer32(a[9]);
+    if (sg) {
+        bytes = sg->scalar_type() == at::kLong ? 8 : sg->scalar_type() == at::kInt ? 4 : 0;
+        if (!bytes || !sg->is_contiguous() || sg->numel() != rows)
+            value_error("slots must be contiguous int64 or int32 [total_rows]");
+    }
+    if (bytes != 4 && bytes != 8) value_error("slot_dtype must be int64 or int32");
+    const int P = fit(fp.numel(), "too many pages"), max_pages = fit(bt.size(1), "block_table too wide");
+    const On on(a[10], c.device);
+    const at::Tensor indptr = ig ? *ig : fresh({(int64_t)B + 1}, at::kInt, c.device);
+    const at::Tensor slots = sg ? *sg : fresh({rows}, bytes == 8 ? at::kLong : at::kInt, c.device);
+    dap_status st;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
+    st = kv_resize_paged(ints(ol), ints(nl), ints(bt), max_pages, ps, ints(fp), P, ints(nf), ints(indptr),
+                         slots.data_ptr(), bytes, rows, B, on.stream);
+    Py_END_ALLOW_THREADS;
+    check_status(st, what);
+    PyObject *x = THPVariable_Wrap(indptr), *y = THPVariable_Wrap(slots);
+    PyObject *both = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return both;
+}
+
+// commit(k_cache, v_cache, block_table, positions, path, accepted, stream)
+void commit(PyObject *const *a) {
+    const char *what = "kv_commit_paged";
+    Call c{what};
+    const at::Tensor &k = c.tensor(a[0], "k_cache"), &v = c.tensor(a[1], "v_cache"), &bt = c.tensor(a[2], "block_table");
+    const at::Tensor &po = c.tensor(a[3], "positions"), &pt = c.tensor(a[4], "path"), &ac = c.tensor(a[5], "accepted");
+    const Caches kv(k, v);
+    const int B = fit(po.numel(), "too many sequences");
+    table_of(bt, B);
+    if (!int32s(po)) value_error("positions must be contiguous int32 [B]");
+    if (!int32s(pt) || pt.dim() != 2 || pt.size(0) != B) value_error("path must be contiguous int32 [B, max_path]");
+    if (!int32s(ac) || ac.numel() != B) value_error("accepted must be contiguous int32 [B]");
+    const int max_pages = fit(bt.size(1), "block_table too wide"), most = fit(pt.size(1), "path too wide");
+    const On on(a[6], c.device);
+    dap_status st;
+    Py_BEGIN_ALLOW_THREADS;  // (nothing in here may raise)
+    st = kv_commit_paged(k.data_ptr(), v.data_ptr(), kv.P, kv.ps, ints(bt), max_pages, ints(po), ints(pt), ints(ac), most,
+                         B, kv.Hkv, kv.D, on.stream);
+    Py_END_ALLOW_THREADS;
+    check_status(st, what);
+}
+
 template <class F>
 PyObject *entry(Py_ssize_t n, Py_ssize_t want, F f) {
     HANDLE_TH_ERRORS
@@ -308,6 +445,18 @@ PyObject *py_read_runs(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *py_decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return entry(n, 15, [&] { return decode_shared(a); });
 }
+PyObject *py_decode_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 16, [&] { return decode_span(a); });
+}
+PyObject *py_resize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 11, [&] { return resize(a); });
+}
+PyObject *py_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry(n, 7, [&]() -> PyObject * {
+        commit(a);
+        Py_RETURN_NONE;
+    });
+}
 PyObject *py_set_error(PyObject *, PyObject *cls) {
     Py_XINCREF(cls);
     Py_XSETREF(g_error, cls);
@@ -323,6 +472,10 @@ PyMethodDef g_methods[] = {
     {"append_runs", as_function(py_append_runs), METH_FASTCALL, "kv_append_paged_fp8_multi on tensors"},
     {"read_runs", as_function(py_read_runs), METH_FASTCALL, "kv_read_paged_fp8 on tensors"},
     {"decode_shared", as_function(py_decode_shared), METH_FASTCALL, "decode_attn_paged_shared on tensors"},
+    {"decode_span", as_function(py_decode_span), METH_FASTCALL,
+     "decode_attn_paged_window and decode_attn_paged_tree on tensors"},
+    {"resize", as_function(py_resize), METH_FASTCALL, "kv_resize_paged on tensors"},
+    {"commit", as_function(py_commit), METH_FASTCALL, "kv_commit_paged on tensors"},
     {"set_error", py_set_error, METH_O, "the exception class for library statuses"},
     {nullptr, nullptr, 0, nullptr},
 };
