@@ -1017,6 +1017,7 @@ dap_status dap_get_device_errors(unsigned int *flags, int clear) {
     if (!read_errors_shared_suffix_gather(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_span(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_span_gather(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_span_tc(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_tables(flags, clear != 0)) return DAP_ERR_CUDA;
     return DAP_OK;
 }

@@ -195,6 +195,8 @@ constexpr int kTreeMost = 256;  // nodes of one tree
 int span_tokens_per_tile(int G, int D, int max_q_len);
 dap_status launch_span(const SpanArgs &a, cudaStream_t stream);
 dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream);
+dap_status launch_span_tc(const SpanArgs &a, cudaStream_t stream);
+bool read_errors_span_tc(unsigned int *flags, bool clear);
 bool read_errors_span(unsigned int *flags, bool clear);
 bool read_errors_span_gather(unsigned int *flags, bool clear);
 

@@ -4,14 +4,17 @@
 
 namespace dap {
 
-// 8 / G tokens while they hold the longest run of new tokens, else 16 / G.
+// 8 / G tokens, or 16 / G, while they hold the longest run of new tokens; beyond that the rows of tensor-memory products
+// where the head dim has them.
 int span_tokens_per_tile(int G, int D, int max_q_len) {
-    (void)D;
     if (G < 1 || G > 8) return 0;
-    return max_q_len <= 8 / G ? 8 / G : 16 / G;
+    if (max_q_len <= 8 / G) return 8 / G;
+    if (max_q_len > 16 / G && (D == 64 || D == 128 || D == 256)) return (D == 256 ? 128 : 256) / G;
+    return 16 / G;
 }
 
 dap_status launch_span(const SpanArgs &a, cudaStream_t stream) {
+    if (a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) >= 128) return launch_span_tc(a, stream);
     return a.d.page_size % 8 != 0 ? launch_span_gather(a, stream) : span_dims<false>(a, stream);
 }
 

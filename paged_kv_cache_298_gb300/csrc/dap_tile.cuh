@@ -173,6 +173,77 @@ __device__ __forceinline__ void fill_tile_rows(uint8_t *stage, const RowPages<C>
     cp_async_mbar_arrive(full);
 }
 
+// Page ids of a producer warp: lane l holds entries base + l and base + 32 + l of the sequence's table row, so that a
+// load of 32 entries serves 32 pages and is in flight while the 32 before it are used.  (A page id that was loaded for
+// the next tile and range-checked at once held the warp for the load's latency: 0.3 us a tile.)
+struct PageWindow {
+    const int32_t *row;
+    int base, end, lane;
+    int cur, nxt;
+    __device__ __forceinline__ PageWindow(const int32_t *row_, int first, int max_pages, int lane_)
+        : row(row_), base(first), end(max_pages), lane(lane_) {
+        cur = get(first + lane);
+        nxt = get(first + 32 + lane);
+    }
+    __device__ __forceinline__ int get(int e) const { return e < end ? __ldg(row + e) : 0; }
+    // Entry e of each lane, first <= e < first + 32 (first: the same in every lane, never falling).
+    __device__ __forceinline__ int at(int e, int first) {
+        if (first >= base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = get(base + 32 + lane);
+        }
+        const int a = __shfl_sync(0xFFFFFFFFu, cur, e - base), b = __shfl_sync(0xFFFFFFFFu, nxt, e - base - 32);
+        return e - base < 32 ? a : b;
+    }
+};
+
+// Row gather of a tile of one tensor, or (BOTH) of K and V behind each other: fill_tile_rows with the source rows of
+// eight copies exchanged before the first of them is issued, since a copy's row otherwise costs it the latency of a
+// shuffle (a 64-key prefix tile at page size 12: 0.53 us for 0.65 at D = 64, 0.64 for 1.61 at D = 128, 1.00 for 1.27 at
+// D = 256).  A row's number fits 32 bits: 2^32 rows of 64 dims are 550 GB.
+template <class C, bool BOTH>
+__device__ __forceinline__ void gather_rows(uint8_t *tile, const __nv_bfloat16 *x, const __nv_bfloat16 *y,
+                                            const RowPages<C> &rp, int nvalid, int kvh, const SplitParams &p,
+                                            uint64_t *full, int lane) {
+    constexpr int CPR = C::ROWB / 16, N = RowPages<C>::N, RPI = 32 / CPR, U = 8;
+    static_assert(C::SWB == 128 && RPI <= 8 && C::BT % (RPI * U) == 0, "batches of whole rows");
+    uint32_t row[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        int pg = rp.pg[k];
+        if (lane + 32 * k < nvalid && (pg < 0 || pg >= p.num_pages)) {
+            flag_error(DAP_DEVERR_PAGE);
+            pg = 0;
+        }
+        row[k] = (uint32_t)pg * (uint32_t)p.page_size + (uint32_t)rp.slot[k];
+    }
+    if (lane == 0) mbar_arrive(full);
+    const int c = lane % CPR, r0 = lane / CPR;
+    const uint32_t pitch = (uint32_t)(p.Hkv * C::D * 2);
+    const uint32_t to = smem_addr(tile) + c / C::CPB * (C::BT * 128) + r0 * 128 + ((c % C::CPB ^ r0) << 4);
+    const char *sx = reinterpret_cast<const char *>(x + (long long)kvh * C::D + c * 8);
+    const char *sy = BOTH ? reinterpret_cast<const char *>(y + (long long)kvh * C::D + c * 8) : nullptr;
+#pragma unroll
+    for (int i0 = 0; i0 < C::BT / RPI; i0 += U) {
+        uint32_t src[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            src[u] = __shfl_sync(0xFFFFFFFFu, row[(RPI * (i0 + u)) >> 5], (r0 + RPI * (i0 + u)) & 31);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = RPI * (i0 + u);  // (+ r0: the swizzle's chunk is c ^ r0 ^ r's low bits)
+            if (r0 + r < nvalid) {
+                const uint32_t dst = (to ^ ((r & 7) << 4)) + r * 128;
+                const unsigned long long off = (unsigned long long)src[u] * pitch;
+                cp_async_16(dst, sx + off);
+                if (BOTH) cp_async_16(dst + C::TILE_BYTES, sy + off);
+            }
+        }
+    }
+    cp_async_mbar_arrive(full);
+}
+
 // Arrivals a stage's full barrier expects: one (the producer's arrive with the TMA byte
 // count), or in row-gather mode one per producer lane plus lane 0's own arrive (which
 // carries the bytes of the tile's TMA copies).
