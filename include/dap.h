@@ -451,17 +451,17 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
  * in it, of which ctx = seq_lens[b] - q_len[b] lie in front of its new tokens, and new token i is in place ctx + i.
  *
  * dap_span_tokens_per_tile: new tokens of a work tile of these calls (dap_q_tile_map builds the map with it): 8 / G or
- * 16 / G while they hold the longest run of new tokens, longer runs of head dims 64, 128 and 256 in 128 or 256 rows of
- * tensor-memory products; 0 for unsupported heads.
+ * 16 / G while they hold the longest run of new tokens, longer runs of head dims 64, 128 and 256 in 128 or, where a batch
+ * of B sequences fills the device's sm_count SMs with them, 256 rows of tensor-memory products; 0 for unsupported heads.
  * dap_span_splits: the split count that a call runs for the num_splits it is given (0: the planner's).  The keys of a
  * tile are at most the window, the sinks and what rounding to 64 keys adds, so they, not the lengths, are cut.
  *   tree      whether the call has parents.  total_kv: sum of seq_lens (host), 0: unknown.
  * Returns 0 for invalid arguments.  Size the workspace with dap_workspace_bytes_multi(total_q, Hq, D, <the value>).
  * Pure host functions; no CUDA call.
  */
-int dap_span_tokens_per_tile(int Hq, int Hkv, int D, int max_q_len);
-int dap_span_splits(int sm_count, int num_tiles, int Hq, int Hkv, int D, int tokens_per_tile, int max_kv_len, int window,
-                    int sinks, int tree, long long total_kv, int num_splits);
+int dap_span_tokens_per_tile(int sm_count, int B, int Hq, int Hkv, int D, int max_q_len);
+int dap_span_splits(int sm_count, int num_tiles, int total_q, int B, int Hq, int Hkv, int D, int tokens_per_tile,
+                    int max_kv_len, int window, int sinks, int tree, long long total_kv, int num_splits);
 
 /*
  * Sliding-window paged GQA attention with sinks, for one or many new tokens a sequence: token i, in place and position
@@ -473,7 +473,7 @@ int dap_span_splits(int sm_count, int num_tiles, int Hq, int Hkv, int D, int tok
  *                flagged (DAP_DEVERR_QMAP); tokens that no entry names have undefined results.
  *   qo_indptr, tile_batch, tile_index   the work map, made with tokens_per_tile; or all three NULL: one new token a
  *                sequence (total_q = num_tiles = B, tokens_per_tile 8 / G).
- *   tokens_per_tile  8 / G, 16 / G or, at D 64, 128 and 256, dap_span_tokens_per_tile's for long runs.
+ *   tokens_per_tile  8 / G, 16 / G or, at D 64, 128 and 256, 128 / G or, at D 64 and 128, 256 / G.
  *   window       >= 1 (one that reaches max_kv_len is none).  sinks >= 0.
  *   num_splits   as dap_span_splits on the device's SMs with total_kv = 0.
  *   workspace    >= dap_workspace_bytes_multi(total_q, Hq, D, S) bytes for the S used, 16-byte aligned.  Calls that may

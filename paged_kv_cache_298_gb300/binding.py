@@ -145,9 +145,9 @@ def load(build_if_missing: bool = True):
         lib.decode_attn_paged_shared.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I,
                                                  F, I, I, P, SZ, P, LL, LL, P]
         lib.decode_attn_paged_shared.restype = I
-        lib.dap_span_tokens_per_tile.argtypes = [I, I, I, I]
+        lib.dap_span_tokens_per_tile.argtypes = [I, I, I, I, I, I]
         lib.dap_span_tokens_per_tile.restype = I
-        lib.dap_span_splits.argtypes = [I, I, I, I, I, I, I, I, I, I, LL, I]
+        lib.dap_span_splits.argtypes = [I, I, I, I, I, I, I, I, I, I, I, I, LL, I]
         lib.dap_span_splits.restype = I
         lib.decode_attn_paged_window.argtypes = [P, LL, LL, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
                                                  F, I, P, SZ, P, LL, LL, P]
@@ -744,17 +744,25 @@ def decode_attn_paged_shared(q, k_cache, v_cache, block_table, seq_lens, prefix_
 
 class SpanPlan:
     """The work map of one batch of new-token counts for decode_attn_paged_window and decode_attn_paged_tree, made once
-    for as long as the counts last (a decode step of B sequences: ``[1] * B``).  The lengths are not part of it."""
+    for as long as the counts last (a decode step of B sequences: ``[1] * B``).  The lengths are not part of it.
+    Without tokens_per_tile the library's rule picks it."""
 
-    def __init__(self, q_lens, Hq: int, Hkv: int, D: int, device):
+    def __init__(self, q_lens, Hq: int, Hkv: int, D: int, device, tokens_per_tile: int | None = None):
         ql = [int(n) for n in (q_lens.tolist() if isinstance(q_lens, torch.Tensor) else q_lens)]
         self.Hq, self.Hkv, self.D = int(Hq), int(Hkv), int(D)
         self.max_q_len = max(ql, default=0)
-        self.tokens_per_tile = load().dap_span_tokens_per_tile(self.Hq, self.Hkv, self.D, max(0, self.max_q_len))
+        if tokens_per_tile is None:
+            lib, sms = load(), 0
+            if torch.device(device).type == "cuda":
+                with _on(torch.device(device).index if torch.device(device).index is not None else _current_device()):
+                    sms = lib.dap_device_sm_count()
+            tokens_per_tile = lib.dap_span_tokens_per_tile(sms, len(ql), self.Hq, self.Hkv, self.D, max(0, self.max_q_len))
+        self.tokens_per_tile = int(tokens_per_tile)
         _need(self.tokens_per_tile > 0, "Hq / Hkv must be 1, 2, 4 or 8")
         _need(min(ql, default=0) >= 0 and sum(ql) < 1 << 31, "q_lens must be counts >= 0")
         self.B, self.total_q = len(ql), sum(ql)
-        if ql and min(ql) == self.max_q_len == 1:   # a token each: the library needs no map
+        G = self.Hq // self.Hkv
+        if ql and min(ql) == self.max_q_len == 1 and self.tokens_per_tile * G == 8:   # a token each: no map is needed
             self.num_tiles, self.map = self.B, None
         else:
             qi, tb, ti = q_tile_map(ql, self.tokens_per_tile)
@@ -780,8 +788,8 @@ class SpanPlan:
             if device >= 0:
                 with _on(device):
                     sms = lib.dap_device_sm_count()
-            found = lib.dap_span_splits(sms, self.num_tiles, self.Hq, self.Hkv, self.D, self.tokens_per_tile, max_kv_len,
-                                        window, sinks, int(tree), total_kv, num_splits)
+            found = lib.dap_span_splits(sms, self.num_tiles, self.total_q, self.B, self.Hq, self.Hkv, self.D,
+                                        self.tokens_per_tile, max_kv_len, window, sinks, int(tree), total_kv, num_splits)
             _need(found > 0, "bounds and num_splits must be >= 0")
         self._last = asked, rounded, found
         return found

@@ -689,19 +689,48 @@ dap_status decode_attn_paged_shared(const void *q, long long q_stride_b, long lo
     return merged ? DAP_OK : launch_shared_combine(a, cs);
 }
 
-int dap_span_tokens_per_tile(int Hq, int Hkv, int D, int max_q_len) {
-    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !supported_group(Hq / Hkv) || max_q_len < 0) return 0;
-    return span_tokens_per_tile(Hq / Hkv, D, max_q_len);
+int dap_span_tokens_per_tile(int sm_count, int B, int Hq, int Hkv, int D, int max_q_len) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !supported_group(Hq / Hkv) || max_q_len < 0) return 0;
+    return span_tokens_per_tile(std::max(1, sm_count), B, Hkv, Hq / Hkv, D, max_q_len);
 }
 
-int dap_span_splits(int sm_count, int num_tiles, int Hq, int Hkv, int D, int tokens_per_tile, int max_kv_len, int window,
-                    int sinks, int tree, long long total_kv, int num_splits) {
-    if (num_tiles < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || tokens_per_tile < 1 || max_kv_len < 0 ||
-        window < 0 || sinks < 0 || num_splits < 0 || total_kv < 0)
+int dap_span_splits(int sm_count, int num_tiles, int total_q, int B, int Hq, int Hkv, int D, int tokens_per_tile,
+                    int max_kv_len, int window, int sinks, int tree, long long total_kv, int num_splits) {
+    if (num_tiles < 0 || total_q < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || tokens_per_tile < 1 ||
+        max_kv_len < 0 || window < 0 || sinks < 0 || num_splits < 0 || total_kv < 0)
         return 0;
     const int most = span_keys(max_kv_len, window, sinks, tree ? kTreeMost : tokens_per_tile);
-    if (total_kv > 0) total_kv = std::min(total_kv, (long long)num_tiles * most);
-    return dap_resolve_splits(num_splits, sm_count, num_tiles, Hq, Hkv, D, 1, most, total_kv);
+    if (num_splits == 0 && num_tiles > 0 && most > 0) {
+        // The count with the least time by this model, in microseconds, fitted to sweeps over 110 batches (1.6% above the
+        // best count in the mean, 25% at most): a CTA starts and ends in `fixed` and takes `tile` a K/V tile; with more CTAs
+        // than fit at once they follow one another, and the longest is late at the end; K/V at 6.6 MB/us; merging costs a
+        // launch, a trip to memory a few splits, and the partial rows' way.
+        const int sms = std::max(1, sm_count), cols = tokens_per_tile * (Hq / Hkv);
+        const bool warp = cols <= 16, wide = cols == 256;
+        const double fixed = warp ? 4.0 : wide ? 10.1 : 7.7;
+        const double tile = warp ? (D == 256 ? 1.08 : D == 128 ? 0.54 : 0.43) : wide ? 0.79 : 0.76;
+        const double keys = warp ? 32. : 64.;
+        const long long slots = (long long)sms * (warp ? (D == 256 ? 2 : 4) : wide || D == 256 ? 1 : 2);
+        const double avg = total_kv > 0 ? std::min<double>(most, std::max(1., (double)total_kv / std::max(1, B))) : most;
+        const long long units = (long long)num_tiles * Hkv;
+        double best = 1e300;
+        const int limit = (int)std::min<long long>(128, ceil_div_ll(most, kTileTokens));
+        for (int S = 1; S <= limit; ++S) {
+            const double chunk = dap_chunk_tokens(most, S);
+            const double eff = std::max(1., std::min<double>(S, ceil(avg / chunk)));
+            const double longest = fixed + tile * std::min<double>(most, chunk) / keys;
+            const double mean = fixed + tile * std::min(avg / eff, chunk) / keys;
+            const double waves = (double)units * eff / (double)slots;
+            double us = std::max(longest, mean * waves + (waves > 1. ? 0.84 * longest : 0.));
+            if (cols != 128) us = std::max(us, fixed + (double)units * avg * D * 4e-6 / 6.6);
+            if (S > 1) us += 2.3 + 0.1 * eff + (double)total_q * Hq * eff * D * 8e-6 / 7.8;
+            if (us < best) {
+                best = us;
+                num_splits = S;
+            }
+        }
+    }
+    return dap_resolve_splits(std::max(1, num_splits), sm_count, num_tiles, Hq, Hkv, D, 1, most, 0);
 }
 
 static dap_status span_call(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
@@ -728,16 +757,16 @@ static dap_status span_call(const void *q, long long q_stride_t, long long q_str
         !aligned4(tile_batch) || !aligned4(tile_index) || !aligned4(parents))
         return DAP_ERR_ALIGN;
     const int G = Hq / Hkv;
-    const bool known = tokens_per_tile == 8 / G || tokens_per_tile == 16 / G ||
-                       tokens_per_tile == span_tokens_per_tile(G, D, 0x7FFFFFFF);
-    if (!known || (!mapped && (total_q != B || num_tiles != B || tokens_per_tile != 8 / G))) return DAP_ERR_SHAPE;
+    const int cols = tokens_per_tile * G;
+    const bool known = cols == 8 || cols == 16 || (D >= 64 && cols == 128) || ((D == 64 || D == 128) && cols == 256);
+    if (!known || (!mapped && (total_q != B || num_tiles != B || cols != 8))) return DAP_ERR_SHAPE;
     if (window >= max_kv_len) window = 0;  // (no token is further from a key)
     if (window == 0) sinks = 0;
     sinks = std::min(sinks, max_kv_len);
     int sms = 0;
     if (num_splits == 0 && (sms = dap_device_sm_count()) <= 0) return DAP_ERR_CUDA;
-    const int S = dap_span_splits(sms, num_tiles, Hq, Hkv, D, tokens_per_tile, max_kv_len, window, sinks, tree, 0,
-                                  num_splits);
+    const int S = dap_span_splits(sms, num_tiles, total_q, B, Hq, Hkv, D, tokens_per_tile, max_kv_len, window, sinks, tree,
+                                  0, num_splits);
     if (S == 0) return DAP_ERR_SHAPE;
     if (S > 1 && (!workspace || workspace_bytes < dap_workspace_bytes_multi(total_q, Hq, D, S) || !aligned16(workspace)))
         return DAP_ERR_WORKSPACE;

@@ -192,7 +192,7 @@ struct SpanArgs {
     int window, sinks;       // window 0: none
 };
 constexpr int kTreeMost = 256;  // nodes of one tree
-int span_tokens_per_tile(int G, int D, int max_q_len);
+int span_tokens_per_tile(int sms, int B, int Hkv, int G, int D, int max_q_len);
 dap_status launch_span(const SpanArgs &a, cudaStream_t stream);
 dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream);
 dap_status launch_span_tc(const SpanArgs &a, cudaStream_t stream);

@@ -10,9 +10,9 @@
 //   out_i = sum_t softmax_t(scale q_i . K_t) V_t.
 // A tile of new tokens (the packed-q work map of the multi-token decode) therefore reads the places [0, s) and
 // [lo, end), where lo is the first that its first token's window has and end lies behind its last token.  The two spans are
-// laid behind each other, cut at multiples of 64 keys, so that a K/V tile has keys of one of them: tile places v below s64 =
-// s rounded up to 64 are places t = v, those above are t = v + gap.  Splits and chunks are cut in v.  The K/V rows between
-// s and lo that the rounding leaves in are read from a page that is seen anyway and enter the products with weight zero and
+// laid behind each other, cut at multiples of a K/V tile, so that a K/V tile has keys of one of them: tile places v below
+// s rounded up to tiles are places t = v, those above are t = v + gap.  Splits and chunks are cut in v.  Of the rows between
+// s and lo that the rounding leaves in, those of whole copies are not copied, and all enter the products with weight zero and
 // V = 0: pages that no token sees are never looked at.
 #pragma once
 
@@ -24,6 +24,7 @@ struct SpanParams {
     SplitParams sp;
     const int32_t *parents;
     int window, sinks;
+    int gran;  // keys of a K/V tile
 };
 
 constexpr int kTreeWords = kTreeMost / 32;
@@ -31,9 +32,9 @@ constexpr int kTreeWords = kTreeMost / 32;
 struct SpanTile : MultiTile {
     int ctx;        // places in front of the sequence's new tokens
     int lo;         // first place that the window of the tile's first token has (0: no window)
-    int s64, gap;   // v -> t
+    int sink_end, gap;  // v -> t
     int len;        // of the spans, in v
-    __device__ __forceinline__ int place(int v) const { return v < s64 ? v : v + gap; }
+    __device__ __forceinline__ int place(int v) const { return v < sink_end ? v : v + gap; }
 };
 
 __device__ __forceinline__ bool span_tile(const SpanParams &pp, int b, int tindex, int q0, int q1, int L, int qt,
@@ -45,8 +46,8 @@ __device__ __forceinline__ bool span_tile(const SpanParams &pp, int b, int tinde
     }
     t->ctx = t->pos0 - t->i0;
     t->lo = pp.window > 0 ? max(0, (pp.parents ? t->ctx : t->pos0) - pp.window + 1) : 0;
-    t->s64 = (pp.sinks + 63) & ~63;
-    t->gap = max(0, (t->lo & ~63) - t->s64);
+    t->sink_end = (pp.sinks + pp.gran - 1) & -pp.gran;
+    t->gap = max(0, (t->lo & -pp.gran) - t->sink_end);
     t->len = t->kv_end - t->gap;
     return true;
 }
@@ -300,12 +301,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
     if (warp == NWC) {
         const int32_t *table = p.block_table + (long long)tl.b * p.max_pages;
-        // The page of the `rows` places from t on, or, where none of them is seen, of the window's first: raw, it is
-        // looked at a tile later.
-        auto entry = [&](int t, int rows) -> int {
-            const int seen = t >= pp.sinks && t + rows <= tl.lo ? tl.lo : t;
-            return __ldg(table + seen / p.page_size);
-        };
+        // places t .. t + rows - 1 lie between the spans: no token of the tile sees them
+        auto hidden = [&](int t, int rows) { return t >= pp.sinks && t + rows <= tl.lo; };
         int issued = 0;
         if constexpr (C::GATHER) {  // ---- producer warp, row gather
             RowPages<C> next;
@@ -313,8 +310,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 const int v = v0 + i * BT + lane, t = tl.place(v0 + i * BT) + lane;
                 next.pg[0] = 0;
                 next.slot[0] = 0;
-                if (i < ntiles && v < v1) {
-                    next.pg[0] = entry(t, 1);
+                if (i < ntiles && v < v1) {  // (a hidden row: some row of a page that is seen)
+                    next.pg[0] = __ldg(table + (hidden(t, 1) ? tl.lo : t) / p.page_size);
                     next.slot[0] = t % p.page_size;
                 }
             };
@@ -333,30 +330,33 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 issued = i + 1;
             }
         } else {  // ---- producer warp: page lookup + TMA issue
-            auto lookup = [&](int i) -> int {
-                const int v = v0 + i * BT + lane * R;
-                return i < ntiles && lane * R < BT && v < v1 ? entry(tl.place(v0 + i * BT) + lane * R, R) : 0;
+            // the page of the lane's box, raw (it is looked at a tile later), and whether it has one
+            auto lookup = [&](int i, bool *box) -> int {
+                const int v = v0 + i * BT + lane * R, t = tl.place(v0 + i * BT) + lane * R;
+                *box = i < ntiles && lane * R < BT && v < v1 && !hidden(t, R);
+                return *box ? __ldg(table + t / p.page_size) : 0;
             };
-            int next = lookup(0);
+            bool has, has_next;
+            int next = lookup(0, &has_next);
             for (int i = 0; i < ntiles; ++i) {
                 const int st = i % NS;
                 int pg = next;
-                next = lookup(i + 1);
+                has = has_next;
+                next = lookup(i + 1, &has_next);
                 if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((i / NS) - 1) & 1))) {
                     misc[1] = 1;
                     break;
                 }
-                const int v = v0 + i * BT;
-                const int nbox = (min(BT, v1 - v) + R - 1) / R;
+                const int nbox = __popc(__ballot_sync(0xFFFFFFFFu, has));
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB * 2));
                 __syncwarp();
-                if (lane < nbox) {
+                if (has) {
                     if (pg < 0 || pg >= p.num_pages) {
                         flag_error(DAP_DEVERR_PAGE);
                         pg = 0;
                     }
                     issue_kv_box<C>(smem + st * C::STAGE_BYTES, lane, R, &mapK, &mapV, kvh,
-                                    (tl.place(v) + lane * R) % p.page_size, pg, &full[st]);
+                                    (tl.place(v0 + i * BT) + lane * R) % p.page_size, pg, &full[st]);
                 }
                 issued = i + 1;
             }
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 }
 
 // Merge of the split partials of every (token, head) row whose tile took more than one split, as combine_multi_kernel: a
-// warp per (token, HPW consecutive heads).
-template <int D, int HPW>
+// warp per (token, HPW consecutive heads), SB splits per batch of loads, in split order.
+template <int D, int HPW, int SB>
 __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams pp, int qt) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -460,23 +460,35 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams pp, 
 #pragma unroll
         for (int j = 0; j < DPV; ++j) acc[h][j] = 0.f;
     }
-    for (int s = 0; s < nsplit; ++s) {
-        float x[HPW][DPV];
-        float2 ml[HPW];
+    for (int s0 = 0; s0 < nsplit; s0 += SB) {
+        float x[HPW][SB][DPV];
+        float2 ml[HPW][SB];
+#pragma unroll
+        for (int h = 0; h < HPW; ++h)
+#pragma unroll
+            for (int k = 0; k < SB; ++k) {
+                const long long row = rbase + (long long)min(s0 + k, nsplit - 1) * p.Hq + h;
+                load_row_part<DPV>(p.o_part + row * D + lane * DPV, x[h][k]);
+                ml[h][k] = *reinterpret_cast<const float2 *>(p.ml_part + row * 2);
+            }
 #pragma unroll
         for (int h = 0; h < HPW; ++h) {
-            const long long row = rbase + (long long)s * p.Hq + h;
-            load_row_part<DPV>(p.o_part + row * D + lane * DPV, x[h]);
-            ml[h] = *reinterpret_cast<const float2 *>(p.ml_part + row * 2);
-        }
+            float m = M[h];
 #pragma unroll
-        for (int h = 0; h < HPW; ++h) {
-            const float m = fmaxf(M[h], ml[h].x), mu = m == -INFINITY ? 0.f : m;
-            const float old = ex2(M[h] - mu), f = ex2(ml[h].x - mu);
-            lsum[h] = fmaf(f, ml[h].y, lsum[h] * old);
-#pragma unroll
-            for (int j = 0; j < DPV; ++j) acc[h][j] = fmaf(f, x[h][j], acc[h][j] * old);
+            for (int k = 0; k < SB; ++k) m = fmaxf(m, ml[h][k].x);  // (the last one may come more than once here)
+            const float mu = m == -INFINITY ? 0.f : m, old = ex2(M[h] - mu);
             M[h] = m;
+            lsum[h] *= old;
+#pragma unroll
+            for (int j = 0; j < DPV; ++j) acc[h][j] *= old;
+#pragma unroll
+            for (int k = 0; k < SB; ++k)
+                if (s0 + k < nsplit) {
+                    const float f = ex2(ml[h][k].x - mu);
+                    lsum[h] = fmaf(f, ml[h][k].y, lsum[h]);
+#pragma unroll
+                    for (int j = 0; j < DPV; ++j) acc[h][j] = fmaf(f, x[h][k][j], acc[h][j]);
+                }
         }
     }
 #pragma unroll
@@ -486,8 +498,9 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams pp, 
 
 namespace {
 
-SpanParams span_params(const SpanArgs &a, int box_rows) {
+SpanParams span_params(const SpanArgs &a, int box_rows, int gran) {
     SpanParams p = {};
+    p.gran = gran;
     p.sp = make_params(a.d);
     p.sp.box_rows = box_rows;
     p.sp.o_part = static_cast<float *>(a.d.workspace);
@@ -504,13 +517,15 @@ SpanParams span_params(const SpanArgs &a, int box_rows) {
 template <int D>
 dap_status launch_span_combine(const SpanArgs &a, const SpanParams &p, int qt, cudaStream_t stream) {
     if (a.d.num_splits <= 1) return DAP_OK;
-    const int hpw = a.d.Hq % 4 == 0 ? 4 : a.d.Hq % 2 == 0 ? 2 : 1;
-    const long long ctas = ((long long)a.d.total_q * (a.d.Hq / hpw) + 7) / 8;
+    // Few rows: a warp a row, eight splits a trip to memory, since latency is all there is (one sequence of 8192 keys in 15
+    // splits: 17.9 us in all for 26.0); many: four heads a warp, whose sequence is found once.
+    const long long rows = (long long)a.d.total_q * a.d.Hq;
+    const bool few = rows <= 8192 || a.d.Hq % 4 != 0;
+    const long long ctas = ((few ? rows : rows / 4) + 7) / 8;
     if (ctas > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
     const dim3 grid((unsigned)ctas);
-    const cudaError_t e = hpw == 4   ? launch_dependent(span_combine_kernel<D, 4>, grid, dim3(256), stream, p, qt)
-                          : hpw == 2 ? launch_dependent(span_combine_kernel<D, 2>, grid, dim3(256), stream, p, qt)
-                                     : launch_dependent(span_combine_kernel<D, 1>, grid, dim3(256), stream, p, qt);
+    const cudaError_t e = few ? launch_dependent(span_combine_kernel<D, 1, 8>, grid, dim3(256), stream, p, qt)
+                              : launch_dependent(span_combine_kernel<D, 4, 1>, grid, dim3(256), stream, p, qt);
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
@@ -527,7 +542,7 @@ dap_status launch_span_warp(const SpanArgs &a, cudaStream_t stream) {
     if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
     const long long grid = (long long)a.d.num_tiles * a.d.Hkv * a.d.num_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
-    const SpanParams p = span_params(a, R);
+    const SpanParams p = span_params(a, R, C::BT);
     if (launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mk, mv, p) != cudaSuccess)
         return DAP_ERR_CUDA;
     return launch_span_combine<D>(a, p, C::QT, stream);

@@ -1,16 +1,29 @@
 // dap_span_tc.cu -- attention over spans of the paged cache (dap_span.cuh has the operation) for many query rows, on the
 // tcgen05 tensor cores: verification of larger trees, chunks of prompts behind a window.
 //
-// One CTA takes a work tile of up to 256 query rows of one kv head (row r: new token r / G of the tile, head r % G), or 128
-// at D = 256, against one chunk of the tile's spans, in two streams of 128 rows (one at D = 256), as the prefix kernel of
-// the shared-prefix decode does (dap_shared_prefix.cu; the ring, the two score buffers a stream, who issues what and why
-// are described there): with more than 128 rows each stream has its own and both take every K/V tile of 64 keys, else both
-// hold the same rows and take every other tile, merged through shared memory at the end.  What differs:
-//   * the tiles walk two spans (the sinks, the window), and a tile has to be masked by row where an end of a window, the
-//     new tokens or a tree's nodes lie in it.  A row's mask of the 64 keys is one 64-bit word, made of its bounds and its
-//     line of ancestors; tiles that every row of a warp sees whole, nearly all, skip it;
-//   * V rows that no row of the tile sees are zeroed by the softmax threads, before they hand over the tile's weights;
-//   * with one split the rows leave as bf16 outputs, whole rows a store, and no combine follows.
+// One CTA takes a work tile of query rows of one kv head (row r: new token r / G of the tile, head r % G) against one chunk of
+// the tile's spans, in streams of 128 rows: one stream, in which case two CTAs share an SM (one at D = 256), or two (WIDE),
+// which share every K/V tile (span_tokens_per_tile has the rule).
+//   shared memory: q (128-byte swizzled, one TMA copy per 64 dims of 128 rows), a ring of K/V tiles of 64 keys.  K tiles are
+//                  column block major, [D / 64][64 keys][128 bytes], a copy per page run and column block; V tiles one box per
+//                  page run, [D / 64][R keys][128 bytes], since a product takes 16 keys of V at a time (row gather: both
+//                  column block major);
+//   tensor memory (lane = row): S  columns [128 x + 64 e, + 64) of stream x: fp32 scores of tile n in buffer e = n & 1; P (bf16
+//                  pairs) overwrites the first 32 once they are read;  O  columns [TO + x D, + D): fp32 accumulator.
+// Warps: four softmax warps a stream (thread = row), a producer each for K and V, one a stream that issues its scores, one
+// that issues the products with V.  S(n + 2) needs only PV(n), whose P it replaces.
+//   * Spans: a tile has to be masked by row where an end of a window, the new tokens or a tree's nodes lie in it.  A row's
+//     mask of the 64 keys is one 64-bit word, made of its bounds and its line of ancestors; tiles that every row of a warp
+//     sees whole, nearly all, skip it.
+//   * V rows that no row of the tile sees are zeroed by the softmax threads, before they hand over the tile's weights.
+//   * With one split the rows leave as bf16 outputs, whole rows a store, and no combine follows.
+// Bound, at many rows: the chain of a tile, 1750 cycles for 256 rows x 64 keys (D = 128), of which the products take 1330 - 1580
+// (24 of them, 50 to 66 cycles each whatever their size) and a softmax warp 930 - 1070; a CTA's start and end, 15,000 cycles,
+// most of it waits for memory, are what a second CTA on the SM covers.  Measured and not kept: score products of 128 keys with
+// one buffer a stream (1.28 us a 64-key tile of 256 rows for 0.91: the chain S, softmax, PV is then in line), weights taken
+// against the old reference while the maximum is found (0.96 - 1.0), one producer warp for K and V (0.96).
+// Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only when a tile's maximum
+// passes the reference by more than 2^8), so the weights stay <= 256.  They are rounded to bf16 for the product with V.
 #include <algorithm>
 
 #include "dap_span.cuh"
@@ -20,17 +33,18 @@ namespace dap {
 
 namespace {
 
-template <int D_, bool GATHER_>
+// WIDE: 256 rows in two streams, one CTA an SM; else 128 rows in one stream, two CTAs an SM (D = 256: one).
+template <int D_, bool WIDE_, bool GATHER_>
 struct SpanTcCfg {
-    static constexpr bool GATHER = GATHER_, SWZ = true;
+    static constexpr bool GATHER = GATHER_, WIDE = WIDE_, SWZ = true;
     static constexpr int D = D_, BT = 64;
     static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
     static constexpr int TILE_BYTES = BT * ROWB;  // K or V of one tile
-    static constexpr int NSTREAM = D == 256 ? 1 : 2, ROWS = 128 * NSTREAM;
-    static constexpr int NS = D == 64 ? 6 : D == 128 ? 4 : 2;  // K/V tiles in the ring
+    static constexpr int NSTREAM = WIDE ? 2 : 1, ROWS = 128 * NSTREAM, MINB = WIDE || D == 256 ? 1 : 2;
+    static constexpr int NS = (WIDE ? D == 64 ? 6 : 4 : D == 64 ? 4 : 2);  // K/V tiles in the ring
     static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 2, PV = ISSUER + NSTREAM,
                          THREADS = (PV + 1) * 32;
-    static constexpr int TO = 256, TMEM_COLS = 512;
+    static constexpr int TO = MINB == 1 ? 256 : 128, TMEM_COLS = MINB == 1 ? 512 : 256;
     static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
     static constexpr int RING_OFF = Q_BYTES, BAR_OFF = RING_OFF + NS * 2 * TILE_BYTES;
     // barriers: k_full, k_empty, v_full, v_empty [NS], s_done, p_ready, pv_done [stream][buffer], q_full, fin[3]
@@ -39,47 +53,53 @@ struct SpanTcCfg {
     // a tree's parents, lines and depths (G = 1: as many tokens as rows)
     static constexpr int TREE_OFF = MISC_OFF + 32, LINE_OFF = TREE_OFF + kTreeMost * 4;
     static constexpr int SMEM = LINE_OFF + ROWS * (kTreeWords + 1) * 4 + 1024;  // + slack to align the base
-    static constexpr int ROW_F = D + 4;  // floats of a row of sums on its way out (the 4: no bank conflicts)
-    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA an SM: a second would wait for tensor memory");
-    static_assert(ROWS * ROW_F * 4 <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
+    static constexpr int ROW_B = D * 4 + 16;  // bytes of a row of sums on its way out (the 16: no bank conflicts)
+    static_assert(!WIDE || D <= 128, "tensor memory");
+    static_assert(TO + NSTREAM * D <= TMEM_COLS && 128 * NSTREAM <= TO, "tensor memory");
+    static_assert(SMEM <= 227 * 1024 / MINB, "shared memory");
+    static_assert(MINB == 2 || SMEM > 114 * 1024, "one CTA an SM: a second would wait for tensor memory");
+    static_assert(ROWS * ROW_B <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
 };
 
-// A row's place among a warp's 32 rows of sums, ROW_F floats apart in shared memory, to global memory: `n` rows, NC of their
-// floats from `out` + the lane's `to` on, as they are or, with BF16, times the lane's `inv` and rounded.  Whole rows a
-// store, eight stores' loads ahead of the first.
-template <class C, int NC, bool BF16>
-__device__ __forceinline__ void leave(const float *rows, void *out, long long to, float inv, int n, int lane) {
-    constexpr int PER = BF16 ? 8 : 4, W = NC / PER < 32 ? NC : 32 * PER, LPR = W / PER, RPI = 32 / LPR, U = 4;
-    static_assert(NC % W == 0 && 32 % (RPI * U) == 0, "whole batches");
-    __syncwarp();
+// 32 columns of a row's sums in shared memory, as fp32 or, with BF16, times `f` and rounded (rows are ROW_B bytes apart).
+template <bool BF16>
+__device__ __forceinline__ void put32(uint8_t *row, int c, const float (&o)[32], float f) {
+    if constexpr (BF16) {
 #pragma unroll
-    for (int c0 = 0; c0 < NC; c0 += W) {
-        const int c = c0 + lane % LPR * PER;
+        for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4 *>(row + (c + k) * 2) =
+                make_uint4(pack_bf16x2(o[k] * f, o[k + 1] * f), pack_bf16x2(o[k + 2] * f, o[k + 3] * f),
+                           pack_bf16x2(o[k + 4] * f, o[k + 5] * f), pack_bf16x2(o[k + 6] * f, o[k + 7] * f));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4 *>(row + (c + k) * 4) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    }
+}
+
+// `n` rows that a warp has in shared memory to global memory, BYTES of each: row i of the tile's rows first, first + 1, ..
+// is (token i / G, head i % G) and goes to out + token * st + head * sh.  Whole rows a store, eight loads ahead.
+template <int BYTES, int ROW_B>
+__device__ __forceinline__ void leave(const uint8_t *rows, uint8_t *out, int first, int n, int G, long long st, long long sh,
+                                      int lane) {
+    constexpr int W = BYTES < 512 ? BYTES : 512, LPR = W / 16, RPI = 32 / LPR, U = 32 / RPI < 8 ? 32 / RPI : 8;
+    static_assert(BYTES % W == 0, "whole rows");
+    __syncwarp();
+    const int sub = lane / LPR, gs = 31 - __clz(G);
+#pragma unroll
+    for (int c0 = 0; c0 < BYTES; c0 += W) {
+        const int c = c0 + lane % LPR * 16;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += RPI * U) {
             uint4 v[U];
-            long long at[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4 *>(rows + (i0 + u * RPI + sub) * ROW_B + c);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * RPI + lane / LPR;
-                at[u] = __shfl_sync(0xFFFFFFFFu, to, i & 31);
-                const float f = BF16 ? __shfl_sync(0xFFFFFFFFu, inv, i & 31) : 1.f;
-                const float4 x = *reinterpret_cast<const float4 *>(rows + i * C::ROW_F + c);
-                if constexpr (BF16) {
-                    const float4 y = *reinterpret_cast<const float4 *>(rows + i * C::ROW_F + c + 4);
-                    v[u] = make_uint4(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f),
-                                      pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-                } else {
-                    v[u] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
-                                      __float_as_uint(x.w));
-                }
+                const int i = i0 + u * RPI + sub;
+                if (i < n)
+                    *reinterpret_cast<uint4 *>(out + ((first + i) >> gs) * st + ((first + i) & (G - 1)) * sh + c) = v[u];
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * RPI + lane / LPR < n) {
-                    if constexpr (BF16) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at[u] + c) = v[u];
-                    else *reinterpret_cast<uint4 *>(static_cast<float *>(out) + at[u] + c) = v[u];
-                }
         }
     }
 }
@@ -96,9 +116,10 @@ __device__ __forceinline__ uint64_t line_bits(const uint32_t *line, int o) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
+__global__ void __launch_bounds__(C::THREADS, C::MINB)
     span_tc_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                   const __grid_constant__ CUtensorMap mapV, const SpanParams pp, const int G) {
+                   const __grid_constant__ CUtensorMap mapV, const SpanParams pp, const int G,
+                   const bool longest_first) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = aligned_smem<C>(smem_raw);
     constexpr int BT = C::BT, NS = C::NS, D = C::D;
@@ -108,7 +129,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
     uint64_t *s_done = v_empty + NS, *p_ready = s_done + 4, *pv_done = p_ready + 4;  // [2 stream + buffer]
     uint64_t *q_full = pv_done + 4, *fin = q_full + 1;
-    // [0], [1] K and V tiles issued, [2] abort, [4] tensor memory
+    // [0], [1] K and V tiles issued, [2] abort, [3] the work tile, [4] tensor memory
     volatile int *misc = reinterpret_cast<volatile int *>(smem + C::MISC_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF) + 4;
     uint8_t *ring = smem + C::RING_OFF;
@@ -116,8 +137,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int units = p.num_tiles * p.Hkv;
     const int s = (int)(blockIdx.x / units);
     const int rem = (int)(blockIdx.x - s * units);
-    const int w = rem / p.Hkv;
-    const int kvh = rem - w * p.Hkv;
+    const int slot = rem / p.Hkv;
+    const int kvh = rem - slot * p.Hkv;
 
     // Tensor memory touches nothing the previous kernel writes: it is allocated before the wait.
     if (warp == 0) {
@@ -138,41 +159,55 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int wb = p.tile_batch[w], wi = p.tile_index[w];
-    const int bb = (wb >= 0 && wb < p.B) ? wb : 0;
     const int qt = C::ROWS / G;
-    SpanTile tl;
     const bool first = s == 0 && kvh == 0;
-    const bool live = span_tile(pp, wb, wi, p.qo_indptr[bb], p.qo_indptr[bb + 1], p.seq_lens[bb], qt,
-                                threadIdx.x == 0 && first, &tl);
+    auto tile_of = [&](int i, bool report, SpanTile *t) -> bool {
+        const int wb = p.tile_batch[i], bb = (wb >= 0 && wb < p.B) ? wb : 0;
+        return span_tile(pp, wb, p.tile_index[i], p.qo_indptr[bb], p.qo_indptr[bb + 1], p.seq_lens[bb], qt, report, t);
+    };
+    int w = slot;
+    if (longest_first) {
+        // CTAs start in the order of their numbers, so the slot-th longest tile goes to this one: every CTA ranks all tiles.
+        int *len = reinterpret_cast<int *>(ring);
+        SpanTile t;
+        for (int i = threadIdx.x; i < p.num_tiles; i += C::THREADS) len[i] = tile_of(i, false, &t) ? t.len : -1;
+        __syncthreads();
+        for (int i = warp; i < p.num_tiles; i += C::THREADS / 32) {
+            const int mine = len[i];
+            int rank = 0;
+            for (int k = lane; k - lane < p.num_tiles; k += 32)
+                rank += __popc(__ballot_sync(0xFFFFFFFFu, k < p.num_tiles && (len[k] > mine || (len[k] == mine && k < i))));
+            if (rank == slot && lane == 0) misc[3] = i;
+        }
+        fence_async_smem();  // (the ring's copies come after these reads and writes)
+        __syncthreads();
+        w = misc[3];
+    }
+    SpanTile tl;
+    const bool live = tile_of(w, threadIdx.x == 0 && first, &tl);
     const int nsplit = live ? span_splits(tl, p.chunk) : 0;
     const int nrows = s < nsplit ? tl.ntok * G : 0;
     const int v0 = s * p.chunk, v1 = s < nsplit ? min(tl.len, v0 + p.chunk) : v0;
     const int J = max(0, v1 - v0 + BT - 1) / BT;  // K/V tiles of this CTA
     const bool work = nrows > 0 && J > 0;
-    const bool both = C::NSTREAM == 2 && nrows > 128;  // the streams have rows of their own
-    // K/V tiles of stream x: all of them, or tiles x, x + 2, ...
-    auto tiles_of = [&](int x) { return both || C::NSTREAM == 1 ? J : (J - x + 1) / 2; };
-    auto tile_at = [&](int x, int n) { return both || C::NSTREAM == 1 ? n : 2 * n + x; };
-    auto rows_of = [&](int x) { return both ? min(128, nrows - 128 * x) : nrows; };
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&k_full[i], full_arrivals<C>());
-            mbar_init(&v_full[i], full_arrivals<C>());
-            // a commit of every stream that takes the K tile, one after the last product that reads the V tile
-            mbar_init(&k_empty[i], both ? 2 : 1);
-            mbar_init(&v_empty[i], 1);
-        }
-        for (int e = 0; e < 4; ++e) {
-            mbar_init(&s_done[e], 1);
-            mbar_init(&p_ready[e], (uint32_t)max(1, (rows_of(e >> 1) + 31) / 32));  // one per warp with rows
-            mbar_init(&pv_done[e], 1);
-        }
-        mbar_init(q_full, 1);
-        for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
-        misc[0] = misc[1] = misc[2] = 0;
+    const int streams = C::WIDE && nrows > 128 ? 2 : 1;  // that have rows
+    auto rows_of = [&](int x) { return max(0, min(128, nrows - 128 * x)); };
+    if (threadIdx.x < C::NBAR) {  // a thread a barrier
+        const int i = threadIdx.x, e = i - 4 * NS;
+        uint32_t n = 1;  // s_done, pv_done, fin: a commit; q_full: bytes
+        if (i < NS || (i >= 2 * NS && i < 3 * NS)) n = full_arrivals<C>();  // k_full, v_full
+        else if (i < 2 * NS) n = streams;  // k_empty: a commit of every stream's scores (v_empty: one, the last product's)
+        else if (e >= 4 && e < 8) n = (uint32_t)max(1, (rows_of((e - 4) >> 1) + 31) / 32);  // p_ready: the warps with rows
+        mbar_init(k_full + i, n);
         fence_barrier_init();
     }
+    if (threadIdx.x < 3) misc[threadIdx.x] = 0;
+    // The producers ask for their first page ids meanwhile (32 entries of the first span each, and of the window).
+    const int32_t *table = p.block_table + (long long)(work ? tl.b : 0) * p.max_pages;
+    const bool jumps = work && tl.gap > 0 && v0 < tl.sink_end && tl.sink_end < v1;
+    const int e_first = work ? tl.place(v0) / p.page_size : 0, e_jump = jumps ? tl.place(tl.sink_end) / p.page_size : e_first;
+    const bool asks = !C::GATHER && work && (warp == C::PRODUCER || warp == C::PRODUCER + 1);
+    PageWindow pages(table, e_first, asks ? p.max_pages : 0, lane), beyond(table, e_jump, asks && jumps ? p.max_pages : 0, lane);
     tc_fence_before();
     __syncthreads();  // barriers and the tensor-memory address are visible
     tc_fence_after();
@@ -184,16 +219,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (work && (warp == C::PRODUCER || warp == C::PRODUCER + 1)) {
         // ---- a producer warp each for K and V
         const int tensor = warp - C::PRODUCER;
-        const int32_t *table = p.block_table + (long long)tl.b * p.max_pages;
         const int R = p.box_rows;
         uint64_t *full = tensor ? v_full : k_full, *empty = tensor ? v_empty : k_empty;
         uint8_t *place = ring + tensor * C::TILE_BYTES;
         int done = 0;  // tiles issued
         auto load_q = [&] {  // 64 dims of 128 rows a copy (rows past the tile's tokens are never read)
-            if (tensor == 0 && lane == 0) {
-                const int parts = both ? 2 : 1;
-                mbar_arrive_expect_tx(q_full, (uint32_t)(parts * C::NBLK * C::QBLK));
-                for (int x = 0; x < parts; ++x)
+            if (tensor == 1 && lane == 0) {
+                mbar_arrive_expect_tx(q_full, (uint32_t)(streams * C::NBLK * C::QBLK));
+                for (int x = 0; x < streams; ++x)
                     for (int cb = 0; cb < C::NBLK; ++cb)
                         tma_load_3d(smem + (x * C::NBLK + cb) * C::QBLK, &mapQ, cb * 64, kvh * G,
                                     tl.q0 + tl.i0 + x * (128 / G), q_full);
@@ -250,25 +283,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             };
             start(tl.place(v0));
-            PageWindow pages(table, e0, p.max_pages, lane);
-            // (the window's first entries are asked for before the sinks' tiles)
-            const bool jumps = tl.gap > 0 && v0 < tl.s64 && tl.s64 < v1;
-            PageWindow beyond(table, jumps ? tl.place(tl.s64) / p.page_size : e0, p.max_pages, lane);
-            const int shown = __ldg(table + tl.lo / p.page_size);
             load_q();
             for (; done < J; ++done) {
                 const int st = done % NS, v = v0 + done * BT, t = tl.place(v);
-                if (jumps && v == tl.s64) {
+                if (jumps && v == tl.sink_end) {
                     start(t);
                     pages = beyond;
                 }
                 const int nbox = (min(BT, v1 - v) + R - 1) / R;
                 int pg = pages.at(e, e0);
-                if (hidden(t + j * R, R)) pg = shown;
+                const bool has = j < nbox && !hidden(t + j * R, R);
+                const int copied = __popc(__ballot_sync(0xFFFFFFFFu, has)) / kb;
                 if (done >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], ((done / NS) - 1) & 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nbox * R * C::ROWB));
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(copied * R * C::ROWB));
                 __syncwarp();
-                if (j < nbox) {
+                if (has) {
                     if (pg < 0 || pg >= p.num_pages) {
                         flag_error(DAP_DEVERR_PAGE);
                         pg = 0;
@@ -294,17 +323,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // registers.  Two barriers are polled at a time, each by half the lanes.
         auto same = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
         const int role = same(warp - C::ISSUER);  // a stream's scores; NSTREAM: all products with V
-        const int Ju = same(J), last = same(nlast);
-        const bool two = same(both) != 0;
+        const int Ju = same(J), last = same(nlast), live_streams = same(streams);
         const uint32_t tm = same(tmem);
-        const int step = two || C::NSTREAM == 1 ? 1 : 2;  // tile n of stream x is step * n + (step == 2 ? x : 0)
         const uint32_t sQ = smem_addr(smem), sR = smem_addr(ring);
-        // A V tile is made of boxes [column block][vR keys][128 bytes]; byte offset of key 16 i and the strides of
-        // the product's blocks of 64 dims and groups of 8 keys.
-        const int vR = same(p.box_rows);
-        const uint32_t v_lbo = vR * 128, v_sbo = vR == 8 ? 8 * C::ROWB : 1024;
-        auto v_off = [&](int i) -> uint32_t { return i * 16 / vR * vR * C::ROWB + i * 16 % vR * 128; };
-        const uint32_t a1 = v_off(1) >> 4, a2 = v_off(2) >> 4, a3 = v_off(3) >> 4;
         auto wait = [&](uint64_t *b0, int n0, uint64_t *b1, int n1) -> bool {
             const bool odd = lane & 1;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(odd ? b1 : b0, (odd ? n1 : n0) & 1)) != 0;
@@ -312,48 +333,49 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_fence_after();
             return ok;
         };
-        auto scores = [&](int x, int n) -> bool {
-            const int j = step * n + (step == 2 ? x : 0), st = j % NS, e = 2 * x + (n & 1);
-            uint64_t *k = &k_full[st];
-            if (!(n >= 2 ? wait(k, j / NS, &pv_done[e], (n - 2) >> 1) : wait(k, j / NS, q_full, 0))) return false;
-            const uint64_t dQ = sw128_desc(sQ + (two ? x * C::NBLK * C::QBLK : 0), 16, 1024);
-            const uint64_t dK = sw128_desc(sR + st * 2 * C::TILE_BYTES, 16, 1024);
-            const uint32_t tS = tm + 64 * e;
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    umma_bf16(tS, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
-                              dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
-                umma_commit(&s_done[e]);
-                umma_commit(&k_empty[st]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](int x, int n) -> bool {
-            const int j = step * n + (step == 2 ? x : 0), st = j % NS, e = 2 * x + (n & 1);
-            if (!wait(&p_ready[e], n >> 1, &v_full[st], j / NS)) return false;
-            const int nv = j == Ju - 1 ? last : BT;
-            const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, v_lbo, v_sbo);
-            const uint32_t tP = tm + 64 * e, tOx = tm + C::TO + x * D;
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < BT / 16; ++i)
-                    if (i * 16 < nv)
-                        umma_bf16_tmem_a(tOx, tP + i * 8, dV + (i == 0 ? 0u : i == 1 ? a1 : i == 2 ? a2 : a3), idO,
-                                         n > 0 || i > 0);
-                umma_commit(&pv_done[e]);
-                if (!two || x == 1) umma_commit(&v_empty[st]);  // (a commit covers all products before it)
-            }
-            __syncwarp();
-            return true;
-        };
-        const int N0 = (Ju + step - 1) / step, N1 = C::NSTREAM == 1 ? 0 : Ju / step;
         bool ok = true;
-        if (role == C::NSTREAM) {
-            for (int n = 0; ok && n < N0; ++n) ok = values(0, n) && (n >= N1 || values(1, n));
-        } else {
-            for (int n = 0; ok && n < (role == 0 ? N0 : N1); ++n) ok = scores(role, n);
+        if (role < C::NSTREAM) {  // S(n), once PV(n - 2), whose P it replaces, is done
+            const uint64_t dQ = sw128_desc(sQ + role * C::NBLK * C::QBLK, 16, 1024);
+            for (int n = 0; n < (role < live_streams ? Ju : 0); ++n) {
+                const int st = n % NS, e = 2 * role + (n & 1);
+                if (!(ok = n >= 2 ? wait(&k_full[st], n / NS, &pv_done[e], (n - 2) >> 1) : wait(&k_full[st], n / NS, q_full, 0)))
+                    break;
+                const uint64_t dK = sw128_desc(sR + st * 2 * C::TILE_BYTES, 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        umma_bf16(tm + 64 * e, dQ + (((i >> 2) * C::QBLK + (i & 3) * 32) >> 4),
+                                  dK + (((i >> 2) * CS + (i & 3) * 32) >> 4), idS, i > 0);
+                    umma_commit(&s_done[e]);
+                    umma_commit(&k_empty[st]);
+                }
+                __syncwarp();
+            }
+        } else {  // O += P(n) . V(n), stream by stream
+            // A V tile is made of boxes [column block][vR keys][128 bytes]; byte offset of key 16 i and the strides of
+            // the product's blocks of 64 dims and groups of 8 keys.
+            const int vR = same(p.box_rows);
+            const uint32_t v_lbo = vR * 128, v_sbo = vR == 8 ? 8 * C::ROWB : 1024;
+            auto v_off = [&](int i) -> uint32_t { return (i * 16 / vR * vR * C::ROWB + i * 16 % vR * 128) >> 4; };
+            const uint32_t a1 = v_off(1), a2 = v_off(2), a3 = v_off(3);
+            for (int n = 0; ok && n < Ju; ++n) {
+                const int st = n % NS, nv = n == Ju - 1 ? last : BT;
+                const uint64_t dV = sw128_desc(sR + (st * 2 + 1) * C::TILE_BYTES, v_lbo, v_sbo);
+                for (int x = 0; x < live_streams; ++x) {
+                    const int e = 2 * x + (n & 1);
+                    if (!(ok = wait(&p_ready[e], n >> 1, &v_full[st], n / NS))) break;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < BT / 16; ++i)
+                            if (i * 16 < nv)
+                                umma_bf16_tmem_a(tm + C::TO + x * D, tm + 64 * e + i * 8,
+                                                 dV + (i == 0 ? 0u : i == 1 ? a1 : i == 2 ? a2 : a3), idO, n > 0 || i > 0);
+                        umma_commit(&pv_done[e]);
+                        if (x == live_streams - 1) umma_commit(&v_empty[st]);  // (a commit covers all products before it)
+                    }
+                    __syncwarp();
+                }
+            }
         }
         if (!ok && lane == 0) misc[2] = 1;
         if (elect_one()) umma_commit(&fin[role]);  // this warp's products are done when it completes
@@ -367,12 +389,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int nx = soft ? rows_of(x) : 0;      // rows of the stream
     const bool rvalid = r < nx;
     const bool active = (warp & 3) * 32 < nx;  // this warp holds rows
-    const int row = both ? 128 * x + r : r;    // row of the tile
+    const int row = 128 * x + r;               // row of the tile
     const int tok = row / G, hq = kvh * G + row - tok * G;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + C::TO + x * D + lane_base;
     float m_ref = -INFINITY, l = 0.f;
-    const int N = soft ? tiles_of(x) : 0;
     if (soft) {
         const bool tree = pp.parents != nullptr;
         const uint32_t *lines = reinterpret_cast<const uint32_t *>(smem + C::LINE_OFF);
@@ -394,8 +415,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int seen = tree ? tl.ctx : lim + 1;  // places below it are seen as far as the window lets
         // Rows are independent through both products: a warp without rows skips the tiles, and what
         // its rows of P hold reaches only its own rows of O, which are never read.
-        for (int n = 0; n < (active ? N : 0); ++n) {
-            const int e = 2 * x + (n & 1), j = tile_at(x, n), t = tl.place(v0 + j * BT);
+        for (int n = 0; n < (active ? J : 0); ++n) {
+            const int e = 2 * x + (n & 1), t = tl.place(v0 + n * BT);
             const uint32_t tS = tmem + 64 * e + lane_base;
             const bool whole = t + BT <= seen && (t >= lo || t + BT <= pp.sinks);
             const bool masked = !__all_sync(0xFFFFFFFFu, whole || !rvalid);
@@ -482,11 +503,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
             // V rows that no row of the tile sees enter the product with weight zero, whatever they hold: those between the
             // spans, and past the end up to a multiple of 16
-            const int nv = j == J - 1 ? nlast : BT;
+            const int nv = n == J - 1 ? nlast : BT;
             const int z0 = max(0, pp.sinks - t), z1 = min(BT, tl.lo - t), end = (nv + 15) & ~15;
             if (z1 > z0 || nv < end) {
-                const int st = j % NS;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&v_full[st], (j / NS) & 1))) {
+                const int st = n % NS;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&v_full[st], (n / NS) & 1))) {
                     misc[2] = 1;
                     break;
                 }
@@ -508,74 +529,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     __syncthreads();
     if (soft) {
-        const bool done = __all_sync(0xFFFFFFFFu, mbar_wait(&fin[0], 0) && mbar_wait(&fin[1], 0) &&
-                                                         (C::NSTREAM == 1 || mbar_wait(&fin[2], 0)));
+        // (with a wait that gave up, misc[2] was set before the barrier above)
+        const bool good = misc[2] == 0 &&
+                          (!active || __all_sync(0xFFFFFFFFu, mbar_wait(&pv_done[2 * x + ((J - 1) & 1)], ((J - 1) >> 1) & 1)));
         tc_fence_after();
-        const bool good = done && misc[2] == 0;
-        // q and the ring are idle now: the sums leave through them, whole rows a store
-        float *mine = reinterpret_cast<float *>(smem) + (x * 128 + r) * C::ROW_F;
-        const float *warp_rows = mine - lane * C::ROW_F;
-        const bool direct = nsplit == 1;
-        const long long rq = tl.q0 + tl.i0 + tok;
-        const long long prow = (rq * p.num_splits + s) * p.Hq + hq;
-        const long long to = direct ? rq * p.o_sb + (long long)hq * p.o_sh : prow * D;
-        const int n = min(32, nx - (r - lane));  // rows of this warp
-        if (C::NSTREAM == 2 && !both) {
-            // Both streams hold the same rows: each adds the other's sums to its own for half of the dims (stream 0 for
-            // the first), which it gets through shared memory.
-            constexpr int H = D / 2;
-            const float *other = reinterpret_cast<float *>(smem) + ((1 - x) * 128 + r) * C::ROW_F;
-            if (active && good) {
-#pragma unroll 1
-                for (int c = (1 - x) * H, i = 0; i < H / 32; ++i, c += 32) {
-                    float o[32];
-                    if (N > 0) tmem_ld32(tO + c, o);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4 *>(mine + c + k) =
-                            N > 0 ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-                *reinterpret_cast<float2 *>(mine + D) = make_float2(m_ref, l);
-            }
-            named_sync(1, C::NWS * 32);
-            if (active && good) {
-                const float2 ml = *reinterpret_cast<const float2 *>(other + D);
-                const float m = fmaxf(m_ref, ml.x), mu = m == -INFINITY ? 0.f : m;
-                const float f0 = ex2(m_ref - mu), f1 = ex2(ml.x - mu), sum = l * f0 + ml.y * f1;
-#pragma unroll 1
-                for (int c = x * H, i = 0; i < H / 32; ++i, c += 32) {
-                    float o[32];
-                    if (N > 0) tmem_ld32(tO + c, o);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(other + c + k);
-                        *reinterpret_cast<float4 *>(mine + c + k) =
-                            N > 0 ? make_float4(o[k] * f0 + v.x * f1, o[k + 1] * f0 + v.y * f1,
-                                                o[k + 2] * f0 + v.z * f1, o[k + 3] * f0 + v.w * f1)
-                                  : make_float4(v.x * f1, v.y * f1, v.z * f1, v.w * f1);
-                    }
-                }
-                if (direct) {
-                    leave<C, H, true>(warp_rows + x * H, p.out + x * H, to, sum > 0.f ? 1.f / sum : 0.f, n, lane);
-                } else {
-                    if (rvalid && x == 0) *reinterpret_cast<float2 *>(p.ml_part + prow * 2) = make_float2(m, sum);
-                    leave<C, H, false>(warp_rows + x * H, p.o_part + x * H, to, 1.f, n, lane);
-                }
-            }
-        } else if (active && good) {
+        if (active && good) {
+            // q and the ring are idle now: the sums leave through them
+            uint8_t *mine = smem + row * C::ROW_B;
+            const uint8_t *warp_rows = mine - lane * C::ROW_B;
+            const bool direct = nsplit == 1;
+            const int n = min(32, nx - (r - lane));  // rows of this warp
+            const long long t0 = tl.q0 + tl.i0;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(tO + c, o);
-#pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<float4 *>(mine + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                if (direct) put32<true>(mine, c, o, inv);
+                else put32<false>(mine, c, o, 1.f);
             }
             if (direct) {
-                leave<C, D, true>(warp_rows, p.out, to, l > 0.f ? 1.f / l : 0.f, n, lane);
+                leave<D * 2, C::ROW_B>(warp_rows,
+                                       reinterpret_cast<uint8_t *>(p.out + t0 * p.o_sb + (long long)kvh * G * p.o_sh),
+                                       row - lane, n, G, p.o_sb * 2, p.o_sh * 2, lane);
             } else {
-                if (rvalid) *reinterpret_cast<float2 *>(p.ml_part + prow * 2) = make_float2(m_ref, l);
-                leave<C, D, false>(warp_rows, p.o_part, to, 1.f, n, lane);
+                const long long prow = (t0 * p.num_splits + s) * p.Hq + kvh * G;
+                if (rvalid)
+                    *reinterpret_cast<float2 *>(p.ml_part + (((t0 + tok) * p.num_splits + s) * p.Hq + hq) * 2) =
+                        make_float2(m_ref, l);
+                leave<D * 4, C::ROW_B>(warp_rows, reinterpret_cast<uint8_t *>(p.o_part + prow * D), row - lane, n, G,
+                                       (long long)p.num_splits * p.Hq * D * 4, D * 4, lane);
             }
         }
         if (threadIdx.x == 0 && misc[2]) {
@@ -593,6 +576,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 make_uint4(0u, 0u, 0u, 0u);
         }
     }
+    if (work && warp == 0) (void)mbar_wait(&fin[lane <= C::NSTREAM ? lane : 0], 0);  // all products are done
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -626,9 +610,9 @@ bool encode_q_rows(CUtensorMap *map, const DecodeArgs &a) {
     return encode_bf16(map, a.q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool GATHER>
+template <int D, bool WIDE, bool GATHER>
 dap_status launch_tc(const SpanArgs &a, cudaStream_t stream) {
-    using C = SpanTcCfg<D, GATHER>;
+    using C = SpanTcCfg<D, WIDE, GATHER>;
     const int R = GATHER ? C::BT : gcd_int(a.d.page_size, C::BT), G = a.d.Hq / a.d.Hkv;
     CUtensorMap mq, mk = {}, mv = {};
     if (!encode_q_rows(&mq, a.d)) return DAP_ERR_CUDA;
@@ -641,19 +625,24 @@ dap_status launch_tc(const SpanArgs &a, cudaStream_t stream) {
     if (prepare_kernel(kern, C::THREADS, C::SMEM, &occ, 100) <= 0) return DAP_ERR_CUDA;
     const long long grid = (long long)a.d.num_tiles * a.d.Hkv * a.d.num_splits;
     if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
-    const SpanParams p = span_params(a, R);
-    if (launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p, G) !=
-        cudaSuccess)
+    const SpanParams p = span_params(a, R, C::BT);
+    // More CTAs than fit at once, of unequal lengths (a window makes them about equal), and not so many that ranking them
+    // takes longer than the end of the last ones would: 64 trees of 64 nodes behind 256 .. 4096 keys, 154 us for 170.
+    const bool longest_first = a.window == 0 && grid > (long long)C::MINB * dap_device_sm_count() && a.d.num_tiles > 1 &&
+                               a.d.num_tiles <= 128;
+    if (launch_dependent_smem(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p, G,
+                              longest_first) != cudaSuccess)
         return DAP_ERR_CUDA;
     return launch_span_combine<D>(a, p, C::ROWS / G, stream);
 }
 
 template <bool GATHER>
 dap_status tc_dims(const SpanArgs &a, cudaStream_t stream) {
+    const bool wide = a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) == 256;
     switch (a.d.D) {
-        case 64: return launch_tc<64, GATHER>(a, stream);
-        case 128: return launch_tc<128, GATHER>(a, stream);
-        case 256: return launch_tc<256, GATHER>(a, stream);
+        case 64: return wide ? launch_tc<64, true, GATHER>(a, stream) : launch_tc<64, false, GATHER>(a, stream);
+        case 128: return wide ? launch_tc<128, true, GATHER>(a, stream) : launch_tc<128, false, GATHER>(a, stream);
+        case 256: return launch_tc<256, false, GATHER>(a, stream);
     }
     return DAP_ERR_UNSUPPORTED;
 }

@@ -103,17 +103,17 @@ def test_plans():
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
 def test_tiles_hold_whole_tokens(D, G):
     for n in (0, 1, 2, 8, 9, 16, 17, 100, 5000):
-        t = binding.load().dap_span_tokens_per_tile(8 * G, 8, D, n)
+        t = binding.load().dap_span_tokens_per_tile(148, 100, 8 * G, 8, D, n)
         assert t * G in ((8, 16) if D == 32 else (8, 16, 128, 256))
         assert n <= 8 // G or t > 8 // G
-    assert binding.load().dap_span_tokens_per_tile(8 * G, 8, D, -1) == 0
+    assert binding.load().dap_span_tokens_per_tile(148, 100, 8 * G, 8, D, -1) == 0
 
 
 def test_split_counts():
     lib = binding.load()
 
     def splits(tiles=16, tpt=2, most=32768, window=0, sinks=0, tree=0, total=0, S=0, sms=148):
-        return lib.dap_span_splits(sms, tiles, 32, 8, 128, tpt, most, window, sinks, tree, total, S)
+        return lib.dap_span_splits(sms, tiles, 16, 16, 32, 8, 128, tpt, most, window, sinks, tree, total, S)
     assert splits(S=1) == 1 and splits(S=5) == 5
     # what a window leaves is cut, not the length: 128 + 62 + 2 keys, sinks in a tile of their own
     assert splits(window=128, S=100) == 3 and splits(window=128, sinks=4, S=100) == 4
