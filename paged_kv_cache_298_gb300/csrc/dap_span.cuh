@@ -467,15 +467,18 @@ __global__ void __launch_bounds__(256) span_combine_kernel(const SpanParams pp, 
         for (int h = 0; h < HPW; ++h)
 #pragma unroll
             for (int k = 0; k < SB; ++k) {
-                const long long row = rbase + (long long)min(s0 + k, nsplit - 1) * p.Hq + h;
-                load_row_part<DPV>(p.o_part + row * D + lane * DPV, x[h][k]);
-                ml[h][k] = *reinterpret_cast<const float2 *>(p.ml_part + row * 2);
+                ml[h][k] = make_float2(-INFINITY, 0.f);
+                if (s0 + k < nsplit) {
+                    const long long row = rbase + (long long)(s0 + k) * p.Hq + h;
+                    load_row_part<DPV>(p.o_part + row * D + lane * DPV, x[h][k]);
+                    ml[h][k] = *reinterpret_cast<const float2 *>(p.ml_part + row * 2);
+                }
             }
 #pragma unroll
         for (int h = 0; h < HPW; ++h) {
             float m = M[h];
 #pragma unroll
-            for (int k = 0; k < SB; ++k) m = fmaxf(m, ml[h][k].x);  // (the last one may come more than once here)
+            for (int k = 0; k < SB; ++k) m = fmaxf(m, ml[h][k].x);
             const float mu = m == -INFINITY ? 0.f : m, old = ex2(M[h] - mu);
             M[h] = m;
             lsum[h] *= old;

@@ -33,18 +33,21 @@ namespace dap {
 
 namespace {
 
-// WIDE: 256 rows in two streams, one CTA an SM; else 128 rows in one stream, two CTAs an SM (D = 256: one).
-template <int D_, bool WIDE_, bool GATHER_>
+// PAIR: 128 rows in one stream, two CTAs an SM; WIDE: 256 rows in two streams, one CTA an SM; DEEP: 128 rows and one CTA an SM
+// with all of its memory for the ring (D = 256: always).
+enum Shape { PAIR, WIDE, DEEP };
+template <int D_, Shape SHAPE, bool GATHER_>
 struct SpanTcCfg {
-    static constexpr bool GATHER = GATHER_, WIDE = WIDE_, SWZ = true;
+    static constexpr bool GATHER = GATHER_, SWZ = true;
     static constexpr int D = D_, BT = 64;
     static constexpr int ROWB = D * 2, SWB = 128, NBLK = ROWB / SWB, CPB = SWB / 16;
     static constexpr int TILE_BYTES = BT * ROWB;  // K or V of one tile
-    static constexpr int NSTREAM = WIDE ? 2 : 1, ROWS = 128 * NSTREAM, MINB = WIDE || D == 256 ? 1 : 2;
-    static constexpr int NS = (WIDE ? D == 64 ? 6 : 4 : D == 64 ? 4 : 2);  // K/V tiles in the ring
+    static constexpr int NSTREAM = SHAPE == WIDE ? 2 : 1, ROWS = 128 * NSTREAM, MINB = SHAPE == PAIR ? 2 : 1;
+    // K/V tiles in the ring
+    static constexpr int NS = D == 256 ? 2 : SHAPE == PAIR ? (D == 64 ? 4 : 2) : SHAPE == WIDE ? (D == 64 ? 6 : 4) : (D == 64 ? 10 : 5);
     static constexpr int NWS = 4 * NSTREAM, PRODUCER = NWS, ISSUER = NWS + 2, PV = ISSUER + NSTREAM,
                          THREADS = (PV + 1) * 32;
-    static constexpr int TO = MINB == 1 ? 256 : 128, TMEM_COLS = MINB == 1 ? 512 : 256;
+    static constexpr int TO = SHAPE == WIDE || D == 256 ? 256 : 128, TMEM_COLS = 2 * TO;
     static constexpr int QBLK = 128 * 128, Q_BYTES = NSTREAM * NBLK * QBLK;  // 64 dims of 128 rows; all of q
     static constexpr int RING_OFF = Q_BYTES, BAR_OFF = RING_OFF + NS * 2 * TILE_BYTES;
     // barriers: k_full, k_empty, v_full, v_empty [NS], s_done, p_ready, pv_done [stream][buffer], q_full, fin[3]
@@ -54,7 +57,7 @@ struct SpanTcCfg {
     static constexpr int TREE_OFF = MISC_OFF + 32, LINE_OFF = TREE_OFF + kTreeMost * 4;
     static constexpr int SMEM = LINE_OFF + ROWS * (kTreeWords + 1) * 4 + 1024;  // + slack to align the base
     static constexpr int ROW_B = D * 4 + 16;  // bytes of a row of sums on its way out (the 16: no bank conflicts)
-    static_assert(!WIDE || D <= 128, "tensor memory");
+    static_assert(SHAPE == DEEP || D <= 128, "tensor memory");
     static_assert(TO + NSTREAM * D <= TMEM_COLS && 128 * NSTREAM <= TO, "tensor memory");
     static_assert(SMEM <= 227 * 1024 / MINB, "shared memory");
     static_assert(MINB == 2 || SMEM > 114 * 1024, "one CTA an SM: a second would wait for tensor memory");
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     const int v0 = s * p.chunk, v1 = s < nsplit ? min(tl.len, v0 + p.chunk) : v0;
     const int J = max(0, v1 - v0 + BT - 1) / BT;  // K/V tiles of this CTA
     const bool work = nrows > 0 && J > 0;
-    const int streams = C::WIDE && nrows > 128 ? 2 : 1;  // that have rows
+    const int streams = C::NSTREAM == 2 && nrows > 128 ? 2 : 1;  // that have rows
     auto rows_of = [&](int x) { return max(0, min(128, nrows - 128 * x)); };
     if (threadIdx.x < C::NBAR) {  // a thread a barrier
         const int i = threadIdx.x, e = i - 4 * NS;
@@ -610,9 +613,9 @@ bool encode_q_rows(CUtensorMap *map, const DecodeArgs &a) {
     return encode_bf16(map, a.q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool WIDE, bool GATHER>
+template <int D, Shape SHAPE, bool GATHER>
 dap_status launch_tc(const SpanArgs &a, cudaStream_t stream) {
-    using C = SpanTcCfg<D, WIDE, GATHER>;
+    using C = SpanTcCfg<D, SHAPE, GATHER>;
     const int R = GATHER ? C::BT : gcd_int(a.d.page_size, C::BT), G = a.d.Hq / a.d.Hkv;
     CUtensorMap mq, mk = {}, mv = {};
     if (!encode_q_rows(&mq, a.d)) return DAP_ERR_CUDA;
@@ -636,13 +639,20 @@ dap_status launch_tc(const SpanArgs &a, cudaStream_t stream) {
     return launch_span_combine<D>(a, p, C::ROWS / G, stream);
 }
 
+// DEEP where every CTA has an SM to itself (16 trees of 16 nodes behind 2048 keys, 128 CTAs: 29.9 us for 35.6).
+template <int D, bool GATHER>
+dap_status tc_shape(const SpanArgs &a, cudaStream_t stream) {
+    if (a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) == 256) return launch_tc<D, WIDE, GATHER>(a, stream);
+    if ((long long)a.d.num_tiles * a.d.Hkv * a.d.num_splits <= dap_device_sm_count()) return launch_tc<D, DEEP, GATHER>(a, stream);
+    return launch_tc<D, PAIR, GATHER>(a, stream);
+}
+
 template <bool GATHER>
 dap_status tc_dims(const SpanArgs &a, cudaStream_t stream) {
-    const bool wide = a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) == 256;
     switch (a.d.D) {
-        case 64: return wide ? launch_tc<64, true, GATHER>(a, stream) : launch_tc<64, false, GATHER>(a, stream);
-        case 128: return wide ? launch_tc<128, true, GATHER>(a, stream) : launch_tc<128, false, GATHER>(a, stream);
-        case 256: return launch_tc<256, false, GATHER>(a, stream);
+        case 64: return tc_shape<64, GATHER>(a, stream);
+        case 128: return tc_shape<128, GATHER>(a, stream);
+        case 256: return launch_tc<256, DEEP, GATHER>(a, stream);
     }
     return DAP_ERR_UNSUPPORTED;
 }
