@@ -552,7 +552,7 @@ dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page
  *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT; the rows that there is room for are written.
  *   Where the pool has too few free pages, or would get more than num_pages, nothing is changed: boundaries are all 0,
  *   slots -1, and DAP_DEVERR_POOL is set (new rows past 2^31 - 1 likewise, with DAP_DEVERR_SEQLEN).
- *   Supported: B <= 16384, B * max_pages <= 2^30, int32 slots with num_pages * page_size <= 2^31 - 1.
+ *   Supported: B <= 8192, B * max_pages <= 2^30, int32 slots with num_pages * page_size <= 2^31 - 1.
  */
 dap_status kv_resize_paged(const int32_t *old_lens, const int32_t *new_lens, int32_t *block_table, int max_pages,
                            int page_size, int32_t *free_pages, int num_pages, int32_t *num_free, int32_t *indptr,

@@ -159,7 +159,7 @@ dap_status launch_fp8_runs(const RunArgs &a, bool write, cudaStream_t stream);
 bool read_errors_fp8_runs(unsigned int *flags, bool clear);
 
 // Lengths of a batch changed on the GPU, already validated.
-constexpr int kResizeMost = 16384;  // sequences: three prefix sums of theirs fit a CTA's shared memory
+constexpr int kResizeMost = 8192;  // sequences: six numbers of each fit a CTA's shared memory
 struct ResizeArgs {
     const int32_t *old_lens, *new_lens;
     int32_t *block_table;

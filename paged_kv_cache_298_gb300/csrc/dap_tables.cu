@@ -24,8 +24,9 @@ struct ResizeParams {
     int32_t *indptr;
     void *slots;
     int wide, rows;  // 8-byte slots; rows of the slot map
-    int rows_here;   // the slot map is written by this kernel (else by slots_kernel)
+    int part;        // kAll, kNoCount or kCountOnly
 };
+enum { kAll, kNoCount, kCountOnly };
 
 constexpr int kResizeThreads = 512;
 
@@ -42,16 +43,15 @@ __device__ __forceinline__ Lens lens_of(const ResizeParams &p, int b) {
     return l;
 }
 
-__device__ __forceinline__ int pages_of(int n, int ps) { return (int)(((long long)n + ps - 1) / ps); }
+// (n >= 0; the sum stays below 2^32)
+__device__ __forceinline__ int pages_of(int n, int ps) { return (int)(((unsigned)n + (unsigned)ps - 1u) / (unsigned)ps); }
 
-// The last i in [0, n) with at[i] <= x (at[0] <= x, ascending).
+// The last i in [0, n) with at[i] <= x (at[0] <= x, ascending); the same number of steps whatever x, so that several searches
+// of a thread run beside each other.
 __device__ __forceinline__ int last_at_most(const int *at, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at[mid] <= x) lo = mid;
-        else hi = mid;
-    }
+    int lo = 0;
+    for (int step = 1 << (31 - __clz(n)); step > 0; step >>= 1)
+        if (lo + step < n && at[lo + step] <= x) lo += step;
     return lo;
 }
 
@@ -60,35 +60,43 @@ __device__ __forceinline__ void store_slot(const ResizeParams &p, long long r, l
     else static_cast<int32_t *>(p.slots)[r] = (int32_t)slot;
 }
 
-// The slot of position `pos` in page `page`.
-__device__ __forceinline__ long long slot_of(const ResizeParams &p, int page, int pos) {
+// The slot of row `row` of page `page`.
+__device__ __forceinline__ long long slot_of(const ResizeParams &p, int page, int row) {
     if (page < 0 || page >= p.num_pages) {
         flag_error(DAP_DEVERR_PAGE);
         return -1;
     }
-    return (long long)page * p.page_size + pos % p.page_size;
+    return (long long)page * p.page_size + row;
 }
 
-// One cluster.  Every CTA computes the prefix sums of all sequences, and takes its share of the pages and rows; the CTAs
-// meet once, before the count of free pages that they all read is replaced.
-__global__ void __launch_bounds__(kResizeThreads) resize_kernel(const ResizeParams p) {
+// Every CTA computes the prefix sums of all sequences and takes its share of the pages and rows.  All of it in one cluster
+// (kAll): the CTAs meet once, before the count of free pages that they all read is replaced.  Many rows: on the whole device
+// (kNoCount), and then one CTA for the count (kCountOnly).
+__global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeParams p) {
     extern __shared__ int smem[];
-    int *s_rel = smem, *s_take = smem + (p.B + 1), *s_more = s_take + (p.B + 1);  // exclusive prefix sums, [B + 1]
+    // per sequence: exclusive sums of pages returned and taken and of new rows [B + 1]; where its first returned entry is in
+    // the block table, less its number, and its first taken one; old length
+    int *s_rel = smem, *s_take = s_rel + p.B + 1, *s_more = s_take + p.B + 1, *s_src = s_more + p.B + 1, *s_dst = s_src + p.B + 1;
+    int *s_from = s_dst + p.B + 1;
     __shared__ unsigned long long w_pages[kResizeThreads / 32], w_rows[kResizeThreads / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int count = *p.num_free;
-    // (returned << 32 | taken: neither sum passes 2^30, and new rows)
+    const bool tells = blockIdx.x == 0 && p.part != kCountOnly;
+    // (returned << 32 | taken: neither sum passes 2^30; and new rows)
     unsigned long long pages0 = 0, rows0 = 0;
     for (int b0 = 0; b0 < p.B; b0 += kResizeThreads) {
         const int b = b0 + tid;
         unsigned long long pages = 0, rows = 0;
+        Lens l = {0, 0, false};
+        int had = 0, has = 0;
         if (b < p.B) {
-            const Lens l = lens_of(p, b);
-            if (l.bad && blockIdx.x == 0) flag_error(DAP_DEVERR_SEQLEN);
-            const int d = pages_of(l.to, p.page_size) - pages_of(l.from, p.page_size);
-            pages = d < 0 ? (unsigned long long)(-d) << 32 : (unsigned long long)d;
+            l = lens_of(p, b);
+            if (l.bad && tells) flag_error(DAP_DEVERR_SEQLEN);
+            had = pages_of(l.from, p.page_size);
+            has = pages_of(l.to, p.page_size);
+            pages = has < had ? (unsigned long long)(had - has) << 32 : (unsigned long long)(has - had);
             rows = (unsigned long long)max(0, l.to - l.from);
         }
         unsigned long long ip = pages, ir = rows;
@@ -106,13 +114,24 @@ __global__ void __launch_bounds__(kResizeThreads) resize_kernel(const ResizePara
         }
         __syncthreads();
         unsigned long long bp = pages0, br = rows0;
-        for (int w = 0; w < kResizeThreads / 32; ++w) {
-            if (w < warp) {
-                bp += w_pages[w];
-                br += w_rows[w];
+        {   // lane w of every warp: the sums of warps 0 .. w
+            constexpr int W = kResizeThreads / 32;
+            unsigned long long x = lane < W ? w_pages[lane] : 0, y = lane < W ? w_rows[lane] : 0;
+#pragma unroll
+            for (int o = 1; o < W; o <<= 1) {
+                const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, x, o), c = __shfl_up_sync(0xFFFFFFFFu, y, o);
+                if (lane >= o) {
+                    x += a;
+                    y += c;
+                }
             }
-            pages0 += w_pages[w];
-            rows0 += w_rows[w];
+            const unsigned long long xb = __shfl_sync(0xFFFFFFFFu, x, (warp - 1) & 31), yb = __shfl_sync(0xFFFFFFFFu, y, (warp - 1) & 31);
+            if (warp > 0) {
+                bp += xb;
+                br += yb;
+            }
+            pages0 += __shfl_sync(0xFFFFFFFFu, x, W - 1);
+            rows0 += __shfl_sync(0xFFFFFFFFu, y, W - 1);
         }
         if (b < p.B) {
             bp += ip - pages;
@@ -120,6 +139,9 @@ __global__ void __launch_bounds__(kResizeThreads) resize_kernel(const ResizePara
             s_rel[b] = (int)(bp >> 32);
             s_take[b] = (int)(bp & 0xFFFFFFFFu);
             s_more[b] = (int)min(br, 0x7FFFFFFFull);
+            s_src[b] = b * p.max_pages + has - s_rel[b];
+            s_dst[b] = b * p.max_pages + had - s_take[b];
+            s_from[b] = l.from;
         }
         __syncthreads();
     }
@@ -133,110 +155,130 @@ __global__ void __launch_bounds__(kResizeThreads) resize_kernel(const ResizePara
         s_rel[p.B] = R;
         s_take[p.B] = A;
         s_more[p.B] = rows;
-        if (blockIdx.x == 0) {
+        if (tells) {
             if (!ok) flag_error(too_long ? DAP_DEVERR_SEQLEN : DAP_DEVERR_POOL);
             if (rows > p.rows) flag_error(DAP_DEVERR_SLOT);
         }
     }
-    // every CTA has read the count
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (p.part == kAll) {  // every CTA has read the count
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     __syncthreads();
     const int at = blockIdx.x * kResizeThreads + tid, all = gridDim.x * kResizeThreads;
-    if (at == 0 && ok) *p.num_free = (int)(top - A);
+    if (at == 0 && ok && p.part != kNoCount) *p.num_free = (int)(top - A);
+    if (p.part == kCountOnly) return;
     for (int b = at; b <= p.B; b += all) p.indptr[b] = ok ? s_more[b] : 0;
-    auto returned = [&](int r) -> int {  // the r-th returned page
-        const int b = last_at_most(s_rel, p.B, r);
-        const int i = pages_of(lens_of(p, b).to, p.page_size) + r - s_rel[b];
-        return p.block_table[(long long)b * p.max_pages + i];
-    };
+    auto returned = [&](int r) -> int { return p.block_table[s_src[last_at_most(s_rel, p.B, r)] + r]; };  // the r-th
     auto taken = [&](int e) -> int {  // the e-th taken page
         const int i = (int)(top - A) + e;
         return i < count ? p.free_pages[i] : returned(i - count);
     };
+    constexpr int U = 4;  // entries or rows that a thread has in flight
     if (ok) {
-        for (int r = at; r < R; r += all) p.free_pages[count + r] = returned(r);
-        for (int e = at; e < A; e += all) {
-            const int b = last_at_most(s_take, p.B, e);
-            const int i = pages_of(lens_of(p, b).from, p.page_size) + e - s_take[b];
-            p.block_table[(long long)b * p.max_pages + i] = taken(e);
+        for (int r0 = at; r0 < R; r0 += U * all) {
+            int page[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r0 + u * all < R) page[u] = returned(r0 + u * all);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r0 + u * all < R) p.free_pages[count + r0 + u * all] = page[u];
+        }
+        for (int e0 = at; e0 < A; e0 += U * all) {
+            int page[U], to[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + u * all;
+                if (e < A) {
+                    to[u] = s_dst[last_at_most(s_take, p.B, e)] + e;
+                    page[u] = taken(e);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e0 + u * all < A) p.block_table[to[u]] = page[u];
         }
     }
-    if (!p.rows_here) return;
-    for (int r = at; r < p.rows; r += all) {
-        long long slot = -1;
-        if (r < rows) {
-            const int b = last_at_most(s_more, p.B, r);
-            const int from = lens_of(p, b).from, pos = from + r - s_more[b];
-            const int i = pos / p.page_size, had = pages_of(from, p.page_size);
-            slot = slot_of(p, i < had ? p.block_table[(long long)b * p.max_pages + i] : taken(s_take[b] + i - had), pos);
+    for (long long r0 = at; r0 < p.rows; r0 += U * all) {
+        long long slot[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long r = r0 + u * all;
+            slot[u] = -1;
+            if (r < rows) {
+                const int b = last_at_most(s_more, p.B, (int)r);
+                const int pos = s_from[b] + (int)r - s_more[b], i = pos / p.page_size;
+                const int e = b * p.max_pages + i - s_dst[b];  // number among the taken; an entry that was there: before them
+                slot[u] = slot_of(p, e < s_take[b] ? p.block_table[s_dst[b] + e] : taken(e), pos - i * p.page_size);
+            }
         }
-        store_slot(p, r, slot);
-    }
-}
-
-// The slot map from the tables and boundaries that resize_kernel wrote.
-__global__ void __launch_bounds__(256) slots_kernel(const ResizeParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int rows = p.indptr[p.B];
-    for (long long r = (long long)blockIdx.x * 256 + threadIdx.x; r < p.rows; r += (long long)gridDim.x * 256) {
-        long long slot = -1;
-        if (r < rows) {
-            const int b = last_at_most(p.indptr, p.B, (int)r);
-            const int pos = p.old_lens[b] + (int)r - p.indptr[b];
-            slot = slot_of(p, p.block_table[(long long)b * p.max_pages + pos / p.page_size], pos);
-        }
-        store_slot(p, r, slot);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r0 + u * all < p.rows) store_slot(p, r0 + u * all, slot[u]);
     }
 }
 
 // ---- accepted drafts ------------------------------------------------------------------------------------------
-// The rows of node path[j] go to place j behind the context.  The path ascends strictly, so path[j] >= j, and a place that
-// is written is the source of no later row: each thread moves its 16 bytes of every row in order, in place, and no two
-// threads share an address.
+// The rows of node path[j] go to place j behind the context.  The path ascends strictly, so path[j] >= j: with 32 rows at a
+// time read before any of them is written, no place that is written is the source of a later batch, and pieces of a row are
+// independent.  One warp moves a piece of up to 1 KB of every row of a sequence's path, K or V: a lane a row, by bulk copies
+// through shared memory, so that all rows of a batch are in flight at once whatever the registers (7.8 us for 15.8 with
+// 16-byte loads, 16 rows in flight: 256 paths of up to 24 rows of 2 KB).
 
 struct CommitParams {
-    uint4 *cache[2];
+    char *k_cache, *v_cache;
     int num_pages, page_size, max_pages;
     const int32_t *block_table, *positions, *path, *accepted;
-    int max_path, B;
-    long long row_chunks;  // 16-byte chunks of a row of all kv heads
-    int groups;            // of 32 chunks
+    int max_path, row_bytes, pieces;
 };
+constexpr int kPieceBytes = 1024;
 
-__global__ void __launch_bounds__(128) commit_kernel(const CommitParams p) {
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(32) commit_kernel(const CommitParams p) {
+    __shared__ __align__(128) char rows[32 * kPieceBytes];
+    __shared__ uint64_t bar;
+    const int lane = threadIdx.x;
+    const int b = blockIdx.x / (2 * p.pieces), rest = blockIdx.x - b * 2 * p.pieces;  // (sequence, K or V, piece)
+    const int at = (rest >> 1) * kPieceBytes, bytes = min(kPieceBytes, p.row_bytes - at);
+    if (lane == 0) {
+        mbar_init(&bar, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);  // (sequence, K or V, 32 chunks)
-    const int lane = threadIdx.x & 31;
-    const int per = 2 * p.groups;
-    const int b = (int)(w / per), rest = (int)(w - (long long)b * per), x = rest / p.groups;
-    if (b >= p.B) return;
-    const int n = p.accepted[b];
-    const long long base = p.positions[b];
     const int32_t *path = p.path + (long long)b * p.max_path;
+    // (one trip for all three: the first 32 nodes are there whatever the count)
+    const int n = p.accepted[b], head = lane < p.max_path ? path[lane] : 0;
+    const long long base = p.positions[b];
     const bool tells = rest == 0 && lane == 0;
     if (n == 0) return;
     // the whole path is looked at before the first row moves
     bool good = n > 0 && n <= p.max_path && base >= 0;
     if (good) {
         bool up = true;
-        int last = 0;
+        int last = -1;  // the node before lane 0's, then the path's last
         for (int j0 = 0; j0 < n; j0 += 32) {
-            const int j = j0 + lane;
-            if (j < n) {
-                last = path[j];
-                up = up && last > (j > 0 ? path[j - 1] : -1);
-            }
+            const int j = j0 + lane, x = j0 == 0 ? head : j < n ? path[j] : 0;
+            const int left = __shfl_up_sync(0xFFFFFFFFu, x, 1);
+            if (j < n) up = up && x > (lane > 0 ? left : last);
+            last = __shfl_sync(0xFFFFFFFFu, x, min(31, n - 1 - j0));
         }
         good = __all_sync(0xFFFFFFFFu, up);
-        if (good) {
-            const int end = __shfl_sync(0xFFFFFFFFu, last, (n - 1) & 31);
-            if (base + end >= (long long)p.max_pages * p.page_size) {
-                if (tells) flag_error(DAP_DEVERR_SEQLEN);
-                return;
-            }
+        if (good && base + last >= (long long)p.max_pages * p.page_size) {
+            if (tells) flag_error(DAP_DEVERR_SEQLEN);
+            return;
         }
     }
     if (!good) {
@@ -244,39 +286,40 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitParams p) {
         return;
     }
     const int32_t *table = p.block_table + (long long)b * p.max_pages;
-    const long long c = (long long)(rest - x * p.groups) * 32 + lane;
-    uint4 *cache = p.cache[x] + c;
-    const bool mine = c < p.row_chunks;
+    char *cache = ((rest & 1) ? p.v_cache : p.k_cache) + at, *mine = rows + lane * kPieceBytes;
+    const uint32_t ps = p.page_size;
+    uint32_t phase = 0;
     for (int j0 = 0; j0 < n; j0 += 32) {
-        // lane j: the cache rows that row j0 + j is read from and goes to; -1: it stays
-        long long from = -1, to = -1;
+        // lane j: the cache rows that row j0 + j is read from and goes to (places are below 2^31 + 2^31)
+        long long from = 0, to = -1;  // (-1: it stays)
         if (j0 + lane < n) {
-            const long long s = base + path[j0 + lane], d = base + j0 + lane;
+            const uint32_t s = (uint32_t)(base + (j0 == 0 ? head : path[j0 + lane])), d = (uint32_t)(base + j0 + lane);
             if (s != d) {
-                const int sp = table[s / p.page_size], dp = table[d / p.page_size];
+                const uint32_t se = s / ps, de = d / ps;
+                const int sp = table[se], dp = table[de];
                 if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) {
                     if (rest == 0) flag_error(DAP_DEVERR_PAGE);
                 } else {
-                    from = (long long)sp * p.page_size + s % p.page_size;
-                    to = (long long)dp * p.page_size + d % p.page_size;
+                    from = (long long)sp * ps + (s - se * ps);
+                    to = (long long)dp * ps + (d - de * ps);
                 }
             }
         }
-        const int m = min(32, n - j0);
-        for (int k0 = 0; k0 < m; k0 += 8) {
-            uint4 v[8];
-            long long at[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const long long f = __shfl_sync(0xFFFFFFFFu, from, (k0 + k) & 31);
-                at[k] = __shfl_sync(0xFFFFFFFFu, to, (k0 + k) & 31);
-                if (k0 + k >= m) at[k] = -1;
-                if (at[k] >= 0 && mine) v[k] = cache[f * p.row_chunks];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (at[k] >= 0 && mine) cache[at[k] * p.row_chunks] = v[k];
+        const uint32_t moves = __ballot_sync(0xFFFFFFFFu, to >= 0);
+        if (moves == 0) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&bar, (uint32_t)__popc(moves) * (uint32_t)bytes);
+        __syncwarp();
+        if (to >= 0) bulk_load(mine, cache + from * p.row_bytes, (uint32_t)bytes, &bar);
+        // (a phase a batch that moves anything)
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar, phase))) {
+            (void)mbar_wait(&bar, phase);  // gave up: once more for the copies in flight, before the shared memory goes
+            return;
         }
+        phase ^= 1u;
+        if (to >= 0) bulk_store(cache + to * p.row_bytes, mine, (uint32_t)bytes);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 }
 
@@ -297,23 +340,35 @@ dap_status launch_resize(const ResizeArgs &a, cudaStream_t stream) {
     p.slots = a.slots;
     p.wide = a.slot_bytes == 8;
     p.rows = a.rows;
-    p.rows_here = a.rows <= 8192;
-    const int smem = 3 * (a.B + 1) * 4;
+    const int smem = 6 * (a.B + 1) * 4;
     static PerDeviceOcc occ = {};
-    if (prepare_kernel(resize_kernel, kResizeThreads, 3 * (kResizeMost + 1) * 4, &occ) <= 0) return DAP_ERR_CUDA;
-    const int ctas = a.B > 64 || a.rows > 2048 ? 8 : 1;
-    if (launch_cluster_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, ctas, stream, p) !=
-        cudaSuccess)
+    if (prepare_kernel(resize_kernel, kResizeThreads, 6 * (kResizeMost + 1) * 4, &occ) <= 0) return DAP_ERR_CUDA;
+    // One cluster while its threads have up to four rows each, else the whole device and a launch for the count (1.2 million
+    // rows on 256 sequences taken and returned: 26 us, with the pages by a cluster 48); one CTA where that is enough (16
+    // sequences of 8 rows: 3.3 us).
+    constexpr int kClusterRows = 4 * 8 * kResizeThreads;
+    if (a.rows <= kClusterRows) {
+        const int ctas = a.B > 64 || a.rows > 2048 ? 8 : 1;
+        p.part = kAll;
+        return launch_cluster_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, ctas, stream,
+                                             p) == cudaSuccess
+                   ? DAP_OK
+                   : DAP_ERR_CUDA;
+    }
+    const int most = std::max(1, dap_device_sm_count()) * (smem <= 48 * 1024 ? 4 : 1);
+    const int ctas = std::min(most, (a.rows + 4 * kResizeThreads - 1) / (4 * kResizeThreads));
+    p.part = kNoCount;
+    if (launch_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, stream, p) != cudaSuccess)
         return DAP_ERR_CUDA;
-    if (p.rows_here) return DAP_OK;
-    const dim3 grid((unsigned)std::min(8 * std::max(1, dap_device_sm_count()), (a.rows + 255) / 256));
-    return launch_dependent(slots_kernel, grid, dim3(256), stream, p) == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
+    p.part = kCountOnly;
+    return launch_dependent_smem(resize_kernel, dim3(1), dim3(kResizeThreads), smem, stream, p) == cudaSuccess ? DAP_OK
+                                                                                                              : DAP_ERR_CUDA;
 }
 
 dap_status launch_commit(const CommitArgs &a, cudaStream_t stream) {
     CommitParams p = {};
-    p.cache[0] = static_cast<uint4 *>(a.k_cache);
-    p.cache[1] = static_cast<uint4 *>(a.v_cache);
+    p.k_cache = static_cast<char *>(a.k_cache);
+    p.v_cache = static_cast<char *>(a.v_cache);
     p.num_pages = a.num_pages;
     p.page_size = a.page_size;
     p.max_pages = a.max_pages;
@@ -322,13 +377,13 @@ dap_status launch_commit(const CommitArgs &a, cudaStream_t stream) {
     p.path = a.path;
     p.accepted = a.accepted;
     p.max_path = a.max_path;
-    p.B = a.B;
-    p.row_chunks = (long long)a.Hkv * a.D / 8;
-    p.groups = (int)((p.row_chunks + 31) / 32);
-    const long long grid = ((long long)a.B * 2 * p.groups + 3) / 4;
-    if (grid > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
-    return launch_dependent(commit_kernel, dim3((unsigned)grid), dim3(128), stream, p) == cudaSuccess ? DAP_OK
-                                                                                                      : DAP_ERR_CUDA;
+    const long long row_bytes = (long long)a.Hkv * a.D * 2, pieces = (row_bytes + kPieceBytes - 1) / kPieceBytes;
+    if (row_bytes > 0x7FFFFFFFLL || 2 * pieces * a.B > 0x7FFFFFFFLL) return DAP_ERR_SHAPE;
+    p.row_bytes = (int)row_bytes;
+    p.pieces = (int)pieces;
+    return launch_dependent(commit_kernel, dim3((unsigned)(2 * pieces * a.B)), dim3(32), stream, p) == cudaSuccess
+               ? DAP_OK
+               : DAP_ERR_CUDA;
 }
 
 bool read_errors_tables(unsigned int *flags, bool clear) {

@@ -69,7 +69,7 @@ def test_bad_arguments_of_a_commit(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), SHAPE), (dict(maxp=0), SHAPE), (dict(ps=0), SHAPE), (dict(P=0), SHAPE), (dict(rows=-1), SHAPE),
-    (dict(bytes=2), SHAPE), (dict(bytes=0), SHAPE), (dict(B=16385), UNSUPPORTED), (dict(B=1 << 14, maxp=(1 << 16) + 1), UNSUPPORTED),
+    (dict(bytes=2), SHAPE), (dict(bytes=0), SHAPE), (dict(B=8193), UNSUPPORTED), (dict(B=1 << 13, maxp=(1 << 17) + 1), UNSUPPORTED),
     (dict(bytes=4, P=1 << 20, ps=1 << 11), UNSUPPORTED), (dict(old=None), NULL), (dict(new=None), NULL), (dict(table=None), NULL),
     (dict(free=None), NULL), (dict(count=None), NULL), (dict(indptr=None), NULL), (dict(slots=None), NULL), (dict(old=ODD), ALIGN),
     (dict(new=ODD), ALIGN), (dict(table=ODD), ALIGN), (dict(free=ODD), ALIGN), (dict(count=ODD), ALIGN), (dict(indptr=ODD), ALIGN),

@@ -91,10 +91,10 @@ def test_steps_of_all_kinds(ps, B):
     assert binding.get_device_errors() == 0
 
 
-@pytest.mark.parametrize("rows", [8192, 8193, 50000])
+@pytest.mark.parametrize("rows", [2048, 2049, 16384, 16385, 50000])
 @pytest.mark.parametrize("wide", [False, True])
 def test_long_slot_maps(rows, wide):
-    """Either side of the size from which the slot map has a kernel of its own."""
+    """Either side of the sizes from which a cluster, and then the whole device, works on the rows."""
     r = random.Random(rows)
     cuts = sorted(r.randint(0, rows) for _ in range(36))
     lens = [b - a for a, b in zip([0] + cuts, cuts + [rows])]
