@@ -701,30 +701,32 @@ int dap_span_splits(int sm_count, int num_tiles, int total_q, int B, int Hq, int
         return 0;
     const int most = span_keys(max_kv_len, window, sinks, tree ? kTreeMost : tokens_per_tile);
     if (num_splits == 0 && num_tiles > 0 && most > 0) {
-        // The count with the least time by this model, in microseconds, fitted to sweeps over 110 batches (1.4% above the
-        // best count in the mean, 24% at most): a CTA starts and ends in `fixed` and takes `tile` a K/V tile, less where it
-        // has an SM to itself; with more CTAs than fit at once they follow one another, and the longest is late at the end;
-        // K/V at 6.6 MB/us; merging costs a launch, trips to memory, and the partial rows' way.
+        // The count with the least time by this model, in microseconds, fitted to sweeps over 110 batches (0.8% above the
+        // best count in the mean, 24% at most): a CTA starts and ends in `fixed` and takes `tile` for 64 keys, by the kernel
+        // that its number selects; with more CTAs than fit at once they follow one another, and the longest is late at the
+        // end; K/V at `rate` MB/us; merging costs a launch, trips to memory, and the partial rows' way.
         const int sms = std::max(1, sm_count), cols = tokens_per_tile * (Hq / Hkv);
         const bool warp = cols <= 16, wide = cols == 256;
-        const double keys = warp ? 32. : 64.;
-        const long long slots = (long long)sms * (warp ? (D == 256 ? 2 : 4) : wide || D == 256 ? 1 : 2);
+        const double dims = D == 256 ? 2. : D == 128 ? 1. : 0.8;
         const double avg = total_kv > 0 ? std::min<double>(most, std::max(1., (double)total_kv / std::max(1, B))) : most;
         const long long units = (long long)num_tiles * Hkv;
+        const double unit_mb = avg * D * 4e-6, mb = (cols == 128 ? (double)B * Hkv : (double)units) * unit_mb;
         double best = 1e300;
         const int limit = (int)std::min<long long>(128, ceil_div_ll(most, kTileTokens));
         for (int S = 1; S <= limit; ++S) {
-            const bool alone = cols == 128 && D < 256 && units * S <= sms;
-            const double fixed = warp ? 4.1 : wide ? 10.8 : alone ? 7.0 : 8.0;
-            const double tile = warp ? (D == 256 ? 1.06 : D == 128 ? 0.53 : 0.42) : wide ? 0.86 : alone ? 0.69 : 1.0;
+            const bool few = warp && span_few(sms, units * S, D), alone = cols == 128 && D < 256 && units * S <= sms;
+            const double fixed = few ? 4.1 : warp ? 3.3 : wide ? 11.5 : alone ? 7.7 : 8.3;
+            const double tile = few ? 0.73 * dims : warp ? 2.1 * dims : wide ? 0.83 : alone ? 0.68 : 1.0;
+            const long long slots = (long long)sms * (few ? (D == 256 ? 1 : 2) : warp ? (D == 256 ? 2 : 4) : wide || D == 256 ? 1 : 2);
             const double chunk = dap_chunk_tokens(most, S);
             const double eff = std::max(1., std::min<double>(S, ceil(avg / chunk)));
-            const double longest = fixed + tile * std::min<double>(most, chunk) / keys;
-            const double mean = fixed + tile * std::min(avg / eff, chunk) / keys;
+            const double longest = fixed + tile * std::min<double>(most, chunk) / 64.;
+            const double mean = fixed + tile * std::min(avg / eff, chunk) / 64.;
             const double waves = (double)units * eff / (double)slots;
             double us = std::max(longest, mean * waves + (waves > 1. ? 0.66 * longest : 0.));
-            if (cols != 128) us = std::max(us, fixed + (double)units * avg * D * 4e-6 / 6.6);
-            if (S > 1) us += 2.3 + 0.06 * eff + (double)total_q * Hq * eff * D * 8e-6 / 9.1;
+            if (cols != 128) us = std::max(us, fixed + mb / 6.6);
+            else if (!alone && D < 256) us = std::max(us, fixed + mb / 5.9);
+            if (S > 1) us += 1.7 + 0.08 * eff + (double)total_q * Hq * eff * D * 8e-6 / 10.1;
             if (us < best) {
                 best = us;
                 num_splits = S;
@@ -1047,6 +1049,8 @@ dap_status dap_get_device_errors(unsigned int *flags, int clear) {
     if (!read_errors_shared_suffix_gather(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_span(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_span_gather(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_span_few(flags, clear != 0)) return DAP_ERR_CUDA;
+    if (!read_errors_span_few_gather(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_span_tc(flags, clear != 0)) return DAP_ERR_CUDA;
     if (!read_errors_tables(flags, clear != 0)) return DAP_ERR_CUDA;
     return DAP_OK;

@@ -195,6 +195,11 @@ constexpr int kTreeMost = 256;  // nodes of one tree
 int span_tokens_per_tile(int sms, int B, int Hkv, int G, int D, int max_q_len);
 dap_status launch_span(const SpanArgs &a, cudaStream_t stream);
 dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream);
+dap_status launch_span_few(const SpanArgs &a, cudaStream_t stream);
+dap_status launch_span_few_gather(const SpanArgs &a, cudaStream_t stream);
+bool span_few(int sms, long long ctas, int D);
+bool read_errors_span_few(unsigned int *flags, bool clear);
+bool read_errors_span_few_gather(unsigned int *flags, bool clear);
 dap_status launch_span_tc(const SpanArgs &a, cudaStream_t stream);
 bool read_errors_span_tc(unsigned int *flags, bool clear);
 bool read_errors_span(unsigned int *flags, bool clear);

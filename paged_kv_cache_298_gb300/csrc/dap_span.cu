@@ -17,9 +17,15 @@ int span_tokens_per_tile(int sms, int B, int Hkv, int G, int D, int max_q_len) {
     return (wide ? 256 : 128) / G;
 }
 
+// 64-key tiles where their CTAs, two an SM (one at D = 256), all run at once.
+bool span_few(int sms, long long ctas, int D) { return ctas <= (D == 256 ? 1LL : 2LL) * sms; }
+
 dap_status launch_span(const SpanArgs &a, cudaStream_t stream) {
     if (a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) >= 128) return launch_span_tc(a, stream);
-    return a.d.page_size % 8 != 0 ? launch_span_gather(a, stream) : span_dims<false>(a, stream);
+    const bool gather = a.d.page_size % 8 != 0;
+    if (span_few(dap_device_sm_count(), (long long)a.d.num_tiles * a.d.Hkv * a.d.num_splits, a.d.D))
+        return gather ? launch_span_few_gather(a, stream) : launch_span_few(a, stream);
+    return gather ? launch_span_gather(a, stream) : span_dims<2, false>(a, stream);
 }
 
 bool read_errors_span(unsigned int *flags, bool clear) { return read_span_errors(flags, clear); }

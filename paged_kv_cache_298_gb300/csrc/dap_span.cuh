@@ -80,15 +80,18 @@ __device__ __forceinline__ void load_parents(int *to, const int32_t *from, int n
 }
 
 // ---- warp-level kernel: 8 NT query columns (tokens x the G heads of a kv head) --------------------------------------
-// The multi-token kernel's producer and consumer over spans, in CTAs of 32-key tiles and two consumer warps, four to an
-// SM (two at D = 256), so that one's start and end are covered by the others.
+// The multi-token kernel's producer and consumer over spans, in two shapes (launch_span has the rule): KW = 2, 32-key tiles and
+// two consumer warps, four CTAs an SM (two at D = 256), so that one's start and end are covered by the others; KW = 4, 64-key
+// tiles and four consumer warps, two CTAs an SM (one at D = 256), where there are no more CTAs than that and a tile's chain
+// (scores, maximum, weights, values: 0.5 us whatever its keys) is what counts.
 
-template <int D_, int G_, int NT_, bool GATHER_>
+template <int D_, int G_, int NT_, int KW_, bool GATHER_>
 struct SpanCfg {
     static constexpr bool GATHER = GATHER_, MMA = true, SWZ = true, MASK = false;
-    static constexpr int D = D_, G = G_, HG = 1, NT = NT_, CG = 1, KW = 2, NWC = 2, BT = 32, KPW = 16;
+    static constexpr int D = D_, G = G_, HG = 1, NT = NT_, CG = 1, KW = KW_, NWC = KW, BT = 16 * KW, KPW = 16;
     static constexpr int NCOL = 8 * NT, QT = NCOL / G;
-    static constexpr int NS = D == 32 ? 8 : D == 64 ? 6 : 3, MINB = D == 256 ? 2 : 4;
+    static constexpr int NS = D == 32 ? 8 : D == 64 ? (KW == 2 ? 6 : 5) : 3;
+    static constexpr int MINB = (D == 256 ? 2 : 4) / (KW / 2);
     static constexpr int ROWB = D * 2, SWB = D >= 64 ? 128 : 64, NBLK = ROWB / SWB, CPB = SWB / 16;
     static constexpr int TILE_BYTES = BT * ROWB, STAGE_BYTES = 2 * TILE_BYTES;
     static constexpr int NPART = D == 32 ? 2 : 4;
@@ -307,15 +310,17 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         if constexpr (C::GATHER) {  // ---- producer warp, row gather
             RowPages<C> next;
             auto lookup = [&](int i) {
-                const int v = v0 + i * BT + lane, t = tl.place(v0 + i * BT) + lane;
-                next.pg[0] = 0;
-                next.slot[0] = 0;
-                if (i < ntiles && v < v1) {  // (a hidden row: some row of a page that is seen)
-                    next.pg[0] = __ldg(table + (hidden(t, 1) ? tl.lo : t) / p.page_size);
-                    next.slot[0] = t % p.page_size;
+#pragma unroll
+                for (int k = 0; k < RowPages<C>::N; ++k) {
+                    const int r = lane + 32 * k, v = v0 + i * BT + r, t = tl.place(v0 + i * BT) + r;
+                    next.pg[k] = 0;
+                    next.slot[k] = 0;
+                    if (i < ntiles && v < v1) {  // (a hidden row: some row of a page that is seen)
+                        next.pg[k] = __ldg(table + (hidden(t, 1) ? tl.lo : t) / p.page_size);
+                        next.slot[k] = t % p.page_size;
+                    }
                 }
             };
-            static_assert(RowPages<C>::N == 1, "a row a lane");
             lookup(0);
             for (int i = 0; i < ntiles; ++i) {
                 const int st = i % NS;
@@ -532,9 +537,9 @@ dap_status launch_span_combine(const SpanArgs &a, const SpanParams &p, int qt, c
     return e == cudaSuccess ? DAP_OK : DAP_ERR_CUDA;
 }
 
-template <int D, int G, int NT, bool GATHER>
+template <int D, int G, int NT, int KW, bool GATHER>
 dap_status launch_span_warp(const SpanArgs &a, cudaStream_t stream) {
-    using C = SpanCfg<D, G, NT, GATHER>;
+    using C = SpanCfg<D, G, NT, KW, GATHER>;
     const int R = GATHER ? 1 : gcd_int(a.d.page_size, C::BT);
     CUtensorMap mk = {}, mv = {};  // (the row-gather producer reads the cache directly)
     if (!GATHER && (!encode_cache_map<C>(&mk, a.d.k, a.d.D, a.d.Hkv, a.d.page_size, a.d.num_pages, R) ||
@@ -551,26 +556,26 @@ dap_status launch_span_warp(const SpanArgs &a, cudaStream_t stream) {
     return launch_span_combine<D>(a, p, C::QT, stream);
 }
 
-template <int D, int NT, bool GATHER>
+template <int D, int NT, int KW, bool GATHER>
 dap_status span_groups(const SpanArgs &a, cudaStream_t stream) {
     switch (a.d.Hq / a.d.Hkv) {
-        case 1: return launch_span_warp<D, 1, NT, GATHER>(a, stream);
-        case 2: return launch_span_warp<D, 2, NT, GATHER>(a, stream);
-        case 4: return launch_span_warp<D, 4, NT, GATHER>(a, stream);
-        case 8: return launch_span_warp<D, 8, NT, GATHER>(a, stream);
+        case 1: return launch_span_warp<D, 1, NT, KW, GATHER>(a, stream);
+        case 2: return launch_span_warp<D, 2, NT, KW, GATHER>(a, stream);
+        case 4: return launch_span_warp<D, 4, NT, KW, GATHER>(a, stream);
+        case 8: return launch_span_warp<D, 8, NT, KW, GATHER>(a, stream);
     }
     return DAP_ERR_UNSUPPORTED;
 }
 
 // 8 or 16 query columns a tile.
-template <bool GATHER>
+template <int KW, bool GATHER>
 dap_status span_dims(const SpanArgs &a, cudaStream_t stream) {
     const bool narrow = a.d.tokens_per_tile * (a.d.Hq / a.d.Hkv) == 8;
     switch (a.d.D) {
-        case 32: return narrow ? span_groups<32, 1, GATHER>(a, stream) : span_groups<32, 2, GATHER>(a, stream);
-        case 64: return narrow ? span_groups<64, 1, GATHER>(a, stream) : span_groups<64, 2, GATHER>(a, stream);
-        case 128: return narrow ? span_groups<128, 1, GATHER>(a, stream) : span_groups<128, 2, GATHER>(a, stream);
-        case 256: return narrow ? span_groups<256, 1, GATHER>(a, stream) : span_groups<256, 2, GATHER>(a, stream);
+        case 32: return narrow ? span_groups<32, 1, KW, GATHER>(a, stream) : span_groups<32, 2, KW, GATHER>(a, stream);
+        case 64: return narrow ? span_groups<64, 1, KW, GATHER>(a, stream) : span_groups<64, 2, KW, GATHER>(a, stream);
+        case 128: return narrow ? span_groups<128, 1, KW, GATHER>(a, stream) : span_groups<128, 2, KW, GATHER>(a, stream);
+        case 256: return narrow ? span_groups<256, 1, KW, GATHER>(a, stream) : span_groups<256, 2, KW, GATHER>(a, stream);
     }
     return DAP_ERR_UNSUPPORTED;
 }

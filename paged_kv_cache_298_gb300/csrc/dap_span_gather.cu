@@ -4,7 +4,7 @@
 
 namespace dap {
 
-dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream) { return span_dims<true>(a, stream); }
+dap_status launch_span_gather(const SpanArgs &a, cudaStream_t stream) { return span_dims<2, true>(a, stream); }
 
 bool read_errors_span_gather(unsigned int *flags, bool clear) { return read_span_errors(flags, clear); }
 
