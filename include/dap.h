@@ -467,7 +467,8 @@ int dap_span_splits(int sm_count, int num_tiles, int total_q, int B, int Hq, int
  * Sliding-window paged GQA attention with sinks, for one or many new tokens a sequence: token i, in place and position
  * p = ctx + i, sees the places t <= p with t > p - window or t < sinks:
  *   out[qo_indptr[b] + i, h, :] = sum_t softmax_t(scale * q[.., h, :] . K[b,t,h/G,:]) V[b,t,h/G,:].
- * A token with p < 0 (q_len[b] > seq_lens[b], flagged DAP_DEVERR_SEQLEN) gives a zero row.
+ * A token with p < 0 (q_len[b] > seq_lens[b], flagged DAP_DEVERR_SEQLEN) gives a zero row; so do, unflagged, the tokens of a
+ * sequence of length 0 (the padding of a captured batch).
  *   q, k_cache, v_cache, block_table, seq_lens, max_kv_len, out, scale, strides, alignment: as decode_attn_paged_multi,
  *                max_kv_len at most 2^30 - 64.  A work-map entry that names no token of its sequence is skipped and
  *                flagged (DAP_DEVERR_QMAP); tokens that no entry names have undefined results.
@@ -549,7 +550,9 @@ dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page
  *                       block_table[b][t / page_size] * page_size + t % page_size; rows behind the last have -1, and so has
  *                       a row whose page is outside the pool (DAP_DEVERR_PAGE).  (int64: what kv_append_fp8 takes.  int32:
  *                       a block table of one-slot pages, through which kv_append_paged writes the rows of a whole run.)
- *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT; the rows that there is room for are written.
+ *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT, unless it is 0 (no slot map is wanted); the rows
+ *                       that there is room for are written.
+ *   Calls on the same pool or table must not overlap.
  *   Where the pool has too few free pages, or would get more than num_pages, nothing is changed: boundaries are all 0,
  *   slots -1, and DAP_DEVERR_POOL is set (new rows past 2^31 - 1 likewise, with DAP_DEVERR_SEQLEN).
  *   Supported: B <= 8192, B * max_pages <= 2^30, int32 slots with num_pages * page_size <= 2^31 - 1.

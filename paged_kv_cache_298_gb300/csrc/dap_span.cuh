@@ -39,7 +39,8 @@ struct SpanTile : MultiTile {
 
 __device__ __forceinline__ bool span_tile(const SpanParams &pp, int b, int tindex, int q0, int q1, int L, int qt,
                                           bool report, SpanTile *t) {
-    if (!multi_tile(pp.sp, b, tindex, q0, q1, L, qt, report, t)) return false;
+    // (a sequence of length 0 is padding: zero rows, and no error)
+    if (!multi_tile(pp.sp, b, tindex, q0, q1, L, qt, report && (L != 0 || b < 0 || b >= pp.sp.B), t)) return false;
     if (pp.parents && t->qlen > kTreeMost) {
         if (report) flag_error(DAP_DEVERR_QMAP);
         return false;

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeP
         s_more[p.B] = rows;
         if (tells) {
             if (!ok) flag_error(too_long ? DAP_DEVERR_SEQLEN : DAP_DEVERR_POOL);
-            if (rows > p.rows) flag_error(DAP_DEVERR_SLOT);
+            if (rows > p.rows && p.rows > 0) flag_error(DAP_DEVERR_SLOT);
         }
     }
     if (p.part == kAll) {  // every CTA has read the count

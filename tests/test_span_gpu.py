@@ -169,6 +169,34 @@ def test_strided_views_and_given_buffers():
             assert (out == 7.0).all()   # nothing beside the view was written
 
 
+@pytest.mark.parametrize("n,D", [(1, 64), (3, 128), (40, 128), (40, 256), (60, 64)])
+def test_heads_further_apart_than_tokens(n, D):
+    b = Batch([100, 300], [n, n], 8, 2, D, 16, seed=4, kind="mixed")
+    want = tree(b)
+    b.check(want)
+    b.q = b.q.transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.empty((8, b.total, D), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    assert torch.equal(tree(b, out=out), want)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_padding_of_a_batch(n):
+    """Sequences of length 0 give zero rows and no error, whatever their tables and q hold."""
+    for kind in (None, "mixed"):
+        b = Batch([200, 0, 90, 0], [n] * 4, 8, 2, 128, 16, seed=6, kind=kind)
+        call = window if kind is None else tree
+        want = call(b, 50, 3).clone()
+        b.seq_lens[1] = b.seq_lens[3] = 0
+        b.table[1] = b.table[3] = -1
+        b.q[n:2 * n] = float("nan")
+        for S in (0, 1, 3):
+            got = call(b, 50, 3, num_splits=S)
+            assert (got[n:2 * n] == 0).all() and (got[3 * n:] == 0).all()
+            if S == 0:
+                assert torch.equal(got[:n], want[:n]) and torch.equal(got[2 * n:3 * n], want[2 * n:3 * n])
+    assert binding.get_device_errors() == 0
+
+
 def test_errors_are_flagged_and_kept_in_bounds():
     for n in (1, 40):
         b = Batch([200, 90], [n, n], 8, 2, 128, 16, seed=6, kind="chain")

@@ -168,6 +168,16 @@ def test_more_rows_than_the_slot_map_holds():
         p.same()
 
 
+@pytest.mark.parametrize("B", [3, 200])
+def test_a_call_that_wants_no_slot_map(B):
+    p = Pool([5] * B, 16, 8, 7 * B, seed=2)
+    indptr, slots = p.resize([100] * B, 0)
+    want_indptr, _ = p.python([100] * B)
+    assert indptr.tolist() == want_indptr and slots.numel() == 0
+    p.same()
+    assert binding.get_device_errors() == 0
+
+
 def test_pages_outside_the_pool_have_no_slot():
     for rows in (30, 9000):
         p = Pool([0, 10], 16, rows // 16 + 2, rows // 16 + 3, seed=2)
