@@ -524,6 +524,7 @@ dap_status decode_attn_paged_tree(const void *q, long long q_stride_t, long long
  *   A path that does not ascend, or a count out of range, leaves its sequence as it is and sets DAP_DEVERR_QMAP; so does a
  *   place outside [0, max_pages * page_size) with DAP_DEVERR_SEQLEN.  A row whose page, from or to, is outside the pool is
  *   not moved (DAP_DEVERR_PAGE).  No two sequences may write to the same place, nor one where another reads.
+ *   k_cache and v_cache must not overlap (DAP_ERR_SHAPE).
  *   Supported: D a multiple of 8; pointers 16-byte aligned.
  */
 dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page_size, const int32_t *block_table,
@@ -552,7 +553,8 @@ dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page
  *                       a block table of one-slot pages, through which kv_append_paged writes the rows of a whole run.)
  *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT, unless it is 0 (no slot map is wanted); the rows
  *                       that there is room for are written.
- *   Calls on the same pool or table must not overlap.
+ *   Calls on the same pool or table must not overlap.  A returned page is free whoever else names it: sequences that share
+ *   pages (a common prefix) must not give them up while another still reads them.
  *   Where the pool has too few free pages, or would get more than num_pages, nothing is changed: boundaries are all 0,
  *   slots -1, and DAP_DEVERR_POOL is set (new rows past 2^31 - 1 likewise, with DAP_DEVERR_SEQLEN).
  *   Supported: B <= 8192, B * max_pages <= 2^30, int32 slots with num_pages * page_size <= 2^31 - 1.

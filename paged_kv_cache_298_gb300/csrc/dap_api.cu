@@ -849,6 +849,9 @@ dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(positions) || !aligned4(path) ||
         !aligned4(accepted))
         return DAP_ERR_ALIGN;
+    // (K and V rows move independently of each other: in one buffer each would read what the other has written)
+    const uintptr_t k0 = reinterpret_cast<uintptr_t>(k_cache), v0 = reinterpret_cast<uintptr_t>(v_cache);
+    if ((double)(k0 > v0 ? k0 - v0 : v0 - k0) < (double)num_pages * page_size * Hkv * D * 2) return DAP_ERR_SHAPE;
     CommitArgs a = {};
     a.k_cache = k_cache;
     a.v_cache = v_cache;

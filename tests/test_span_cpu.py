@@ -147,3 +147,11 @@ def test_the_binding_refuses_before_the_library_sees_a_pointer():
         binding.kv_commit_paged(cache, cache, table, lens, table, lens)
     with pytest.raises(binding.DapError):
         binding.kv_resize_paged(lens, lens, table, lens, lens[:1], page_size=16)
+
+
+def test_a_commit_refuses_caches_that_overlap():
+    row = 2 * 64 * 2
+    for apart, status in ((0, SHAPE), (row, SHAPE), (4 * 16 * row - 16, SHAPE)):
+        for k, v in ((0, apart), (apart, 0)):
+            assert binding.load().kv_commit_paged(ctypes.c_void_p((1 << 20) + k), ctypes.c_void_p((1 << 20) + v), 4, 16, FAKE, 4,
+                                                  FAKE, FAKE, FAKE, 5, 2, 2, 64, None) == status
