@@ -356,7 +356,7 @@ dap_status launch_resize(const ResizeArgs &a, cudaStream_t stream) {
                    : DAP_ERR_CUDA;
     }
     const int most = std::max(1, dap_device_sm_count()) * (smem <= 48 * 1024 ? 4 : 1);
-    const int ctas = std::min(most, (a.rows + 4 * kResizeThreads - 1) / (4 * kResizeThreads));
+    const int ctas = (int)std::min<long long>(most, (a.rows + 4LL * kResizeThreads - 1) / (4 * kResizeThreads));
     p.part = kNoCount;
     if (launch_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, stream, p) != cudaSuccess)
         return DAP_ERR_CUDA;

@@ -106,6 +106,32 @@ def test_long_slot_maps(rows, wide):
     assert binding.get_device_errors() == 0
 
 
+def test_the_longest_slot_map():
+    rows = (1 << 31) - 1                        # (8.6 GB of int32 slots; only the first sequences' rows are there)
+    p = Pool([5, 30], 16, 8, 12)
+    new = [100, 20]
+    out = torch.empty(rows, dtype=torch.int32, device="cuda")
+    got, slots = binding.kv_resize_paged(ints(p.lens), ints(new), *p.gpu, page_size=16, total_rows=rows, slots=out)
+    indptr, want = p.python(new)
+    assert got.tolist() == indptr and slots[:len(want)].tolist() == want
+    assert all(bool((x == -1).all()) for x in slots[len(want):].split(1 << 29))
+    p.same()
+
+
+@pytest.mark.parametrize("B", [65, 300, 8192])
+def test_many_sequences_of_a_few_rows(B):
+    r = random.Random(B)
+    p = Pool([r.randint(0, 40) for _ in range(B)], 12, 5, B * 4, B)
+    for rows in (0, B * 3, 17000 + B * 3):      # (in one cluster, and on the whole device)
+        new = [min(60, max(0, n + r.choice([-13, -1, 0, 1, 3, 3]))) for n in p.lens]
+        old = ints(p.lens)
+        got, slots = binding.kv_resize_paged(old, ints(new), *p.gpu, page_size=12, total_rows=rows)
+        indptr, want = p.python(new)
+        assert got.tolist() == indptr and slots.tolist() == (want + [-1] * rows)[:rows]
+        p.same()
+    assert binding.get_device_errors() == 0
+
+
 def test_backwards_restores_everything():
     r = random.Random(3)
     p = Pool([r.randint(0, 300) for _ in range(100)], 16, 20, 400, seed=3)
