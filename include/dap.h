@@ -550,7 +550,8 @@ dap_status kv_commit_paged(void *k_cache, void *v_cache, int num_pages, int page
  *                       of sequence b, at position t = old_lens[b] + r - indptr[b], has slot
  *                       block_table[b][t / page_size] * page_size + t % page_size; rows behind the last have -1, and so has
  *                       a row whose page is outside the pool (DAP_DEVERR_PAGE).  (int64: what kv_append_fp8 takes.  int32:
- *                       a block table of one-slot pages, through which kv_append_paged writes the rows of a whole run.)
+ *                       a block table of one-slot pages, through which kv_append_paged writes the rows of a whole run; it
+ *                       skips a row of slot -1 as one whose page is outside the pool, DAP_DEVERR_PAGE.)
  *                       total_rows below indptr[B] sets DAP_DEVERR_SLOT, unless it is 0 (no slot map is wanted); the rows
  *                       that there is room for are written.
  *   Calls on the same pool or table must not overlap.  A returned page is free whoever else names it: sequences that share

@@ -329,3 +329,48 @@ def test_two_streams_at_once():
     for x, y in got:
         assert torch.equal(x, want_a) and torch.equal(y, want_b)
     assert binding.get_device_errors() == 0
+
+
+@pytest.mark.parametrize("ps", [12, 16])
+def test_caches_of_more_than_32_bits(ps):
+    """Pages at both ends of a cache of more than 2^32 numbers give the bits of a small one, and its rows move alike."""
+    pages = (1 << 32) // (ps * 2 * 128) + 200
+    big = [torch.empty((pages, ps, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for n in (1, 3, 40):
+        b = Batch([300, 71], [n, n], 8, 2, 128, ps, seed=n, kind="mixed")
+        to = torch.arange(b.pool, device="cuda")
+        to[1:] = pages - to[1:]                       # (one page at the cache's beginning)
+        for x, y in zip(big, (b.k, b.v)):
+            x[to] = y
+        table = torch.where(b.table >= 0, to[b.table.long().clamp(min=0)].int(), b.table)
+        for S in (1, 3):
+            want = [tree(b, num_splits=S), window(b, 100, 5, num_splits=S)]
+            small = b.k, b.v, b.table
+            b.k, b.v, b.table = *big, table
+            assert torch.equal(tree(b, num_splits=S), want[0]) and torch.equal(window(b, 100, 5, num_splits=S), want[1])
+            b.k, b.v, b.table = small
+        path = torch.arange(n // 2, n, dtype=torch.int32, device="cuda").repeat(2, 1)
+        count = torch.full((2,), n - n // 2, dtype=torch.int32, device="cuda")
+        base = b.seq_lens - n
+        binding.kv_commit_paged(b.k, b.v, b.table, base, path, count)
+        binding.kv_commit_paged(*big, table, base, path, count)
+        for x, y in zip(big, (b.k, b.v)):
+            assert torch.equal(x[to].view(torch.int16), y.view(torch.int16))
+    assert binding.get_device_errors() == 0
+
+
+@pytest.mark.parametrize("D,n", [(128, 128), (64, 2)])
+def test_partial_sums_of_more_than_32_bits(D, n):
+    """512 x 128 or 65536 x 2 new tokens of 32 heads in 16 or more splits: the partial sums pass 2^32 numbers."""
+    seqs = 512 if n == 128 else 65536
+    b = Batch([1000 if n == 128 else 1023], [n], 32, 4, D, 16, seed=1)
+    q = torch.randn((seqs * n, 32, D), device="cuda").to(torch.bfloat16)
+    plan = binding.SpanPlan([n] * seqs, 32, 4, D, "cuda")
+    S = plan.splits(b.max_len, 1100, 0, num_splits=64)
+    assert q.numel() * S > 1 << 32
+    out = binding.decode_attn_paged_window(q, b.k, b.v, b.table.expand(seqs, -1).contiguous(), b.seq_lens.expand(seqs).contiguous(),
+                                           plan, window=1100, max_kv_len=b.max_len, num_splits=S)
+    for at in (0, seqs // 2, seqs - 1):
+        b.q = q[at * n:at * n + n]
+        b.check(out[at * n:at * n + n], 1100, 0, what=at)
+    assert binding.get_device_errors() == 0
