@@ -25,6 +25,7 @@ struct ResizeParams {
     void *slots;
     int wide, rows;  // 8-byte slots; rows of the slot map
     int part;        // kAll, kNoCount or kCountOnly
+    bool vectors;    // the slot map begins at a multiple of 16 bytes
 };
 enum { kAll, kNoCount, kCountOnly };
 
@@ -71,7 +72,9 @@ __device__ __forceinline__ long long slot_of(const ResizeParams &p, int page, in
 
 // Every CTA computes the prefix sums of all sequences and takes its share of the pages and rows.  All of it in one cluster
 // (kAll): the CTAs meet once, before the count of free pages that they all read is replaced.  Many rows: on the whole device
-// (kNoCount), and then one CTA for the count (kCountOnly).
+// (kNoCount), and then one CTA for the count (kCountOnly).  LARGE: more than one CTA (one alone gets by with less code, which
+// has to come from memory too: 6.0 us for 6.6, 16 sequences of 8 rows taken and returned).
+template <bool LARGE>
 __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeParams p) {
     extern __shared__ int smem[];
     // per sequence: exclusive sums of pages returned and taken and of new rows [B + 1]; where its first returned entry is in
@@ -175,47 +178,111 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeP
         return i < count ? p.free_pages[i] : returned(i - count);
     };
     constexpr int U = 4;  // entries or rows that a thread has in flight
-    if (ok) {
-        for (int r0 = at; r0 < R; r0 += U * all) {
-            int page[U];
+    // The n entries of a list whose sums per sequence are `sums`: next to each other for the lanes of a warp, or, with more of
+    // them than one pass takes, U2 in a row for a thread, which then searches for the first alone (75,000 pages taken by the
+    // device and returned by one cluster, with 1.2 million rows: 17.4 us for 20.2).
+    constexpr int U2 = 8;
+    auto entries = [&](const int *sums, int n, auto &&load, auto &&store) {
+        if (!LARGE || n <= U * all) {
+            for (int e0 = at; e0 < n; e0 += U * all) {
+                int x[U], b[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r0 + u * all < R) page[u] = returned(r0 + u * all);
+                for (int u = 0; u < U; ++u)
+                    if (e0 + u * all < n) x[u] = load(e0 + u * all, b[u] = last_at_most(sums, p.B, e0 + u * all));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r0 + u * all < R) p.free_pages[count + r0 + u * all] = page[u];
+                for (int u = 0; u < U; ++u)
+                    if (e0 + u * all < n) store(e0 + u * all, b[u], x[u]);
+            }
+            return;
         }
-        for (int e0 = at; e0 < A; e0 += U * all) {
-            int page[U], to[U];
+        for (int e0 = U2 * at; e0 < n; e0 += U2 * all) {
+            int x[U2], b[U2], i = last_at_most(sums, p.B, e0), end = sums[i + 1];
+#pragma unroll
+            for (int u = 0; u < U2; ++u) {
+                if (e0 + u < n && e0 + u >= end) end = sums[(i = last_at_most(sums, p.B, e0 + u)) + 1];
+                b[u] = i;
+            }
+#pragma unroll
+            for (int u = 0; u < U2; ++u)
+                if (e0 + u < n) x[u] = load(e0 + u, b[u]);
+#pragma unroll
+            for (int u = 0; u < U2; ++u)
+                if (e0 + u < n) store(e0 + u, b[u], x[u]);
+        }
+    };
+    if (ok) {
+        entries(s_rel, R, [&](int r, int b) { return p.block_table[s_src[b] + r]; },
+                [&](int r, int, int page) { p.free_pages[count + r] = page; });
+        entries(s_take, A, [&](int e, int) { return taken(e); }, [&](int e, int b, int page) { p.block_table[s_dst[b] + e] = page; });
+    }
+    auto page_of = [&](int b, int i) -> int {  // of entry i of sequence b
+        const int e = b * p.max_pages + i - s_dst[b];  // number among the taken; an entry that was there: before them
+        return e < s_take[b] ? p.block_table[s_dst[b] + e] : taken(e);
+    };
+    if (!LARGE || p.part == kAll) {  // a thread's rows far apart: one each, mostly
+        for (long long r0 = at; r0 < p.rows; r0 += U * all) {
+            long long slot[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int e = e0 + u * all;
-                if (e < A) {
-                    to[u] = s_dst[last_at_most(s_take, p.B, e)] + e;
-                    page[u] = taken(e);
+                const long long r = r0 + u * all;
+                slot[u] = -1;
+                if (r < rows) {
+                    const int b = last_at_most(s_more, p.B, (int)r);
+                    const int pos = s_from[b] + (int)r - s_more[b], i = pos / p.page_size;
+                    slot[u] = slot_of(p, page_of(b, i), pos - i * p.page_size);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (e0 + u * all < A) p.block_table[to[u]] = page[u];
+                if (r0 + u * all < p.rows) store_slot(p, r0 + u * all, slot[u]);
         }
+        return;
     }
-    for (long long r0 = at; r0 < p.rows; r0 += U * all) {
+    // Many rows: U next to each other, which are nearly always of one sequence and one page (1.2 million rows: 20.2 us for 25.8
+    // with a search for each; a CTA for 2048 of them instead of 4096: 19.9 for 17.4, of all that happens there and back).
+    for (long long r0 = (long long)U * at; r0 < p.rows; r0 += (long long)U * all) {
         long long slot[U];
+        int end = 0, left = 0;  // the sequence's last row + 1; rows left in the page
+        int b = 0, i = 0;
+        long long next = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long r = r0 + u * all;
+            const long long r = r0 + u;
             slot[u] = -1;
             if (r < rows) {
-                const int b = last_at_most(s_more, p.B, (int)r);
-                const int pos = s_from[b] + (int)r - s_more[b], i = pos / p.page_size;
-                const int e = b * p.max_pages + i - s_dst[b];  // number among the taken; an entry that was there: before them
-                slot[u] = slot_of(p, e < s_take[b] ? p.block_table[s_dst[b] + e] : taken(e), pos - i * p.page_size);
+                if (u == 0 || r >= end || left == 0) {
+                    int row = 0;
+                    if (u == 0 || r >= end) {
+                        b = last_at_most(s_more, p.B, (int)r);
+                        end = s_more[b + 1];
+                        const int pos = s_from[b] + (int)r - s_more[b];
+                        i = pos / p.page_size;
+                        row = pos - i * p.page_size;
+                    } else {
+                        ++i;
+                    }
+                    left = p.page_size - row;
+                    next = slot_of(p, page_of(b, i), row);
+                }
+                slot[u] = next;
+                if (next >= 0) ++next;
+                --left;
             }
         }
+        if (p.vectors && r0 + U <= p.rows) {
+            if (p.wide) {
+                longlong2 *to = reinterpret_cast<longlong2 *>(static_cast<int64_t *>(p.slots) + r0);
+                to[0] = make_longlong2(slot[0], slot[1]);
+                to[1] = make_longlong2(slot[2], slot[3]);
+            } else {
+                *reinterpret_cast<int4 *>(static_cast<int32_t *>(p.slots) + r0) =
+                    make_int4((int)slot[0], (int)slot[1], (int)slot[2], (int)slot[3]);
+            }
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r0 + u * all < p.rows) store_slot(p, r0 + u * all, slot[u]);
+            for (int u = 0; u < U; ++u)
+                if (r0 + u < p.rows) store_slot(p, r0 + u, slot[u]);
+        }
     }
 }
 
@@ -340,29 +407,32 @@ dap_status launch_resize(const ResizeArgs &a, cudaStream_t stream) {
     p.slots = a.slots;
     p.wide = a.slot_bytes == 8;
     p.rows = a.rows;
+    p.vectors = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
     const int smem = 6 * (a.B + 1) * 4;
-    static PerDeviceOcc occ = {};
-    if (prepare_kernel(resize_kernel, kResizeThreads, 6 * (kResizeMost + 1) * 4, &occ) <= 0) return DAP_ERR_CUDA;
+    constexpr int kMostSmem = 6 * (kResizeMost + 1) * 4;
+    const bool large = a.B > 64 || a.rows > 2048;
+    static PerDeviceOcc occ[2] = {};
+    if (prepare_kernel(large ? resize_kernel<true> : resize_kernel<false>, kResizeThreads, kMostSmem, &occ[large]) <= 0)
+        return DAP_ERR_CUDA;
     // One cluster while its threads have up to four rows each, else the whole device and a launch for the count (1.2 million
-    // rows on 256 sequences taken and returned: 26 us, with the pages by a cluster 48); one CTA where that is enough (16
-    // sequences of 8 rows: 3.3 us).
+    // rows on 256 sequences taken and returned: 17.4 us, with the pages by a cluster 48); one CTA where that is enough (16
+    // sequences of 8 rows: 3.0 us).
     constexpr int kClusterRows = 4 * 8 * kResizeThreads;
     if (a.rows <= kClusterRows) {
-        const int ctas = a.B > 64 || a.rows > 2048 ? 8 : 1;
         p.part = kAll;
-        return launch_cluster_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, ctas, stream,
-                                             p) == cudaSuccess
+        return launch_cluster_dependent_smem(large ? resize_kernel<true> : resize_kernel<false>, dim3(large ? 8u : 1u),
+                                             dim3(kResizeThreads), smem, large ? 8 : 1, stream, p) == cudaSuccess
                    ? DAP_OK
                    : DAP_ERR_CUDA;
     }
     const int most = std::max(1, dap_device_sm_count()) * (smem <= 48 * 1024 ? 4 : 1);
-    const int ctas = (int)std::min<long long>(most, (a.rows + 4LL * kResizeThreads - 1) / (4 * kResizeThreads));
+    const int ctas = (int)std::min<long long>(most, (a.rows + 8LL * kResizeThreads - 1) / (8 * kResizeThreads));
     p.part = kNoCount;
-    if (launch_dependent_smem(resize_kernel, dim3((unsigned)ctas), dim3(kResizeThreads), smem, stream, p) != cudaSuccess)
+    if (launch_dependent_smem(resize_kernel<true>, dim3((unsigned)ctas), dim3(kResizeThreads), smem, stream, p) != cudaSuccess)
         return DAP_ERR_CUDA;
     p.part = kCountOnly;
-    return launch_dependent_smem(resize_kernel, dim3(1), dim3(kResizeThreads), smem, stream, p) == cudaSuccess ? DAP_OK
-                                                                                                              : DAP_ERR_CUDA;
+    return launch_dependent_smem(resize_kernel<true>, dim3(1), dim3(kResizeThreads), smem, stream, p) == cudaSuccess ? DAP_OK
+                                                                                                                    : DAP_ERR_CUDA;
 }
 
 dap_status launch_commit(const CommitArgs &a, cudaStream_t stream) {

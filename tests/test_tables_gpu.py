@@ -132,6 +132,30 @@ def test_many_sequences_of_a_few_rows(B):
     assert binding.get_device_errors() == 0
 
 
+@pytest.mark.parametrize("ps", [1, 2, 5, 64])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+def test_a_long_slot_map_that_begins_and_ends_anywhere(ps, dtype, off):
+    r = random.Random(ps + off)
+    lens = [r.choice([0, 0, 1, 2, 3, r.randint(0, 900)]) for _ in range(70)]
+    new = [max(0, n + r.choice([0, 0, -5, 1, 1, 2, 3, 700, 900])) for n in lens]
+    wide = max(new) // ps + 2
+    p = Pool(lens, ps, wide, 70 * wide, seed=2)
+    for extra in (0, 1, 2, 3):
+        rows = 17000 + extra
+        out = torch.full((rows + off + 1,), 5, dtype=dtype, device="cuda")
+        indptr, slots = p.resize(new, rows, slots=out[off:off + rows])
+        want_indptr, want = p.python(new)
+        assert indptr.tolist() == want_indptr and slots.tolist() == (want + [-1] * rows)[:rows]
+        assert out[:off].tolist() == [5] * off and out[-1].item() == 5
+        p.same()
+        new = [max(0, n + r.choice([0, 0, -300, 1, 1, 2, 3, 300])) for n in p.lens]
+        new = [min(n, p.max_pages * ps) for n in new]
+        if sum(max(0, n - m) for n, m in zip(new, p.lens)) > sum(m for m in p.lens) // 2:
+            new = [n // 2 for n in p.lens]
+    binding.get_device_errors(clear=True)             # (a map shorter than the rows is flagged)
+
+
 def test_backwards_restores_everything():
     r = random.Random(3)
     p = Pool([r.randint(0, 300) for _ in range(100)], 16, 20, 400, seed=3)
