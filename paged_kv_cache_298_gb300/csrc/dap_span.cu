@@ -6,9 +6,9 @@ namespace dap {
 
 // 8 / G tokens, or 16 / G, while they hold the longest run of new tokens; beyond that the rows of tensor-memory products
 // where the head dim has them: 128, of which two CTAs share an SM and cover each other's start and end (four chunks of 1021
-// tokens behind a window of 2048: 143 us, in tiles of 256 rows 158), or 256 where they and not 128 hold the run, which reads
+// tokens behind a window of 2048: 144 us, in tiles of 256 rows 156), or 256 where they and not 128 hold the run, which reads
 // its K/V once, from twice as many (sequence, kv head) units as SMs on (64 trees of 64 nodes, G = 4, behind 256 .. 4096 keys:
-// 154 us, in tiles of 128 rows 171; 3 trees behind 300 keys 12.2 and 10.6).
+// 151 us, in tiles of 128 rows 171; 3 of them behind 300 keys 16.3 and 14.3).
 int span_tokens_per_tile(int sms, int B, int Hkv, int G, int D, int max_q_len) {
     if (G < 1 || G > 8) return 0;
     if (max_q_len <= 8 / G) return 8 / G;

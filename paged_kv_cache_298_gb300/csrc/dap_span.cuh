@@ -84,7 +84,8 @@ __device__ __forceinline__ void load_parents(int *to, const int32_t *from, int n
 // The multi-token kernel's producer and consumer over spans, in two shapes (launch_span has the rule): KW = 2, 32-key tiles and
 // two consumer warps, four CTAs an SM (two at D = 256), so that one's start and end are covered by the others; KW = 4, 64-key
 // tiles and four consumer warps, two CTAs an SM (one at D = 256), where there are no more CTAs than that and a tile's chain
-// (scores, maximum, weights, values: 0.5 us whatever its keys) is what counts.
+// (scores, maximum, weights, values: 0.5 us for 32 keys, 0.7 for 64, D = 128) is what counts (4 sequences of one token behind a
+// window of 1024: 9.3 us for 14.0).
 
 template <int D_, int G_, int NT_, int KW_, bool GATHER_>
 struct SpanCfg {
