@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     if (PAGED && !C::GATHER && warp == NWC && lane * R < BT) {
         const long long t = (long long)s * p.chunk + lane * R;
         if (t < (long long)p.max_pages * p.page_size)
-            pg_first = __ldg(p.block_table + (long long)b * p.max_pages + t / p.page_size);
+            pg_first = p.block_table[(long long)b * p.max_pages + t / p.page_size];
     }
     if (L < 0 || L > p.max_kv_len) {
         if (threadIdx.x == 0 && s == 0 && kvg == 0) flag_error(DAP_DEVERR_SEQLEN);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             if (!PAGED) return b;
             const int t = tok0 + tile * BT + lane * R;
             if (lane * R >= BT || t >= tok1) return 0;
-            int pg = tile == 0 ? pg_first : __ldg(table + t / p.page_size);
+            int pg = tile == 0 ? pg_first : table[t / p.page_size];
             if (pg < 0 || pg >= p.num_pages) {
                 flag_error(DAP_DEVERR_PAGE);
                 pg = 0;
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
     // tiles of a sequence (an empty sequence still takes one tile, which writes its zeros)
     auto seq_len = [&](int b) -> int {
-        int L = __ldg(p.seq_lens + b);
+        int L = p.seq_lens[b];
         if (L < 0 || L > p.max_kv_len) {
             flag_error(DAP_DEVERR_SEQLEN);
             L = min(max(L, 0), p.max_kv_len);
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             auto lookup_box = [&](int bb, int tt, int LL) -> int {  // page of the box at token tt
                 if (!PAGED) return bb;
                 if (tt >= LL) return 0;
-                int pg = __ldg(p.block_table + (long long)bb * p.max_pages + tt / p.page_size);
+                int pg = p.block_table[(long long)bb * p.max_pages + tt / p.page_size];
                 if (pg < 0 || pg >= p.num_pages) {
                     flag_error(DAP_DEVERR_PAGE);
                     pg = 0;

@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const long long s = __shfl_sync(0xFFFFFFFFu, slot, i);
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if ((ball >> i) & 1u) raw[i] = __ldg(reinterpret_cast<const uint4 *>(piece + s * kHD));
+        raw[i] = load_16_if((ball >> i) & 1u, piece + s * kHD);
     }
     if (lane == 0) cnt[warp] = __popc(ball);
     tc_fence_before();

@@ -38,7 +38,7 @@ __device__ __forceinline__ int find_run(const int32_t *indptr, int B, int r, int
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const long long at = lo + (long long)(lane + 1) * step;
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && __ldg(indptr + at) <= r));
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && indptr[at] <= r));
         hi = (int)min((long long)hi, lo + (long long)(n + 1) * step);
         lo += n * step;
     }
@@ -62,10 +62,10 @@ __device__ __forceinline__ void find_places(const RunArgs &p, int r0, int n, Pla
     const int r = r0 + first + lane;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.indptr + mid) <= r) lo = mid;
+        if (p.indptr[mid] <= r) lo = mid;
         else hi = mid - 1;
     }
-    const long long b0 = __ldg(p.indptr + lo), b1 = __ldg(p.indptr + lo + 1), start = __ldg(p.positions + lo);
+    const long long b0 = p.indptr[lo], b1 = p.indptr[lo + 1], start = p.positions[lo];
     long long code = -1, factor = 0;
     if (r >= b0 && r < b1) {
         const long long pos = start + (r - b0);
@@ -74,7 +74,7 @@ __device__ __forceinline__ void find_places(const RunArgs &p, int r0, int n, Pla
             // (a position below 2^32, as a run starts at an int32 and has fewer than 2^31 rows)
             const int pg = (int)((uint32_t)pos / (uint32_t)p.page_size);
             const int slot = (int)((uint32_t)pos - (uint32_t)pg * (uint32_t)p.page_size);
-            const int page = __ldg(p.block_table + (long long)lo * p.max_pages + pg);
+            const int page = p.block_table[(long long)lo * p.max_pages + pg];
             if (page >= 0 && page < p.num_pages) {
                 code = ((long long)page * p.page_size + slot) * (p.Hkv * p.D);
                 factor = (long long)page * p.Hkv * p.page_size + slot;

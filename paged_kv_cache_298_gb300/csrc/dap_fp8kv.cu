@@ -428,7 +428,7 @@ struct GatherPages {
             pg[k] = 0;
             slot[k] = 0;
             if (r < nvalid) {
-                pg[k] = __ldg(table + (tok + r) / page_size);
+                pg[k] = table[(tok + r) / page_size];
                 slot[k] = (tok + r) % page_size;
             }
         }
@@ -454,7 +454,7 @@ struct GatherPages {
                 f[k][h] = 0u;
                 if (lane + 32 * k < nvalid) {
                     const long long i = ((long long)pg[k] * p.Hkv + kvh0 + h) * p.page_size + slot[k];
-                    f[k][h] = (uint32_t)__ldg(ks + i) | ((uint32_t)__ldg(vs + i) << 16);
+                    f[k][h] = (uint32_t)ks[i] | ((uint32_t)vs[i] << 16);
                 }
             }
     }
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     if (!C::GATHER && warp == NWC && lane * R < BT) {
         const long long t = (long long)s * p.chunk + lane * R;
         if (t < (long long)p.max_pages * p.page_size)
-            pg_first = __ldg(p.block_table + (long long)b * p.max_pages + t / p.page_size);
+            pg_first = p.block_table[(long long)b * p.max_pages + t / p.page_size];
     }
     if (L < 0 || L > p.max_kv_len) {
         if (threadIdx.x == 0 && s == 0 && kvg == 0) flag_error(DAP_DEVERR_SEQLEN);
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         auto lookup = [&](int tile) -> int {
             const int t = tok0 + tile * BT + lane * R;
             if (lane * R >= BT || t >= tok1) return 0;
-            int pg = tile == 0 ? pg_first : __ldg(table + t / p.page_size);
+            int pg = tile == 0 ? pg_first : table[t / p.page_size];
             if (pg < 0 || pg >= p.num_pages) {
                 flag_error(DAP_DEVERR_PAGE);
                 pg = 0;

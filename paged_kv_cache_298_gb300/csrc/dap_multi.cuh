@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     if (!C::GATHER && warp == NWC && lane * R < BT) {
         const long long t = (long long)s * p.chunk + lane * R;
         if (t < (long long)p.max_pages * p.page_size)
-            pg_first = __ldg(p.block_table + (long long)bb * p.max_pages + t / p.page_size);
+            pg_first = p.block_table[(long long)bb * p.max_pages + t / p.page_size];
     }
     MultiTile tl;
     if (!multi_tile(p, wb, wi, q0, q1, Lraw, C::QT, threadIdx.x == 0 && s == 0 && kvh == 0, &tl)) return;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         auto lookup = [&](int tile) -> int {
             const int t = tok0 + tile * BT + lane * R;
             if (lane * R >= BT || t >= tok1) return 0;
-            int pg = tile == 0 ? pg_first : __ldg(table + t / p.page_size);
+            int pg = tile == 0 ? pg_first : table[t / p.page_size];
             if (pg < 0 || pg >= p.num_pages) {
                 flag_error(DAP_DEVERR_PAGE);
                 pg = 0;

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             auto lookup = [&](int tile) -> int {
                 const int t = tok0 + tile * BT + lane * R;
                 if (lane * R >= BT || t >= tok1) return 0;
-                int pg = __ldg(table + t / p.page_size);
+                int pg = table[t / p.page_size];
                 if (pg < 0 || pg >= p.num_pages) {
                     flag_error(DAP_DEVERR_PAGE);
                     pg = 0;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 p.q + (long long)(tl.q0 + tl.i0 + ti) * p.q_sb + (long long)(kvh * G + hc) * p.q_sh;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
-                qv[c] = rvalid ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+                qv[c] = rvalid ? *reinterpret_cast<const uint4 *>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[16];

@@ -23,7 +23,7 @@
 // only).  They start after every prefix CTA has passed its wait, so the writers' grids have ended and their writes are in
 // L2, and no SM holds older copies, as a grid's start invalidates its L1.  Tested where lengths and K/V are written by the
 // call before, again and again without waiting (tests/test_shared_gpu.py: lengths that grow in place, append then
-// decode).
+// decode), and where a resize has just written the tables (tests/test_behind_a_resize_gpu.py).
 #pragma once
 
 #include <algorithm>
@@ -43,7 +43,7 @@ struct SharedParams {
 
 // The prefix length of group g, inside its bound.
 __device__ __forceinline__ int group_prefix(const SharedParams &p, int g) {
-    return min(max(__ldg(p.prefix_lens + g), 0), p.max_prefix_len);
+    return min(max(p.prefix_lens[g], 0), p.max_prefix_len);
 }
 
 // Prefix length and length of sequence b: a length of 0, below the prefix or of no group means
@@ -53,12 +53,12 @@ struct Span {
 };
 __device__ __forceinline__ Span seq_span(const SharedParams &p, int b, unsigned int *flags) {
     // (with one group its number need not be read)
-    const int g = p.num_groups == 1 ? 0 : __ldg(p.seq_group + b), Lraw = __ldg(p.sp.seq_lens + b);
+    const int g = p.num_groups == 1 ? 0 : p.seq_group[b], Lraw = p.sp.seq_lens[b];
     if (g < 0 || g >= p.num_groups) {
         *flags |= DAP_DEVERR_QMAP;
         return {0, 0};
     }
-    const int Praw = __ldg(p.prefix_lens + g);
+    const int Praw = p.prefix_lens[g];
     Span s = {min(max(Praw, 0), p.max_prefix_len), Lraw};
     if (Praw != s.P) *flags |= DAP_DEVERR_SEQLEN;
     const long long top =

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // (group, first sequence of the group, first sequence of the tile, sequences)
-    const int4 tl = __ldg(reinterpret_cast<const int4 *>(pp.tiles) + w);
+    const int4 tl = reinterpret_cast<const int4 *>(pp.tiles)[w];
     const bool valid = tl.x >= 0 && tl.x < pp.num_groups && tl.y >= 0 && tl.y < p.B && tl.z >= 0 && tl.w >= 1 &&
                        tl.w <= pp.seqs_per_tile && tl.w <= p.B - tl.z;
     const int q0 = tl.y, first = tl.z, nseq = valid ? tl.w : 0;

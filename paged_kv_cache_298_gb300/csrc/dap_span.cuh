@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     next.pg[k] = 0;
                     next.slot[k] = 0;
                     if (i < ntiles && v < v1) {  // (a hidden row: some row of a page that is seen)
-                        next.pg[k] = __ldg(table + (hidden(t, 1) ? tl.lo : t) / p.page_size);
+                        next.pg[k] = table[(hidden(t, 1) ? tl.lo : t) / p.page_size];
                         next.slot[k] = t % p.page_size;
                     }
                 }
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             auto lookup = [&](int i, bool *box) -> int {
                 const int v = v0 + i * BT + lane * R, t = tl.place(v0 + i * BT) + lane * R;
                 *box = i < ntiles && lane * R < BT && v < v1 && !hidden(t, R);
-                return *box ? __ldg(table + t / p.page_size) : 0;
+                return *box ? table[t / p.page_size] : 0;
             };
             bool has, has_next;
             int next = lookup(0, &has_next);

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     next.pg[k] = 0;
                     next.slot[k] = 0;
                     if (i < J && v + r < v1) {
-                        next.pg[k] = __ldg(table + (hidden(t, 1) ? tl.lo : t) / p.page_size);
+                        next.pg[k] = table[(hidden(t, 1) ? tl.lo : t) / p.page_size];
                         next.slot[k] = t % p.page_size;
                     }
                 }

@@ -119,7 +119,7 @@ __device__ __forceinline__ void lookup_rows(RowPages<C> &rp, const int32_t *tabl
         rp.slot[k] = 0;
         if (r < nvalid) {
             const int t = tok + r;
-            rp.pg[k] = __ldg(table + t / page_size);
+            rp.pg[k] = table[t / page_size];
             rp.slot[k] = t % page_size;
         }
     }
@@ -185,7 +185,7 @@ struct PageWindow {
         cur = get(first + lane);
         nxt = get(first + 32 + lane);
     }
-    __device__ __forceinline__ int get(int e) const { return e < end ? __ldg(row + e) : 0; }
+    __device__ __forceinline__ int get(int e) const { return e < end ? row[e] : 0; }
     // Entry e of each lane, first <= e < first + 32 (first: the same in every lane, never falling).
     __device__ __forceinline__ int at(int e, int first) {
         if (first >= base + 32) {

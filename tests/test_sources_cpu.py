@@ -44,3 +44,13 @@ def test_dependents_launch_after_tensor_memory_is_held(path):
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_the_device_says_how_many_sms_it_has(path):
     assert not re.search(r"\b1(48|52)(LL|L|u)?\b", code_of(path))
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_load_that_a_running_kernel_may_outdate(path):
+    """A kernel may be resident while the one before it still writes block tables, slots, boundaries, codes or factors (each lets
+    its dependents start early).  A load through the read-only path is only defined for what nobody writes while its kernel
+    lives, from before its wait on, and may be moved in front of that wait: no kernel has one, nor gives the compiler leave
+    to make one."""
+    code = code_of(path)
+    assert not re.search(r"__ldg\b|__ldlu\b|\.nc\b|__restrict__", code)
