@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeP
                 slot[u] = -1;
                 if (r < rows) {
                     const int b = last_at_most(s_more, p.B, (int)r);
-                    const int pos = s_from[b] + (int)r - s_more[b], i = pos / p.page_size;
+                    const int pos = s_from[b] + ((int)r - s_more[b]), i = pos / p.page_size;
                     slot[u] = slot_of(p, page_of(b, i), pos - i * p.page_size);
                 }
             }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1) resize_kernel(const ResizeP
                     if (u == 0 || r >= end) {
                         b = last_at_most(s_more, p.B, (int)r);
                         end = s_more[b + 1];
-                        const int pos = s_from[b] + (int)r - s_more[b];
+                        const int pos = s_from[b] + ((int)r - s_more[b]);
                         i = pos / p.page_size;
                         row = pos - i * p.page_size;
                     } else {
