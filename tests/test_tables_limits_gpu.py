@@ -1,9 +1,12 @@
-"""Page tables at the ends of their ranges: lengths and row numbers near 2^31, and more new rows than that."""
+"""Page tables and commits at the ends of their ranges: lengths and row numbers near 2^31, more new rows than that, and rows whose
+bits are no numbers."""
+import random
+
 import pytest
 import torch
 
 from paged_kv_cache_298_gb300 import binding
-from test_tables_gpu import Pool
+from test_tables_gpu import Pool, committed, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,28 @@ def test_more_new_rows_than_31_bits(B, rows):
             want[b] = page
         assert p.gpu[0].view(-1).tolist() == want and p.gpu[1].tolist() == p.free
         assert slots.tolist() == [top[0] * ps + r for r in range(rows)]
+
+
+@pytest.mark.parametrize("ps", [1, 16])
+def test_rows_move_whatever_their_bits(ps):
+    """NaN of every kind, infinities and negative zeros in rows that move, in K and in V."""
+    r = random.Random(ps)
+    base, paths = [5, 40], [list(range(1, 100)), [3, 4, 9, 30, 31, 32, 77]]
+    rows = list(range(2 * -(-160 // ps)))
+    r.shuffle(rows)
+    rows = [rows[::2], rows[1::2]]
+    k, v = (torch.randint(-(1 << 15), 1 << 15, (2 * len(rows[0]), ps, 2, 64), device="cuda").to(torch.int16) for _ in "kv")
+    for b, path in enumerate(paths):                          # (each pattern in a row that moves)
+        for i, bits in enumerate((0x7FC0, 0x7FBF, 0x7F81, 0x7FFF, 0x7F80, -0x80, -1, -0x7F, -0x8000)):
+            at = base[b] + path[i % len(path)]
+            k[rows[b][at // ps], at % ps, i % 2], v[rows[b][at // ps], at % ps, 1 - i % 2] = bits, bits
+    want = [x.clone() for x in (k, v)]
+    for x in want:
+        for b, path in enumerate(paths):
+            x.copy_(committed(x, rows[b], ps, base[b], path))
+    assert not any(torch.equal(x, y) for x, y in zip((k, v), want))
+    wide = max(map(len, paths))
+    binding.kv_commit_paged(k.view(torch.bfloat16), v.view(torch.bfloat16), ints(rows), ints(base),
+                            ints([x + [0] * (wide - len(x)) for x in paths]), ints([len(x) for x in paths]))
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    assert binding.get_device_errors() == 0
