@@ -62,6 +62,8 @@ struct SpanTcCfg {
     static_assert(SMEM <= 227 * 1024 / MINB, "shared memory");
     static_assert(MINB == 2 || SMEM > 114 * 1024, "one CTA an SM: a second would wait for tensor memory");
     static_assert(ROWS * ROW_B <= BAR_OFF, "the sums on their way out fit the place of q and the ring");
+    // (a stream's rows leave when its own products are done; all scores are, but not the other stream's last product with V)
+    static_assert(NSTREAM == 1 || 128 * ROW_B <= RING_OFF + TILE_BYTES, "the first stream's rows end before the first V tile");
 };
 
 // 32 columns of a row's sums in shared memory, as fp32 or, with BF16, times `f` and rounded (rows are ROW_B bytes apart).
