@@ -224,6 +224,7 @@ struct SpanConsumer : MultiConsumer<C> {
             }
             const uint32_t w0 = pack_bf16x2(ex2(s[0] - mu[0]), ex2(s[1] - mu[1]));
             const uint32_t w1 = pack_bf16x2(ex2(s[2] - mu[0]), ex2(s[3] - mu[1]));
+            // (rounded to V's type for the product; l sums what the product sees)
             const float2 f0 = bf16x2_to_float2(w0), f1 = bf16x2_to_float2(w1);
             l_run[n][0] = l_run[n][0] * alpha[0] + (f0.x + f1.x);
             l_run[n][1] = l_run[n][1] * alpha[1] + (f0.y + f1.y);

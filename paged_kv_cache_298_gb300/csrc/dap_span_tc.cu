@@ -23,7 +23,10 @@
 // one buffer a stream (1.28 us a 64-key tile of 256 rows for 0.91: the chain S, softmax, PV is then in line), weights taken
 // against the old reference while the maximum is found (0.96 - 1.0), one producer warp for K and V (0.96).
 // Softmax: base 2, scores rounded once; the running maximum is moved lazily (O and l are rescaled only when a tile's maximum
-// passes the reference by more than 2^8), so the weights stay <= 256.  They are rounded to bf16 for the product with V.
+// passes the reference by more than 2^8), so the weights stay <= 256.  They are rounded to bf16 for the product with V, whose
+// type is bf16; l sums them in fp32 before that rounding.  Summing the rounded ones brings the error against 64 bits from 0.0023 of
+// the output to 0.0022 (0.0017 of it is the output's own rounding) and costs 3 to 5%, since the softmax warps' chain is what
+// bounds a tile: 163 us for 157 on 64 trees of 64 nodes, 152.5 for 145 on four chunks of 1021 tokens.
 #include <algorithm>
 
 #include "dap_span.cuh"
